@@ -290,6 +290,133 @@ sr_status mingru_scan_noalloc(int64_t B, int64_t T, int64_t D,
                               const void* k, const void* p, int64_t ld_kp, sr_dtype kp_dtype,
                               const float* h0, float* h, float* h_last, void* stream);
 
+/*
+ * 8-bit codes: symmetric, one fp32 scale per row.
+ *
+ *     scale = max |x| / 127,   q = rint(x / scale) in [-127, 127]
+ *
+ * (two IEEE fp32 divisions, ties to even).  A row of zeros has scale 0 and
+ * codes 0; a row holding a NaN or an infinity has scale NaN and codes 0, so
+ * that every product with it is NaN.  Codes are stored as contiguous rows of
+ * quantized_row_bytes(K) = K rounded up to 128 bytes, zeros behind the K
+ * codes (the products read whole 128-byte lines; zeros add nothing).
+ *
+ * quantize_rows: the rows of x [M,K] (a token's activations each), rows of
+ *   ldx >= K elements, x_dtype SR_F32 or SR_BF16 -> q [M, quantized_row_bytes(K)],
+ *   scale [M].
+ * quantize_columns: the columns of W [K,N] (rows of ldw >= N elements; an
+ *   output channel each) -> q [N, quantized_row_bytes(K)], transposed, scale [N].
+ * q must be 16-byte aligned.  K = 0 gives scales 0 and no codes.
+ */
+int64_t quantized_row_bytes(int64_t K);
+sr_status quantize_rows(int64_t M, int64_t K, const void* x, int64_t ldx, sr_dtype x_dtype,
+                        int8_t* q, float* scale, void* stream);
+sr_status quantize_columns(int64_t K, int64_t N, const void* W, int64_t ldw, sr_dtype w_dtype,
+                           int8_t* q, float* scale, void* stream);
+
+/*
+ * Product of codes with a scale per token and per output channel:
+ *
+ *     y[m, n] = (sum_k a[m, k] b[n, k]) (a_scale[m] b_scale[n])
+ *
+ * The sum is exact (32-bit integers); it is rounded once to fp32, scaled, and
+ * rounded once more when y is bf16.  Results do not depend on the order of
+ * anything, so repeated calls give identical bits.
+ *
+ *   K       stored width of both operands: a multiple of 128, at most 131072
+ *           (larger: SR_ERR_UNSUPPORTED; 127^2 K must stay below 2^31).
+ *   a, b    [M,K] and [N,K] codes in [-127, 127], rows of lda / ldb >= K
+ *           bytes; a, b, lda and ldb multiples of 16.
+ *   y       [M,N] in y_dtype, rows of ldy >= N elements.
+ */
+sr_status matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda,
+                    const float* a_scale, const int8_t* b, int64_t ldb, const float* b_scale,
+                    void* y, int64_t ldy, sr_dtype y_dtype, void* stream);
+
+/*
+ * mingru_step and mingru_forward on 8-bit weights: the activations are
+ * quantised row by row (x before W_in, h before W_out), the products run on
+ * codes, and the recurrence stays in fp32.
+ *
+ *   x_t, x        as in mingru_step / mingru_forward, x_dtype SR_F32 or SR_BF16.
+ *   W_in          [2*D_h, quantized_row_bytes(D_in)] codes and W_in_scale [2*D_h]
+ *                 of the fp32 W_in's columns (quantize_columns).
+ *   W_out         [D_out, quantized_row_bytes(D_h)] codes and W_out_scale [D_out],
+ *                 or NULL (both; then D_out must equal D_h).
+ *   decay_rate    NULL (no time decay; delta_t and saturated must then be NULL),
+ *                 or as in mingru_step_decayed / mingru_forward_decayed with delta_t,
+ *                 log1p_delta and saturated.
+ *   y_t           [B,D_out] in x_dtype.  Without W_out the output is h_next and
+ *                 y_t must be NULL.
+ *   y             [B,T,D_out] in x_dtype; without W_out the states h, in fp32.
+ * mingru_forward_i8 hands [k|p] to the scan in x_dtype: with bf16 activations
+ * the gates are rounded to bf16, which halves the staged bytes and is below
+ * the rounding of the 8-bit codes.  Everything else as in mingru_step / mingru_forward;
+ * codes 16-byte aligned.
+ */
+size_t mingru_step_i8_workspace_size(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out);
+sr_status mingru_step_i8(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out,
+                         const void* x_t, sr_dtype x_dtype,
+                         const int8_t* W_in, const float* W_in_scale,
+                         const int8_t* W_out, const float* W_out_scale,
+                         const float* decay_rate, const float* delta_t, int log1p_delta,
+                         uint32_t* saturated,
+                         const float* h_prev, float* h_next, void* y_t,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+size_t mingru_forward_i8_workspace_size(int64_t B, int64_t T, int64_t D_in, int64_t D_h,
+                                        int64_t D_out, sr_dtype x_dtype, int has_w_out);
+sr_status mingru_forward_i8(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int64_t D_out,
+                            const void* x, sr_dtype x_dtype,
+                            const int8_t* W_in, const float* W_in_scale,
+                            const int8_t* W_out, const float* W_out_scale,
+                            const float* decay_rate, const float* delta_t, int log1p_delta,
+                            uint32_t* saturated,
+                            const float* h0, void* y, float* h_last,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One AdamW step over many tensors, few launches whatever their number.  For
+ * each element, t = step >= 1, c1 = 1 - beta1^t, c2 = 1 - beta2^t:
+ *
+ *     g = grad * grad_scale
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay) - (lr / c1) m / (sqrt(v) / sqrt(c2) + eps)
+ *
+ * in fp32; a bf16 p is rounded once.  In place on params and states.
+ *
+ *   tensors     n_tensors descriptions in HOST memory, read before the call
+ *               returns.  A tensor with grad NULL is left as it is, states
+ *               included.  param and grad are contiguous and aligned to their
+ *               element sizes.
+ *   m, v        device states of all tensors one after another, each tensor's span
+ *               rounded up to 256 elements (adamw_state_elements(n)); state_elements
+ *               is their length, at least the sum of the spans.  16-byte aligned.
+ *   state_bits  32: fp32 m and v; m_scale and v_scale must be NULL.
+ *               8: m and v hold one float8 e4m3 (OCP) code per element, of m and
+ *               of sqrt(v), each block of 256 elements with one fp32 scale in m_scale /
+ *               v_scale [state_elements / 256]: value = code * scale, scale = the
+ *               block's largest magnitude / 448, codes to nearest; a positive sqrt(v)
+ *               never gets the code 0 (it is raised to 2^-9).  A block whose state
+ *               holds a NaN or an infinity gets the scale NaN.  Zeroed buffers are
+ *               the states before the first step.
+ *   grad_scale  device fp32 scalar multiplied onto every gradient (clipping, loss
+ *               scaling), or NULL.
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  int64_t n;               /* elements */
+  sr_dtype param_dtype;    /* SR_F32 or SR_BF16 */
+  sr_dtype grad_dtype;
+} sr_adamw_tensor;
+
+int64_t adamw_state_elements(int64_t n);
+sr_status adamw_step(int64_t n_tensors, const sr_adamw_tensor* tensors, void* m, void* v,
+                     float* m_scale, float* v_scale, int state_bits, int64_t state_elements,
+                     int64_t step, double lr, double beta1, double beta2, double eps,
+                     double weight_decay, const float* grad_scale, void* stream);
+
 /* Text of the last non-OK status returned on this thread ("" if none). */
 const char* scanrnn_last_error(void);
 

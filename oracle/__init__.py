@@ -20,6 +20,8 @@ Everything here is plain, slow and meant to be checked by eye:
 * ``decay``    -- the minGRU recurrence with per-token time decay of the
                   carried state (gap-driven, clamped), sequentially.
 * ``grad``     -- the gradients of both scans (backward in time, chain rule).
+* ``quant``    -- symmetric 8-bit codes with a scale per row, and their product.
+* ``adamw``    -- one AdamW step, and the values of the 8-bit states' codes.
 * ``metrics``  -- the conditioned error measures used by the parity tests.
 
 Sources: the minGRU-pytorch profile (openvist.com), intro and "Requirements &
@@ -38,4 +40,4 @@ minGRU recurrence those sections refer to, taken as stated.
 Parity status of each function is listed in its module docstring.
 """
 
-from . import decay, grad, logspace, metrics, minmax, mingru, scalar  # noqa: F401
+from . import adamw, decay, grad, logspace, metrics, minmax, mingru, quant, scalar  # noqa: F401

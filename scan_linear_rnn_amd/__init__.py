@@ -38,6 +38,16 @@ __all__ = [
     "mingru_scan_backward",
     "mingru_scan_backward_decayed",
     "minmax_scan_backward",
+    "quantized_row_bytes",
+    "quantize_rows",
+    "quantize_columns",
+    "matmul_i8",
+    "mingru_step_i8",
+    "mingru_forward_i8",
+    "adamw_state_elements",
+    "adamw_step",
+    "AdamW",
+    "MinGRUInt8",
     "library_path",
     "ScanRNNError",
 ]
@@ -75,6 +85,16 @@ EXPORTED = (
     "minmax_scan_backward",
     "mingru_scan_noalloc_max_workspace",
     "mingru_scan_noalloc",
+    "quantized_row_bytes",
+    "quantize_rows",
+    "quantize_columns",
+    "matmul_i8",
+    "mingru_step_i8_workspace_size",
+    "mingru_step_i8",
+    "mingru_forward_i8_workspace_size",
+    "mingru_forward_i8",
+    "adamw_state_elements",
+    "adamw_step",
     "scanrnn_last_error",
     "scanrnn_set_lookback_spin_limit",
     "scanrnn_workspace_status",
@@ -137,6 +157,30 @@ def _load() -> ctypes.CDLL:
     lib.mingru_scan_noalloc_max_workspace.argtypes = []
     lib.mingru_scan_noalloc.restype = i32
     lib.mingru_scan_noalloc.argtypes = [i64, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp]
+    lib.quantized_row_bytes.restype = i64
+    lib.quantized_row_bytes.argtypes = [i64]
+    lib.quantize_rows.restype = i32
+    lib.quantize_rows.argtypes = [i64, i64, vp, i64, i32, vp, vp, vp]
+    lib.quantize_columns.restype = i32
+    lib.quantize_columns.argtypes = [i64, i64, vp, i64, i32, vp, vp, vp]
+    lib.matmul_i8.restype = i32
+    lib.matmul_i8.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, i32, vp]
+    lib.mingru_step_i8_workspace_size.restype = sz
+    lib.mingru_step_i8_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.mingru_step_i8.restype = i32
+    lib.mingru_step_i8.argtypes = [i64, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp,
+                                   vp, vp, vp, sz, vp]
+    lib.mingru_forward_i8_workspace_size.restype = sz
+    lib.mingru_forward_i8_workspace_size.argtypes = [i64, i64, i64, i64, i64, i32, i32]
+    lib.mingru_forward_i8.restype = i32
+    lib.mingru_forward_i8.argtypes = [i64, i64, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, i32,
+                                      vp, vp, vp, vp, vp, sz, vp]
+    lib.adamw_state_elements.restype = i64
+    lib.adamw_state_elements.argtypes = [i64]
+    lib.adamw_step.restype = i32
+    f64 = ctypes.c_double
+    lib.adamw_step.argtypes = [i64, vp, vp, vp, vp, vp, i32, i64, i64, f64, f64, f64, f64, f64, vp,
+                               vp]
     lib.scanrnn_last_error.restype = ctypes.c_char_p
     lib.scanrnn_last_error.argtypes = []
     lib.scanrnn_set_lookback_spin_limit.restype = i32
@@ -534,6 +578,299 @@ def minmax_scan_backward(r, s, x0, x_out, dx, dx_last=None, workspace=None):
     return dr, ds, dx0
 
 
+_DTYPES = {torch.float32: SR_F32, torch.bfloat16: SR_BF16}
+
+
+def _rows(t, name, ndim=None):
+    """A GPU tensor of fp32 or bf16 whose last dimension is contiguous and
+    whose rows are evenly strided, as (rows, row stride): a view when it can
+    be one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    if t.dim() < 1 or (ndim is not None and t.dim() != ndim):
+        raise ValueError(f"{name} must have {ndim or 'at least one'} dims (got shape {tuple(t.shape)})")
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < t.shape[1]:
+        t = t.contiguous().view(-1, t.shape[-1]) if t.numel() else t.new_empty((t.shape[:-1].numel(),
+                                                                                t.shape[-1]))
+    return t, (t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1))
+
+
+def _codes(t, name, width=None, rows=None):
+    """An int8 GPU tensor of codes [.., K], K a multiple of 128, as rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be torch.int8 (got {t.dtype})")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least 2 dims (got shape {tuple(t.shape)})")
+    if width is not None and (t.shape[-1] != width or t.dim() != 2 or t.shape[0] != rows):
+        raise ValueError(f"{name} must have shape {(rows, width)} (got {tuple(t.shape)})")
+    if t.shape[-1] % 128:
+        raise ValueError(f"{name} must have rows of a multiple of 128 codes, zeros behind the data "
+                         f"(got {t.shape[-1]})")
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < t.shape[1] or t.stride(0) % 16 \
+            or t.data_ptr() % 16:
+        flat = t.contiguous().view(t.shape[:-1].numel(), t.shape[-1])
+        t = flat if flat.data_ptr() % 16 == 0 else flat.clone()
+    return t, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def quantized_row_bytes(K: int) -> int:
+    """Width of a stored row of K codes: K rounded up to a multiple of 128."""
+    return _lib.quantized_row_bytes(K)
+
+
+def _code_out(q, scale, rows, width, device):
+    if q is None:
+        q = torch.empty((rows, width), dtype=torch.int8, device=device)
+    elif _dev(q, "q", dtype=torch.int8, shape=(rows, width)) is not q or q.device != device:
+        raise ValueError(f"q must be contiguous and on {device}")
+    if scale is None:
+        scale = torch.empty((rows,), dtype=torch.float32, device=device)
+    elif _dev(scale, "scale", shape=(rows,)) is not scale or scale.device != device:
+        raise ValueError(f"scale must be contiguous and on {device}")
+    return q, scale
+
+
+def quantize_rows(x, q=None, scale=None):
+    """Symmetric 8-bit codes of the rows (last dimension) of ``x`` [.., K],
+    fp32 or bf16, with a scale each: scale = max|x| / 127, q = rint(x / scale).
+
+    Returns (q [.., quantized_row_bytes(K)] int8, zeros behind the K codes,
+    scale [..] fp32).  A row of zeros has scale 0; a row with a NaN or an
+    infinity has scale NaN and codes 0.  ``q`` [rows, ..] and ``scale`` [rows]
+    may be given to avoid the allocations."""
+    src, ldx = _rows(x, "x")
+    M, K = src.shape
+    given = q is not None or scale is not None
+    q, scale = _code_out(q, scale, M, _lib.quantized_row_bytes(K), src.device)
+    _check("quantize_rows", _lib.quantize_rows(M, K, _ptr(src), ldx, _DTYPES[src.dtype], _ptr(q),
+                                               _ptr(scale), _stream(src.device)))
+    if given or x.dim() == 2:
+        return q, scale
+    return q.view(*x.shape[:-1], q.shape[1]), scale.view(x.shape[:-1])
+
+
+def quantize_columns(W, q=None, scale=None):
+    """8-bit codes of the columns of a weight ``W`` [K, N] (an output channel
+    each), laid out for matmul_i8: (q [N, quantized_row_bytes(K)] int8, scale
+    [N] fp32), as quantize_rows of its transpose."""
+    src, ldw = _rows(W, "W", ndim=2)
+    K, N = src.shape
+    q, scale = _code_out(q, scale, N, _lib.quantized_row_bytes(K), src.device)
+    _check("quantize_columns", _lib.quantize_columns(K, N, _ptr(src), max(ldw, N),
+                                                     _DTYPES[src.dtype], _ptr(q), _ptr(scale),
+                                                     _stream(src.device)))
+    return q, scale
+
+
+def matmul_i8(a, a_scale, b, b_scale, out_dtype=torch.float32, out=None):
+    """y[.., n] = (sum_k a[.., k] b[n, k]) (a_scale[..] b_scale[n]): the product
+    of codes ``a`` [.., K] (quantize_rows) and ``b`` [N, K] (quantize_columns),
+    summed exactly in 32-bit integers.  K is the stored width, a multiple of
+    128.  Returns y [.., N] in ``out_dtype`` (float32 or bfloat16)."""
+    rows, lda = _codes(a, "a")
+    M, K = rows.shape
+    b, ldb = _codes(b, "b", K, b.shape[0] if isinstance(b, torch.Tensor) and b.dim() else 0)
+    N = b.shape[0]
+    a_scale = _dev(a_scale, "a_scale", shape=a.shape[:-1])
+    b_scale = _dev(b_scale, "b_scale", shape=(N,))
+    for t, name in ((a_scale, "a_scale"), (b, "b"), (b_scale, "b_scale")):
+        if t.device != a.device:
+            raise ValueError(f"{name} must be on {a.device}")
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
+        out = torch.empty((*a.shape[:-1], N), dtype=out_dtype, device=a.device)
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype not in _DTYPES:
+            raise TypeError("out must be a float32 or bfloat16 tensor")
+        if out.device != a.device or tuple(out.shape) != (*a.shape[:-1], N) or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous, of shape {(*a.shape[:-1], N)}, on {a.device}")
+    _check("matmul_i8", _lib.matmul_i8(M, N, K, _ptr(rows), lda, _ptr(a_scale), _ptr(b), ldb,
+                                       _ptr(b_scale), _ptr(out), max(N, 1), _DTYPES[out.dtype],
+                                       _stream(a.device)))
+    return out
+
+
+def _i8_weights(D_in, W_in, W_in_scale, W_out, W_out_scale, device):
+    """Checks the codes and scales of a layer; returns them with D_h and D_out."""
+    if not isinstance(W_in, torch.Tensor) or W_in.dim() != 2 or W_in.shape[0] % 2:
+        raise ValueError("W_in must be codes [2*D_h, quantized_row_bytes(D_in)]")
+    D_h = W_in.shape[0] // 2
+    W_in, _ = _codes(W_in.contiguous(), "W_in", _lib.quantized_row_bytes(D_in), 2 * D_h)
+    W_in_scale = _dev(W_in_scale, "W_in_scale", shape=(2 * D_h,))
+    if (W_out is None) != (W_out_scale is None):
+        raise ValueError("W_out and W_out_scale go together")
+    D_out = D_h
+    if W_out is not None:
+        if not isinstance(W_out, torch.Tensor) or W_out.dim() != 2:
+            raise ValueError("W_out must be codes [D_out, quantized_row_bytes(D_h)]")
+        D_out = W_out.shape[0]
+        W_out, _ = _codes(W_out.contiguous(), "W_out", _lib.quantized_row_bytes(D_h), D_out)
+        W_out_scale = _dev(W_out_scale, "W_out_scale", shape=(D_out,))
+    for t, name in ((W_in, "W_in"), (W_in_scale, "W_in_scale"), (W_out, "W_out"),
+                    (W_out_scale, "W_out_scale")):
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+    return W_in, W_in_scale, W_out, W_out_scale, D_h, D_out
+
+
+def _optional_decay(decay_rate, delta_t, log1p_delta, saturated, D_h, gap_shape, device):
+    if decay_rate is None:
+        if delta_t is not None or saturated is not None:
+            raise ValueError("delta_t and saturated need decay_rate")
+        return None, None, 0, None
+    if delta_t is None:
+        raise ValueError("decay_rate and delta_t go together")
+    return _decay_args((decay_rate, delta_t, log1p_delta, saturated), D_h, gap_shape, device)
+
+
+def _activations(x, name, ndim):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16 (got {x.dtype})")
+    return _dev(x, name, dtype=x.dtype, ndim=ndim)
+
+
+def mingru_step_i8(x_t, W_in, W_in_scale, W_out=None, W_out_scale=None, h_prev=None, h_next=None,
+                   workspace=None, *, decay_rate=None, delta_t=None, log1p_delta=False,
+                   saturated=None):
+    """``mingru_step`` on 8-bit weights: x_t [B,D_in] fp32 or bf16 -> (y_t
+    [B,D_out] in x_t's type, h_t [B,D_h] fp32).
+
+    ``W_in`` and ``W_out`` are the codes of the layer's weights with their
+    scales (quantize_columns); x_t and the new state are quantised row by row
+    inside the call.  Without ``W_out`` the output is the new state (the same
+    tensor is returned twice).  ``decay_rate`` [D_h] with ``delta_t`` [B]: time
+    decay as in ``mingru_step_decayed``."""
+    x_t = _activations(x_t, "x_t", 2)
+    B, D_in = x_t.shape
+    device = x_t.device
+    W_in, W_in_scale, W_out, W_out_scale, D_h, D_out = _i8_weights(D_in, W_in, W_in_scale, W_out,
+                                                                   W_out_scale, device)
+    if h_prev is not None:
+        if not h_prev.is_contiguous():
+            raise ValueError("h_prev must be contiguous")
+        h_prev = _dev(h_prev, "h_prev", shape=(B, D_h))
+    if h_next is None:
+        h_next = torch.empty((B, D_h), dtype=torch.float32, device=device)
+    else:
+        if not h_next.is_contiguous():
+            raise ValueError("h_next must be contiguous")
+        _dev(h_next, "h_next", shape=(B, D_h))
+    y_t = None
+    if W_out is not None:
+        y_t = torch.empty((B, D_out), dtype=x_t.dtype, device=device)
+    rate, gap, log1p, sat = _optional_decay(decay_rate, delta_t, log1p_delta, saturated, D_h, (B,),
+                                            device)
+    nbytes = _lib.mingru_step_i8_workspace_size(B, D_in, D_h, D_out)
+    ws = _use_workspace(workspace, nbytes, device)
+    st = _lib.mingru_step_i8(B, D_in, D_h, D_out, _ptr(x_t), _DTYPES[x_t.dtype], _operand(W_in),
+                             _operand(W_in_scale), _operand(W_out), _operand(W_out_scale),
+                             _ptr(rate), _ptr(gap), log1p, _ptr(sat), _ptr(h_prev), _ptr(h_next),
+                             _ptr(y_t), _ptr(ws), ws.numel(), _stream(device))
+    _check("mingru_step_i8", st)
+    return (h_next if y_t is None else y_t), h_next
+
+
+def mingru_forward_i8(x, W_in, W_in_scale, W_out=None, W_out_scale=None, h0=None,
+                      return_last=False, workspace=None, *, decay_rate=None, delta_t=None,
+                      log1p_delta=False, saturated=None):
+    """``mingru_forward`` on 8-bit weights: x [B,T,D_in] fp32 or bf16 -> y
+    [B,T,D_out] in x's type (without ``W_out`` the states, in fp32), and h_T
+    [B,D_h] fp32 when ``return_last``.  Arguments as in ``mingru_step_i8``; the
+    gate logits and candidates reach the scan in x's type."""
+    x = _activations(x, "x", 3)
+    B, T, D_in = x.shape
+    device = x.device
+    W_in, W_in_scale, W_out, W_out_scale, D_h, D_out = _i8_weights(D_in, W_in, W_in_scale, W_out,
+                                                                   W_out_scale, device)
+    if h0 is not None:
+        h0 = _dev(h0, "h0", shape=(B, D_h))
+    y = torch.empty((B, T, D_out), dtype=torch.float32 if W_out is None else x.dtype, device=device)
+    h_last = torch.empty((B, D_h), dtype=torch.float32, device=device) if return_last else None
+    rate, gap, log1p, sat = _optional_decay(decay_rate, delta_t, log1p_delta, saturated, D_h, (B, T),
+                                            device)
+    nbytes = _lib.mingru_forward_i8_workspace_size(B, T, D_in, D_h, D_out, _DTYPES[x.dtype],
+                                                   int(W_out is not None))
+    ws = _use_workspace(workspace, nbytes, device)
+    st = _lib.mingru_forward_i8(B, T, D_in, D_h, D_out, _ptr(x), _DTYPES[x.dtype], _operand(W_in),
+                                _operand(W_in_scale), _operand(W_out), _operand(W_out_scale),
+                                _ptr(rate), _ptr(gap), log1p, _ptr(sat), _ptr(h0), _ptr(y),
+                                _ptr(h_last), _ptr(ws), ws.numel(), _stream(device))
+    _check("mingru_forward_i8", st)
+    return (y, h_last) if return_last else y
+
+
+def adamw_state_elements(n: int) -> int:
+    """Span of a tensor of n elements in the AdamW state buffers: n rounded up
+    to a multiple of 256."""
+    return _lib.adamw_state_elements(n)
+
+
+def adamw_step(params, grads, m, v, *, step, m_scale=None, v_scale=None, lr=1e-3,
+               betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, grad_scale=None):
+    """One AdamW step over many tensors, in place on ``params`` and the states.
+
+    ``params`` and ``grads``: lists of contiguous GPU tensors of the same
+    shapes, fp32 or bf16 each; a gradient may be None (that tensor is left as
+    it is).  ``step`` counts from 1.  ``m`` and ``v`` hold the states of all
+    tensors one after another, each tensor's span rounded up to 256 elements
+    (``adamw_state_elements``): fp32 without scales, or float8_e4m3fn codes (of
+    m and of sqrt(v)) with one fp32 scale for each 256 elements in ``m_scale``
+    and ``v_scale``.  Zeros are the states before the first step.
+    ``grad_scale``: an fp32 GPU scalar multiplied onto every gradient."""
+    if len(params) != len(grads):
+        raise ValueError(f"{len(params)} params but {len(grads)} grads")
+    if not params:
+        return
+    device = params[0].device
+    if device.type != "cuda":
+        raise ValueError(f"params must be GPU tensors (got {device})")
+    eight = m_scale is not None or v_scale is not None
+    table = []
+    for i, (p, g) in enumerate(zip(params, grads)):
+        pt = _DTYPES.get(p.dtype, -1)
+        n = p.numel()
+        if pt < 0 or p.device != device or not p.is_contiguous():
+            raise ValueError(f"params[{i}] must be a contiguous float32 or bfloat16 tensor on {device}")
+        if g is None:
+            table += (p.data_ptr(), 0, n, pt)
+            continue
+        gt = _DTYPES.get(g.dtype, -1)
+        if gt < 0 or g.device != device or not g.is_contiguous() or g.shape != p.shape:
+            raise ValueError(f"grads[{i}] must be a contiguous float32 or bfloat16 tensor of shape "
+                             f"{tuple(p.shape)} on {device}")
+        table += (p.data_ptr(), g.data_ptr(), n, pt | gt << 32)
+    kind = torch.float8_e4m3fn if eight else torch.float32
+    for t, name, want in ((m, "m", kind), (v, "v", kind), (m_scale, "m_scale", torch.float32),
+                          (v_scale, "v_scale", torch.float32)):
+        if t is None and not eight:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != want:
+            raise TypeError(f"{name} must be a {want} tensor")
+        if t.device != device or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-D tensor on {device}")
+    if v.numel() != m.numel() or (eight and not m_scale.numel() == v_scale.numel() == m.numel() // 256):
+        raise ValueError("m and v must have the same length, and m_scale and v_scale one scale for "
+                         "each 256 elements")
+    if grad_scale is not None and (_dev(grad_scale, "grad_scale").numel() != 1
+                                   or grad_scale.device != device):
+        raise ValueError(f"grad_scale must be one value on {device}")
+    st = _lib.adamw_step(len(params), (ctypes.c_int64 * len(table))(*table), _ptr(m), _ptr(v),
+                         _ptr(m_scale), _ptr(v_scale), 8 if eight else 32, m.numel(), step, lr,
+                         betas[0], betas[1], eps, weight_decay, _ptr(grad_scale), _stream(device))
+    _check("adamw_step", st)
+
+
 def set_lookback_spin_limit(polls: int) -> None:
     """Bound on the polls of an unwritten look-back word for scans launched
     afterwards (process-wide; at most LOOKBACK_SPIN_LIMIT, the default).  For
@@ -671,3 +1008,85 @@ class MinGRU:
                                                return_last=True, **dec)
         self._maybe_warn(dec)
         return (y, h_last) if return_next_prev_hidden else y
+
+    def quantized(self):
+        """The layer with its weights in 8 bits, for serving."""
+        return MinGRUInt8(self)
+
+
+class MinGRUInt8:
+    """A minGRU layer on 8-bit weights, made from a ``MinGRU``: the codes and
+    scales of its W_in and W_out, laid out once.  Called like the layer it was
+    made from, with fp32 or bf16 activations; hidden states stay fp32, outputs
+    have the activations' type.  ``requantize(layer)`` takes over the weights of a
+    layer that a training step changed, into the same buffers."""
+
+    def __init__(self, layer: MinGRU):
+        self.dim, self.dim_inner = layer.dim, layer.dim_inner
+        self.decay_rate, self.log1p_delta = layer.decay_rate, layer.log1p_delta
+        self.W_in, self.W_in_scale = quantize_columns(layer.W_in)
+        self.W_out = self.W_out_scale = None
+        if layer.W_out is not None:
+            self.W_out, self.W_out_scale = quantize_columns(layer.W_out)
+
+    def requantize(self, layer: MinGRU) -> None:
+        quantize_columns(layer.W_in, self.W_in, self.W_in_scale)
+        if self.W_out is not None:
+            quantize_columns(layer.W_out, self.W_out, self.W_out_scale)
+
+    def __call__(self, x, prev_hidden=None, return_next_prev_hidden=False, delta_t=None):
+        weights = (self.W_in, self.W_in_scale, self.W_out, self.W_out_scale)
+        dec = {}
+        if self.decay_rate is not None and delta_t is not None:
+            dec = dict(decay_rate=self.decay_rate, delta_t=delta_t.to(torch.float32),
+                       log1p_delta=self.log1p_delta)
+        h = None if prev_hidden is None else prev_hidden.reshape(x.shape[0], self.dim_inner)
+        if x.dim() == 2 or (x.shape[1] == 1 and prev_hidden is not None):
+            x_t = x.reshape(x.shape[0], x.shape[-1])
+            if dec:
+                dec["delta_t"] = dec["delta_t"].reshape(x_t.shape[0])
+            y, h = mingru_step_i8(x_t, *weights, h, **dec)
+            y = y.unsqueeze(1) if x.dim() == 3 else y
+        else:
+            y, h = mingru_forward_i8(x, *weights, h, return_last=True, **dec)
+        return (y, h) if return_next_prev_hidden else y
+
+
+class AdamW:
+    """AdamW over a list of parameters: ``adamw_step`` with the states it needs.
+
+    ``params``: contiguous GPU tensors, fp32 or bf16.  ``state_bits``: 32, or 8
+    for float8 states with a scale for each 256 elements (2.06 instead of 8
+    bytes per parameter).  ``step()`` uses the parameters' ``.grad``; ``step(grads)``
+    the given ones.  A parameter without a gradient is left as it is.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
+                 state_bits=32):
+        self.params = list(params)
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32 (got {state_bits})")
+        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
+        self.steps = 0
+        total = sum(adamw_state_elements(p.numel()) for p in self.params)
+        device = self.params[0].device if self.params else "cuda"
+        self.m_scale = self.v_scale = None
+        if state_bits == 8:
+            codes = torch.zeros((2, total), dtype=torch.uint8, device=device)
+            self.m, self.v = (c.view(torch.float8_e4m3fn) for c in codes)
+            self.m_scale, self.v_scale = torch.zeros((2, total // 256), device=device)
+        else:
+            self.m, self.v = torch.zeros((2, total), device=device)
+
+    @torch.no_grad()
+    def step(self, grads=None, grad_scale=None) -> None:
+        if grads is None:
+            grads = [p.grad for p in self.params]
+        adamw_step(self.params, grads, self.m, self.v, m_scale=self.m_scale, v_scale=self.v_scale,
+                   step=self.steps + 1, lr=self.lr, betas=self.betas, eps=self.eps,
+                   weight_decay=self.weight_decay, grad_scale=grad_scale)
+        self.steps += 1
+
+    def zero_grad(self) -> None:
+        for p in self.params:
+            p.grad = None

@@ -310,6 +310,77 @@ sr_status mingru_backward_impl(int64_t B, int64_t T, int64_t D, const void* k, c
   return launch_scan_backward(rq);
 }
 
+// ------------------------------------------------------------- 8-bit path
+
+size_t elem_size(sr_dtype t) { return t == SR_BF16 ? 2 : 4; }
+
+bool is_dtype(sr_dtype t) { return t == SR_F32 || t == SR_BF16; }
+
+// Bytes of the codes and of the scales of [M, K], each a multiple of kAlign.
+size_t code_bytes(int64_t M, int64_t K) {
+  return align_up(size_t(M) * size_t(sr::quantized_row_bytes(K)), kAlign);
+}
+size_t scale_bytes(int64_t M) { return align_up(size_t(M) * 4, kAlign); }
+
+// The codes of x and of h are never needed at once: they share one area.
+size_t step_i8_workspace(int64_t B, int64_t D_in, int64_t D_h) {
+  const size_t a = code_bytes(B, D_in), b = code_bytes(B, D_h);
+  return (a > b ? a : b) + scale_bytes(B);
+}
+
+struct I8Layout {
+  size_t q_off, s_off, kp_off, h_off, total;
+};
+
+// Workspace of mingru_forward_i8: the scan's look-back words, the codes and
+// scales of x and then of h, [k|p], and h while W_out follows.
+I8Layout forward_i8_layout(int64_t B, int64_t T, int64_t D_in, int64_t D_h, sr_dtype x_dtype,
+                           bool w_out) {
+  const size_t rows = size_t(B) * size_t(T);
+  const size_t a = code_bytes(B * T, D_in), b = w_out ? code_bytes(B * T, D_h) : 0;
+  I8Layout L{};
+  L.q_off = align_up(scan_workspace_bytes(B, T, D_h), kAlign);
+  L.s_off = L.q_off + (a > b ? a : b);
+  L.kp_off = L.s_off + scale_bytes(B * T);
+  L.h_off = L.kp_off + align_up(rows * size_t(2 * D_h) * elem_size(x_dtype), kAlign);
+  L.total = L.h_off + (w_out ? align_up(rows * size_t(D_h) * 4, kAlign) : 0);
+  return L;
+}
+
+// Sizes whose products (rows by any width, padded widths, weights) fit int64.
+bool i8_sizes_ok(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int64_t D_out) {
+  constexpr int64_t kMost = int64_t(1) << 40;
+  int64_t rows, n;
+  return B >= 0 && T >= 0 && D_in >= 0 && D_h >= 0 && D_out >= 0 && D_in <= kMost && D_h <= kMost &&
+         D_out <= kMost && mul_ok(B, T, &rows) && rows <= kMost &&
+         prod3(rows, 8, 2 * D_h + D_in + D_out + 2 * kI8Align, &n) &&
+         prod3(2 * D_h + D_out, 1, D_in + D_h + 2 * kI8Align, &n);
+}
+
+sr_status check_i8_weights(int64_t D_in, int64_t D_h, int64_t D_out, const int8_t* W_in,
+                           const float* W_in_scale, const int8_t* W_out, const float* W_out_scale) {
+  SR_REQUIRE(W_in != nullptr || D_in == 0 || D_h == 0, "W_in is NULL");
+  SR_REQUIRE(W_in_scale != nullptr || D_h == 0, "W_in_scale is NULL");
+  SR_REQUIRE((W_out != nullptr) == (W_out_scale != nullptr) || D_h == 0 || D_out == 0,
+             "W_out and W_out_scale go together");
+  SR_REQUIRE(aligned(W_in, 16) && aligned(W_out, 16), "codes must be 16-byte aligned");
+  SR_REQUIRE(aligned(W_in_scale, 4) && aligned(W_out_scale, 4), "scales must be 4-byte aligned");
+  if (sr::quantized_row_bytes(D_in) > kMaxI8Depth || sr::quantized_row_bytes(D_h) > kMaxI8Depth)
+    return fail(SR_ERR_UNSUPPORTED, "8-bit products are at most %lld deep (D_in=%lld, D_h=%lld)",
+                (long long)kMaxI8Depth, (long long)D_in, (long long)D_h);
+  return SR_OK;
+}
+
+// `dec.rate` null: no decay, and then nothing else of it may be given.
+sr_status check_optional_decay(const Decay& dec, int64_t n_rate, int64_t n_gap) {
+  if (dec.rate == nullptr) {
+    SR_REQUIRE(dec.delta_t == nullptr && dec.saturated == nullptr,
+               "delta_t or saturated without decay_rate");
+    return SR_OK;
+  }
+  return check_decay(dec, n_rate, n_gap);
+}
+
 }  // namespace
 
 void clear_last_error() { g_last_error[0] = '\0'; }
@@ -499,6 +570,275 @@ sr_status minmax_scan_backward(int64_t B, int64_t T, int64_t D, const float* r, 
   rq.workspace = workspace;
   rq.stream = as_stream(stream);
   return launch_scan_backward(rq);
+}
+
+int64_t quantized_row_bytes(int64_t K) {
+  if (K < 0 || K > INT64_MAX - kI8Align) return 0;
+  return sr::quantized_row_bytes(K);
+}
+
+sr_status quantize_rows(int64_t M, int64_t K, const void* x, int64_t ldx, sr_dtype x_dtype,
+                        int8_t* q, float* scale, void* stream) {
+  g_last_error[0] = '\0';
+  SR_REQUIRE(M >= 0 && K >= 0, "sizes must be non-negative (M=%lld K=%lld)", (long long)M,
+             (long long)K);
+  SR_REQUIRE(is_dtype(x_dtype), "x_dtype %d unsupported", int(x_dtype));
+  SR_REQUIRE(ldx >= K, "ldx (%lld) must be >= K (%lld)", (long long)ldx, (long long)K);
+  int64_t n;
+  SR_REQUIRE(K <= INT64_MAX / 2 && prod3(M, ldx, 4, &n) && prod3(M, K + kI8Align, 1, &n),
+             "tensor sizes overflow int64");
+  SR_REQUIRE(M == 0 || K == 0 || (x != nullptr && q != nullptr), "x or q is NULL");
+  SR_REQUIRE(M == 0 || scale != nullptr, "scale is NULL");
+  SR_REQUIRE(aligned(x, elem_size(x_dtype)), "x must be aligned to its element size");
+  SR_REQUIRE(aligned(q, 16) && aligned(scale, 4), "q must be 16-byte and scale 4-byte aligned");
+  return launch_quantize_rows(M, K, x, ldx, x_dtype, q, scale, as_stream(stream));
+}
+
+sr_status quantize_columns(int64_t K, int64_t N, const void* W, int64_t ldw, sr_dtype w_dtype,
+                           int8_t* q, float* scale, void* stream) {
+  g_last_error[0] = '\0';
+  SR_REQUIRE(K >= 0 && N >= 0, "sizes must be non-negative (K=%lld N=%lld)", (long long)K,
+             (long long)N);
+  SR_REQUIRE(is_dtype(w_dtype), "w_dtype %d unsupported", int(w_dtype));
+  SR_REQUIRE(ldw >= N, "ldw (%lld) must be >= N (%lld)", (long long)ldw, (long long)N);
+  int64_t n;
+  SR_REQUIRE(K <= INT64_MAX / 2 && prod3(K, ldw, 4, &n) && prod3(N, K + kI8Align, 1, &n),
+             "tensor sizes overflow int64");
+  SR_REQUIRE(N == 0 || K == 0 || (W != nullptr && q != nullptr), "W or q is NULL");
+  SR_REQUIRE(N == 0 || scale != nullptr, "scale is NULL");
+  SR_REQUIRE(aligned(W, elem_size(w_dtype)), "W must be aligned to its element size");
+  SR_REQUIRE(aligned(q, 16) && aligned(scale, 4), "q must be 16-byte and scale 4-byte aligned");
+  return launch_quantize_columns(K, N, W, ldw, w_dtype, q, scale, as_stream(stream));
+}
+
+sr_status matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda,
+                    const float* a_scale, const int8_t* b, int64_t ldb, const float* b_scale,
+                    void* y, int64_t ldy, sr_dtype y_dtype, void* stream) {
+  g_last_error[0] = '\0';
+  SR_REQUIRE(M >= 0 && N >= 0 && K >= 0, "sizes must be non-negative (M=%lld N=%lld K=%lld)",
+             (long long)M, (long long)N, (long long)K);
+  SR_REQUIRE(K % kI8Align == 0, "K (%lld) must be a multiple of %lld", (long long)K,
+             (long long)kI8Align);
+  SR_REQUIRE(is_dtype(y_dtype), "y_dtype %d unsupported", int(y_dtype));
+  SR_REQUIRE(lda >= K && ldb >= K && ldy >= N, "lda, ldb must be >= K and ldy >= N");
+  SR_REQUIRE(lda % 16 == 0 && ldb % 16 == 0, "lda and ldb must be multiples of 16");
+  int64_t n;
+  SR_REQUIRE(prod3(M, lda, 1, &n) && prod3(N, ldb, 1, &n) && prod3(M, ldy, 4, &n),
+             "tensor sizes overflow int64");
+  const bool work = M > 0 && N > 0;
+  SR_REQUIRE(!work || K == 0 || (a != nullptr && b != nullptr), "a or b is NULL");
+  SR_REQUIRE(!work || (a_scale != nullptr && b_scale != nullptr && y != nullptr),
+             "a_scale, b_scale or y is NULL");
+  SR_REQUIRE(aligned(a, 16) && aligned(b, 16), "codes must be 16-byte aligned");
+  SR_REQUIRE(aligned(a_scale, 4) && aligned(b_scale, 4) && aligned(y, elem_size(y_dtype)),
+             "scales and y must be aligned to their element size");
+  if (K > kMaxI8Depth)
+    return fail(SR_ERR_UNSUPPORTED, "8-bit products are at most %lld deep (K=%lld)",
+                (long long)kMaxI8Depth, (long long)K);
+  return launch_gemm_i8(M, N, K, a, lda, a_scale, b, ldb, b_scale, y, ldy, y_dtype,
+                        as_stream(stream));
+}
+
+size_t mingru_step_i8_workspace_size(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out) {
+  if (!i8_sizes_ok(B, 1, D_in, D_h, D_out)) return 0;
+  return step_i8_workspace(B, D_in, D_h);
+}
+
+sr_status mingru_step_i8(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out, const void* x_t,
+                         sr_dtype x_dtype, const int8_t* W_in, const float* W_in_scale,
+                         const int8_t* W_out, const float* W_out_scale, const float* decay_rate,
+                         const float* delta_t, int log1p_delta, uint32_t* saturated,
+                         const float* h_prev, float* h_next, void* y_t, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  SR_REQUIRE(i8_sizes_ok(B, 1, D_in, D_h, D_out),
+             "sizes must be non-negative and fit int64 (B=%lld D_in=%lld D_h=%lld D_out=%lld)",
+             (long long)B, (long long)D_in, (long long)D_h, (long long)D_out);
+  SR_REQUIRE(is_dtype(x_dtype), "x_dtype %d unsupported", int(x_dtype));
+  sr_status st = check_i8_weights(D_in, D_h, D_out, W_in, W_in_scale, W_out, W_out_scale);
+  if (st != SR_OK) return st;
+  const bool w_out = W_out_scale != nullptr;
+  if (!w_out) {
+    SR_REQUIRE(D_out == D_h, "without W_out the output width D_out (%lld) must equal D_h (%lld)",
+               (long long)D_out, (long long)D_h);
+    SR_REQUIRE(y_t == nullptr, "y_t must be NULL without W_out (the output is h_next)");
+  }
+  SR_REQUIRE(x_t != nullptr || B * D_in == 0, "x_t is NULL");
+  SR_REQUIRE(h_next != nullptr || B * D_h == 0, "h_next is NULL");
+  SR_REQUIRE(!w_out || y_t != nullptr || B * D_out == 0, "y_t is NULL while W_out is given");
+  SR_REQUIRE(aligned(x_t, elem_size(x_dtype)) && aligned(y_t, elem_size(x_dtype)) &&
+                 aligned(h_prev, 4) && aligned(h_next, 4),
+             "pointers must be aligned to their element size");
+  const Decay dec{decay_rate, delta_t, log1p_delta, saturated};
+  st = check_optional_decay(dec, B * D_h > 0 ? D_h : 0, B * D_h > 0 ? B : 0);
+  if (st != SR_OK) return st;
+  st = check_workspace(workspace, workspace_bytes, step_i8_workspace(B, D_in, D_h));
+  if (st != SR_OK) return st;
+  if (B == 0) return SR_OK;
+  hipStream_t s = as_stream(stream);
+  int8_t* q = static_cast<int8_t*>(workspace);
+  float* scale = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                          step_i8_workspace(B, D_in, D_h) - scale_bytes(B));
+  const StepDecay sd{dec.rate, dec.delta_t, dec.log1p_delta, dec.saturated};
+  const int64_t Ki = sr::quantized_row_bytes(D_in), Kh = sr::quantized_row_bytes(D_h);
+  // Checked first, then launched (as in forward_impl).
+  auto run = [&](bool check_only) -> sr_status {
+    sr_status st2;
+    if (D_h > 0) {
+      st2 = launch_quantize_rows(B, D_in, x_t, D_in, x_dtype, q, scale, s, check_only);
+      if (st2 != SR_OK) return st2;
+      st2 = launch_step_i8(B, Ki, D_h, q, scale, W_in, W_in_scale, h_prev, h_next, s,
+                           dec.rate != nullptr ? &sd : nullptr, check_only);
+      if (st2 != SR_OK) return st2;
+    }
+    if (!w_out || D_out == 0) return SR_OK;
+    st2 = launch_quantize_rows(B, D_h, h_next, D_h, SR_F32, q, scale, s, check_only);
+    if (st2 != SR_OK) return st2;
+    return launch_gemm_i8(B, D_out, Kh, q, Kh, scale, W_out, Kh, W_out_scale, y_t, D_out, x_dtype, s,
+                          check_only);
+  };
+  st = run(true);
+  return st != SR_OK ? st : run(false);
+}
+
+size_t mingru_forward_i8_workspace_size(int64_t B, int64_t T, int64_t D_in, int64_t D_h,
+                                        int64_t D_out, sr_dtype x_dtype, int has_w_out) {
+  if (!i8_sizes_ok(B, T, D_in, D_h, D_out) || !is_dtype(x_dtype)) return 0;
+  return forward_i8_layout(B, T, D_in, D_h, x_dtype, has_w_out != 0).total;
+}
+
+sr_status mingru_forward_i8(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int64_t D_out,
+                            const void* x, sr_dtype x_dtype, const int8_t* W_in,
+                            const float* W_in_scale, const int8_t* W_out, const float* W_out_scale,
+                            const float* decay_rate, const float* delta_t, int log1p_delta,
+                            uint32_t* saturated, const float* h0, void* y, float* h_last,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  SR_REQUIRE(i8_sizes_ok(B, T, D_in, D_h, D_out),
+             "sizes must be non-negative and fit int64 (B=%lld T=%lld D_in=%lld D_h=%lld D_out=%lld)",
+             (long long)B, (long long)T, (long long)D_in, (long long)D_h, (long long)D_out);
+  SR_REQUIRE(is_dtype(x_dtype), "x_dtype %d unsupported", int(x_dtype));
+  sr_status st = check_i8_weights(D_in, D_h, D_out, W_in, W_in_scale, W_out, W_out_scale);
+  if (st != SR_OK) return st;
+  const bool w_out = W_out_scale != nullptr;
+  if (!w_out)
+    SR_REQUIRE(D_out == D_h, "without W_out the output width D_out (%lld) must equal D_h (%lld)",
+               (long long)D_out, (long long)D_h);
+  const int64_t rows = B * T;
+  SR_REQUIRE(x != nullptr || rows * D_in == 0, "x is NULL");
+  SR_REQUIRE(y != nullptr || rows * D_out == 0, "y is NULL");
+  SR_REQUIRE(aligned(x, elem_size(x_dtype)) && aligned(y, w_out ? elem_size(x_dtype) : 4) &&
+                 aligned(h0, 4) && aligned(h_last, 4),
+             "pointers must be aligned to their element size");
+  const Decay dec{decay_rate, delta_t, log1p_delta, saturated};
+  st = check_optional_decay(dec, rows * D_h > 0 ? D_h : 0, rows * D_h > 0 ? rows : 0);
+  if (st != SR_OK) return st;
+  const I8Layout L = forward_i8_layout(B, T, D_in, D_h, x_dtype, w_out);
+  st = check_workspace(workspace, workspace_bytes, L.total);
+  if (st != SR_OK) return st;
+  if (B == 0) return SR_OK;
+  hipStream_t s = as_stream(stream);
+  char* ws = static_cast<char*>(workspace);
+  int8_t* q = reinterpret_cast<int8_t*>(ws + L.q_off);
+  float* scale = reinterpret_cast<float*>(ws + L.s_off);
+  char* kp = ws + L.kp_off;
+  float* h = w_out ? reinterpret_cast<float*>(ws + L.h_off) : static_cast<float*>(y);
+  const int64_t Ki = sr::quantized_row_bytes(D_in), Kh = sr::quantized_row_bytes(D_h);
+  // Checked first, then launched (as in forward_impl).
+  auto run = [&](bool check_only) -> sr_status {
+    sr_status st2;
+    if (rows > 0 && D_h > 0) {
+      st2 = launch_quantize_rows(rows, D_in, x, D_in, x_dtype, q, scale, s, check_only);
+      if (st2 != SR_OK) return st2;
+      st2 = launch_gemm_i8(rows, 2 * D_h, Ki, q, Ki, scale, W_in, Ki, W_in_scale, kp, 2 * D_h,
+                           x_dtype, s, check_only);
+      if (st2 != SR_OK) return st2;
+    }
+    ScanRequest rq{};
+    rq.op = ScanOp::kMinGRU;
+    rq.in_dtype = x_dtype;
+    rq.B = B;
+    rq.T = T;
+    rq.D = D_h;
+    rq.in0 = kp;
+    rq.in1 = kp + size_t(D_h) * elem_size(x_dtype);
+    rq.ld_in = 2 * D_h;
+    rq.init = h0;
+    rq.out = h;
+    rq.last = h_last;
+    rq.workspace = ws;
+    rq.stream = s;
+    rq.decay_rate = dec.rate;
+    rq.delta_t = dec.delta_t;
+    rq.log1p_delta = dec.log1p_delta;
+    rq.saturated = dec.saturated;
+    rq.check_only = check_only;
+    st2 = launch_scan(rq);
+    if (st2 != SR_OK || !w_out || rows == 0 || D_out == 0) return st2;
+    st2 = launch_quantize_rows(rows, D_h, h, D_h, SR_F32, q, scale, s, check_only);
+    if (st2 != SR_OK) return st2;
+    return launch_gemm_i8(rows, D_out, Kh, q, Kh, scale, W_out, Kh, W_out_scale, y, D_out, x_dtype,
+                          s, check_only);
+  };
+  st = run(true);
+  return st != SR_OK ? st : run(false);
+}
+
+int64_t adamw_state_elements(int64_t n) {
+  if (n < 0 || n > INT64_MAX - kStateBlock) return 0;
+  return adamw_span(n);
+}
+
+sr_status adamw_step(int64_t n_tensors, const sr_adamw_tensor* tensors, void* m, void* v,
+                     float* m_scale, float* v_scale, int state_bits, int64_t state_elements,
+                     int64_t step, double lr, double beta1, double beta2, double eps,
+                     double weight_decay, const float* grad_scale, void* stream) {
+  g_last_error[0] = '\0';
+  SR_REQUIRE(n_tensors >= 0, "n_tensors must be non-negative (got %lld)", (long long)n_tensors);
+  SR_REQUIRE(n_tensors == 0 || tensors != nullptr, "tensors is NULL");
+  SR_REQUIRE(state_bits == 8 || state_bits == 32, "state_bits must be 8 or 32 (got %d)", state_bits);
+  SR_REQUIRE(step >= 1, "step counts from 1 (got %lld)", (long long)step);
+  SR_REQUIRE(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1, "betas must be in [0, 1)");
+  SR_REQUIRE(lr >= 0 && eps >= 0 && weight_decay >= 0, "lr, eps and weight_decay must be non-negative");
+  int64_t total = 0;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const sr_adamw_tensor& t = tensors[i];
+    SR_REQUIRE(t.n >= 0 && t.n <= (int64_t(1) << 60), "tensor %lld has %lld elements", (long long)i,
+               (long long)t.n);
+    SR_REQUIRE(is_dtype(t.param_dtype) && is_dtype(t.grad_dtype), "tensor %lld: dtype unsupported",
+               (long long)i);
+    SR_REQUIRE(t.n == 0 || t.param != nullptr, "tensor %lld: param is NULL", (long long)i);
+    SR_REQUIRE(aligned(t.param, elem_size(t.param_dtype)) && aligned(t.grad, elem_size(t.grad_dtype)),
+               "tensor %lld: pointers must be aligned to their element size", (long long)i);
+    SR_REQUIRE(!__builtin_add_overflow(total, adamw_span(t.n), &total), "tensor sizes overflow int64");
+  }
+  SR_REQUIRE(state_elements >= total, "the states have %lld elements, %lld needed",
+             (long long)state_elements, (long long)total);
+  SR_REQUIRE(total == 0 || (m != nullptr && v != nullptr), "m or v is NULL");
+  SR_REQUIRE(aligned(m, 16) && aligned(v, 16), "m and v must be 16-byte aligned");
+  if (state_bits == 8)
+    SR_REQUIRE(total == 0 || (m_scale != nullptr && v_scale != nullptr),
+               "8-bit states need m_scale and v_scale");
+  else
+    SR_REQUIRE(m_scale == nullptr && v_scale == nullptr, "fp32 states have no scales");
+  SR_REQUIRE(aligned(m_scale, 4) && aligned(v_scale, 4) && aligned(grad_scale, 4),
+             "fp32 pointers must be 4-byte aligned");
+  AdamWRequest rq{};
+  rq.n_tensors = n_tensors;
+  rq.tensors = tensors;
+  rq.m = m;
+  rq.v = v;
+  rq.m_scale = m_scale;
+  rq.v_scale = v_scale;
+  rq.step = step;
+  rq.lr = lr;
+  rq.beta1 = beta1;
+  rq.beta2 = beta2;
+  rq.eps = eps;
+  rq.weight_decay = weight_decay;
+  rq.grad_scale = grad_scale;
+  rq.stream = as_stream(stream);
+  return launch_adamw(rq);
 }
 
 sr_status scanrnn_set_lookback_spin_limit(uint32_t polls) {

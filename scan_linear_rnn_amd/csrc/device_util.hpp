@@ -1,0 +1,32 @@
+// Small device helpers shared by the 8-bit and AdamW kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace sr {
+
+constexpr uint32_t kF32InfBits = 0x7F800000u;
+
+// fp32 to bf16, to nearest with ties to even; NaNs stay NaN.
+__device__ __forceinline__ uint32_t bf16_bits(float x) {
+  const uint32_t u = __float_as_uint(x);
+  if ((u & 0x7FFFFFFFu) > kF32InfBits) return 0x7FC0u;
+  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+// Bits of |x|: ordered like the values, infinities and then NaNs on top.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// The largest value of a wave, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_xor(v, d);
+    v = v > o ? v : o;
+  }
+  return v;
+}
+
+}  // namespace sr

@@ -155,6 +155,60 @@ sr_status launch_step_in(int64_t Bsz, int64_t D_in, int64_t D_h,
 int gemm_splits(int64_t M, int64_t N, int64_t K, bool step);
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool step);
 
+// ------------------------------------------------- 8-bit codes and products
+
+// Rows of codes are padded with zeros to a multiple of this many bytes.
+constexpr int64_t kI8Align = 128;
+inline int64_t quantized_row_bytes(int64_t K) { return (K + kI8Align - 1) / kI8Align * kI8Align; }
+// Deepest product whose sums fit 32 bits: 127^2 * K < 2^31.
+constexpr int64_t kMaxI8Depth = 131072;
+// Workgroups of 256 threads in one launch (a 1-D grid has at most 2^32 work-items).
+constexpr int64_t kMaxBlocks256 = int64_t(0xFFFFFFFF) / 256;
+
+// Codes q [M, quantized_row_bytes(K)] and scales [M] of x (rows of ldx elements).
+sr_status launch_quantize_rows(int64_t M, int64_t K, const void* x, int64_t ldx, sr_dtype dtype,
+                               int8_t* q, float* scale, hipStream_t stream, bool check_only = false);
+
+// Codes q [N, quantized_row_bytes(K)] and scales [N] of the columns of W [K, N].
+sr_status launch_quantize_columns(int64_t K, int64_t N, const void* W, int64_t ldw, sr_dtype dtype,
+                                  int8_t* q, float* scale, hipStream_t stream);
+
+// C[M,N] = (A B^T) a_scale b_scale over codes A [M,K], B [N,K] (K a multiple
+// of kI8Align, rows 16-byte aligned).
+sr_status launch_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,
+                         const float* a_scale, const int8_t* B, int64_t ldb, const float* b_scale,
+                         void* C, int64_t ldc, sr_dtype c_dtype, hipStream_t stream,
+                         bool check_only = false);
+
+// The step on codes: [k|p] = the product of x [Bsz,K] and W_in [2 D_h, K],
+// h_next as in launch_step_in.
+sr_status launch_step_i8(int64_t Bsz, int64_t K, int64_t D_h, const int8_t* x, const float* x_scale,
+                         const int8_t* W_in, const float* w_scale, const float* h_prev,
+                         float* h_next, hipStream_t stream, const StepDecay* decay,
+                         bool check_only = false);
+
+// ---------------------------------------------------------------- AdamW
+
+// Elements of a tensor that share a scale of the 8-bit states; also what a
+// tensor's span in the state buffers is rounded up to.
+constexpr int64_t kStateBlock = 256;
+inline int64_t adamw_span(int64_t n) { return (n + kStateBlock - 1) / kStateBlock * kStateBlock; }
+
+struct AdamWRequest {
+  int64_t n_tensors;
+  const sr_adamw_tensor* tensors;  // host memory
+  void* m;
+  void* v;
+  float* m_scale;  // null: fp32 states
+  float* v_scale;
+  int64_t step;
+  double lr, beta1, beta2, eps, weight_decay;
+  const float* grad_scale;
+  hipStream_t stream;
+};
+
+sr_status launch_adamw(const AdamWRequest& rq);
+
 // One MinMax step over n channels (x_next may alias x_prev).
 sr_status launch_minmax_step(const float* r, const float* s, const float* x_prev, float* x_next,
                              int64_t n, hipStream_t stream);
