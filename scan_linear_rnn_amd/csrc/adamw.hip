@@ -19,7 +19,10 @@
 //
 // A wave owns whole blocks (four elements per lane), so a block's largest
 // magnitude is one reduction within the wave and every element is read and
-// written once.
+// written once.  The step is bound by those bytes (28 per element in fp32, 14
+// with bf16 gradients and 8-bit states): four blocks per wave keep 16 loads
+// in flight, and the table of tensors travels in the kernel's arguments, so
+// that a call is one launch for every 64 tensors and nothing is copied.
 
 #include <cmath>
 
@@ -31,7 +34,8 @@ namespace {
 
 constexpr int kBlock = int(kStateBlock);
 constexpr int kWaves = 4;
-constexpr int kTensors = 80;       // per launch: the table travels in the kernel's arguments
+constexpr int kBlocks = 4;         // per wave
+constexpr int kTensors = 64;       // per launch: one lane each finds a workgroup's tensor
 constexpr float kTop = 448.0f;     // largest e4m3 value
 constexpr float kTiny = 0.001953125f;  // smallest positive one, 2^-9
 
@@ -44,9 +48,8 @@ struct Tensor {
 
 struct AdamWParams {
   Tensor t[kTensors];
-  uint32_t first[kTensors];  // first workgroup of each tensor
-  uint8_t types[kTensors];   // bit 0: bf16 param, bit 1: bf16 grad
-  int n_tensors;
+  uint32_t first[kTensors];  // first workgroup of each tensor; past the last: none
+  uint32_t types[kTensors];  // bit 0: bf16 param, bit 1: bf16 grad, bit 2: aligned for vector accesses
   void* m;
   void* v;
   float* m_scale;  // null: fp32 states
@@ -56,39 +59,63 @@ struct AdamWParams {
 };
 static_assert(sizeof(AdamWParams) <= 4096, "kernel arguments");
 
-// Four elements from element i of a tensor of n (zeros past its end).
-__device__ __forceinline__ void load4(const void* p, bool bf16, int64_t i, int64_t n, float (&x)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[j] = 0.0f;
-    if (i + j < n)
-      x[j] = bf16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i + j]) << 16)
-                  : static_cast<const float*>(p)[i + j];
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+// Four elements from element i: 16 bytes of fp32 or 8 of bf16.
+template <bool kBF16>
+__device__ __forceinline__ f32x4 load4(const void* p, int64_t i) {
+  if constexpr (kBF16) {
+    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i));
+    return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                 __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+  } else {
+    return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i));
+  }
+}
+template <bool kBF16>
+__device__ __forceinline__ void store4(void* p, int64_t i, f32x4 x) {
+  if constexpr (kBF16) {
+    u32x2 w;
+    w.x = bf16_pair(x[0], x[1]);
+    w.y = bf16_pair(x[2], x[3]);
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + i));
+  } else {
+    __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(static_cast<float*>(p) + i));
   }
 }
 
-__device__ __forceinline__ void store4(void* p, bool bf16, int64_t i, int64_t n, const float (&x)[4]) {
+// The same one element at a time, for a tensor's last elements and for
+// pointers at odd elements (zeros past n).
+__device__ __forceinline__ f32x4 load4_any(const void* p, bool bf16, int64_t i, int64_t n) {
+  f32x4 x{};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n)
+      x[j] = bf16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i + j]) << 16)
+                  : static_cast<const float*>(p)[i + j];
+  return x;
+}
+__device__ __forceinline__ void store4_any(void* p, bool bf16, int64_t i, int64_t n, f32x4 x) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (i + j < n) {
       if (bf16)
-        static_cast<uint16_t*>(p)[i + j] = uint16_t(bf16_bits(x[j]));
+        static_cast<uint16_t*>(p)[i + j] = uint16_t(bf16_pair(x[j], 0.0f));
       else
         static_cast<float*>(p)[i + j] = x[j];
     }
   }
 }
 
-__device__ __forceinline__ void decode4(uint32_t c, float s, float (&x)[4]) {
-  x[0] = __builtin_amdgcn_cvt_f32_fp8(int(c), 0) * s;
-  x[1] = __builtin_amdgcn_cvt_f32_fp8(int(c), 1) * s;
-  x[2] = __builtin_amdgcn_cvt_f32_fp8(int(c), 2) * s;
-  x[3] = __builtin_amdgcn_cvt_f32_fp8(int(c), 3) * s;
+__device__ __forceinline__ f32x4 decode4(uint32_t c, float s) {
+  return f32x4{__builtin_amdgcn_cvt_f32_fp8(int(c), 0), __builtin_amdgcn_cvt_f32_fp8(int(c), 1),
+               __builtin_amdgcn_cvt_f32_fp8(int(c), 2), __builtin_amdgcn_cvt_f32_fp8(int(c), 3)} * s;
 }
 
-// Codes of a block, four elements per lane, and its scale.
+// Codes of a block, four elements per lane, and its scale (uniform).
 template <bool kPositive>
-__device__ __forceinline__ uint32_t encode4(const float (&x)[4], float* scale) {
+__device__ __forceinline__ uint32_t encode4(f32x4 x, float* scale) {
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -103,74 +130,156 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float* scale) {
   const float s = __uint_as_float(top) / kTop;
   *scale = s;
   if (s == 0.0f) return 0;
+  // A tiny scale is brought up first: its reciprocal would overflow.
+  const float up = s < 0x1p-64f ? 0x1p64f : 1.0f;
+  const float inv = 1.0f / (s * up);
   float y[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     // A subnormal scale may have been rounded down: the clamp keeps its block's top a number.
-    y[j] = fminf(fmaxf(x[j] / s, -kTop), kTop);
-    if (kPositive) y[j] = x[j] > 0.0f ? fmaxf(y[j], kTiny) : 0.0f;
+    const float q = x[j] * up * inv;
+    y[j] = kPositive ? (x[j] > 0.0f ? __builtin_amdgcn_fmed3f(q, kTiny, kTop) : 0.0f)
+                     : __builtin_amdgcn_fmed3f(q, -kTop, kTop);
   }
-  int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  const int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true));
 }
 
-__global__ __launch_bounds__(64 * kWaves) void adamw_kernel(const AdamWParams P) {
-  int t = 0;  // the tensor of this workgroup: the last whose first workgroup is not past it
-  for (int i = 1; i < P.n_tensors; ++i)
-    if (P.first[i] <= blockIdx.x) t = i;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Tensor T = P.t[t];
-  const bool p16 = P.types[t] & 1, g16 = P.types[t] & 2;
-  const int64_t block = int64_t(blockIdx.x - P.first[t]) * kWaves + wave;
-  if (block * kBlock >= T.n) return;
-  const int64_t i = block * kBlock + lane * 4, n = T.n;
-  float p[4], g[4], m[4], v[4];
-  load4(T.param, p16, i, n, p);
-  load4(T.grad, g16, i, n, g);
-  const int64_t s0 = T.state + i;  // this lane's states; a multiple of 4
-  const bool eight = P.m_scale != nullptr;
-  const int64_t sb = T.state / kBlock + block;
-  if (eight) {
-    uint32_t cm = 0, cv = 0;
-    cm = static_cast<const uint32_t*>(P.m)[s0 / 4];
-    cv = static_cast<const uint32_t*>(P.v)[s0 / 4];
-    decode4(cm, P.m_scale[sb], m);
-    decode4(cv, P.v_scale[sb], v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= v[j];
-  } else {
-    load4(static_cast<const float*>(P.m) + T.state, false, i, n, m);
-    load4(static_cast<const float*>(P.v) + T.state, false, i, n, v);
+// One element: p, m and v after the step, and r = sqrt(v).  The root and the
+// reciprocal are good to an ulp, a 2^-23 of the update each.
+__device__ __forceinline__ void update(const AdamWParams& P, float g, float& p, float& m, float& v, float& r) {
+  m = P.b1 * m + P.one_b1 * g;
+  v = P.b2 * v + P.one_b2 * (g * g);
+  r = __builtin_amdgcn_sqrtf(v);
+  p = p * P.decay - P.rate * (m * __builtin_amdgcn_rcpf(r * P.inv_root_c2 + P.eps));
+}
+
+// The states of a block, as loaded: fp32, or codes and scales.
+template <bool kEight>
+struct RawStates;
+template <>
+struct RawStates<false> {
+  f32x4 m, v;
+  __device__ __forceinline__ void load(const AdamWParams& P, int64_t at, int64_t) {
+    m = load4<false>(P.m, at);
+    v = load4<false>(P.v, at);
   }
-  const float gs = P.grad_scale != nullptr ? *P.grad_scale : 1.0f;
-  float root[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float gj = g[j] * gs;
-    m[j] = P.b1 * m[j] + P.one_b1 * gj;
-    v[j] = P.b2 * v[j] + P.one_b2 * (gj * gj);
-    root[j] = sqrtf(v[j]);
-    p[j] = p[j] * P.decay - P.rate * (m[j] / (root[j] * P.inv_root_c2 + P.eps));
+  __device__ __forceinline__ void get(f32x4& mo, f32x4& vo) const { mo = m; vo = v; }
+  static __device__ __forceinline__ void store(const AdamWParams& P, int64_t at, int64_t, f32x4 m, f32x4 v, f32x4) {
+    store4<false>(P.m, at, m);
+    store4<false>(P.v, at, v);
   }
-  store4(T.param, p16, i, n, p);
-  if (eight) {
-    // Elements past the tensor's end stay out of the block's scale and keep the code zero.
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + j >= n) m[j] = root[j] = 0.0f;
+};
+template <>
+struct RawStates<true> {
+  uint32_t m, v;
+  float ms, vs;
+  __device__ __forceinline__ void load(const AdamWParams& P, int64_t at, int64_t block) {
+    m = __builtin_nontemporal_load(static_cast<const uint32_t*>(P.m) + at / 4);
+    v = __builtin_nontemporal_load(static_cast<const uint32_t*>(P.v) + at / 4);
+    ms = P.m_scale[block];
+    vs = P.v_scale[block];
+  }
+  __device__ __forceinline__ void get(f32x4& mo, f32x4& vo) const {
+    mo = decode4(m, ms);
+    vo = decode4(v, vs);
+    vo *= vo;
+  }
+  static __device__ __forceinline__ void store(const AdamWParams& P, int64_t at, int64_t block, f32x4 m, f32x4,
+                                               f32x4 r) {
     float ms, vs;
-    const uint32_t cm = encode4<false>(m, &ms), cv = encode4<true>(root, &vs);
-    static_cast<uint32_t*>(P.m)[s0 / 4] = cm;
-    static_cast<uint32_t*>(P.v)[s0 / 4] = cv;
-    if (lane == 0) {
-      P.m_scale[sb] = ms;
-      P.v_scale[sb] = vs;
+    const uint32_t cm = encode4<false>(m, &ms), cv = encode4<true>(r, &vs);
+    __builtin_nontemporal_store(cm, static_cast<uint32_t*>(P.m) + at / 4);
+    __builtin_nontemporal_store(cv, static_cast<uint32_t*>(P.v) + at / 4);
+    if ((threadIdx.x & 63) == 0) {
+      P.m_scale[block] = ms;
+      P.v_scale[block] = vs;
     }
-  } else {
-    store4(static_cast<float*>(P.m) + T.state, false, i, n, m);
-    store4(static_cast<float*>(P.v) + T.state, false, i, n, v);
+  }
+};
+
+// kBlocks whole blocks of an aligned tensor, from block0 in steps of kWaves.
+template <bool kEight, bool kP16, bool kG16>
+__device__ __forceinline__ void run_blocks(const AdamWParams& P, const Tensor& T, int64_t block0, float gs) {
+  const int lane = threadIdx.x & 63;
+  f32x4 p[kBlocks], g[kBlocks];
+  RawStates<kEight> s[kBlocks];
+#pragma unroll
+  for (int u = 0; u < kBlocks; ++u) {
+    const int64_t i = (block0 + u * kWaves) * kBlock + lane * 4;
+    p[u] = load4<kP16>(T.param, i);
+    g[u] = load4<kG16>(T.grad, i);
+    s[u].load(P, T.state + i, T.state / kBlock + block0 + u * kWaves);
+  }
+#pragma unroll
+  for (int u = 0; u < kBlocks; ++u) {
+    const int64_t i = (block0 + u * kWaves) * kBlock + lane * 4;
+    f32x4 m, v, r;
+    s[u].get(m, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float pj = p[u][j], mj = m[j], vj = v[j], rj;
+      update(P, g[u][j] * gs, pj, mj, vj, rj);
+      p[u][j] = pj;
+      m[j] = mj;
+      v[j] = vj;
+      r[j] = rj;
+    }
+    store4<kP16>(T.param, i, p[u]);
+    RawStates<kEight>::store(P, T.state + i, T.state / kBlock + block0 + u * kWaves, m, v, r);
   }
 }
+
+// One block that ends the tensor, or of one that is not aligned.
+template <bool kEight>
+__device__ __forceinline__ void run_any(const AdamWParams& P, const Tensor& T, bool p16, bool g16, int64_t block,
+                                        float gs) {
+  const int64_t i = block * kBlock + (threadIdx.x & 63) * 4, n = T.n;
+  f32x4 p = load4_any(T.param, p16, i, n);
+  const f32x4 g = load4_any(T.grad, g16, i, n);
+  RawStates<kEight> s;
+  s.load(P, T.state + i, T.state / kBlock + block);  // a tensor's span holds whole blocks
+  f32x4 m, v, r;
+  s.get(m, v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float pj = p[j], mj = m[j], vj = v[j], rj;
+    update(P, g[j] * gs, pj, mj, vj, rj);
+    const bool on = i + j < n;  // the span's tail keeps out of the block's scale, and stays zero
+    p[j] = pj;
+    m[j] = on ? mj : 0.0f;
+    v[j] = on ? vj : 0.0f;
+    r[j] = on ? rj : 0.0f;
+  }
+  store4_any(T.param, p16, i, n, p);
+  RawStates<kEight>::store(P, T.state + i, T.state / kBlock + block, m, v, r);
+}
+
+template <bool kEight>
+__global__ __launch_bounds__(64 * kWaves) void adamw_kernel(const AdamWParams P) {
+  const int lane = threadIdx.x & 63;
+  // The tensor of this workgroup: the last whose first workgroup is not past it.
+  const int t = __builtin_popcountll(__builtin_amdgcn_ballot_w64(P.first[lane] <= blockIdx.x)) - 1;
+  const Tensor T = P.t[t];
+  const uint32_t types = P.types[t];
+  const float gs = P.grad_scale != nullptr ? *P.grad_scale : 1.0f;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t first = int64_t(blockIdx.x - P.first[t]) * (kWaves * kBlocks), block0 = first + wave;
+  if ((first + kWaves * kBlocks) * kBlock <= T.n && (types & 4)) {
+    switch (types & 3) {
+      case 0: return run_blocks<kEight, false, false>(P, T, block0, gs);
+      case 1: return run_blocks<kEight, true, false>(P, T, block0, gs);
+      case 2: return run_blocks<kEight, false, true>(P, T, block0, gs);
+      default: return run_blocks<kEight, true, true>(P, T, block0, gs);
+    }
+  }
+#pragma unroll 1
+  for (int u = 0; u < kBlocks; ++u)
+    if ((block0 + u * kWaves) * kBlock < T.n)
+      run_any<kEight>(P, T, types & 1, types & 2, block0 + u * kWaves, gs);
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
 
@@ -191,30 +300,36 @@ sr_status launch_adamw(const AdamWRequest& rq) {
   P.eps = float(rq.eps);
   // Fills tables of up to kTensors tensors; the first pass only checks that
   // every launch's grid fits.
+  constexpr int64_t kPer = int64_t(kWaves) * kBlocks * kBlock;  // elements of a workgroup
   for (int pass = 0; pass < 2; ++pass) {
     int64_t state = 0, blocks = 0;
-    P.n_tensors = 0;
+    int k = 0;  // tensors in the table
     for (int64_t i = 0; i <= rq.n_tensors; ++i) {
-      if (P.n_tensors > 0 && (i == rq.n_tensors || P.n_tensors == kTensors)) {
+      if (k > 0 && (i == rq.n_tensors || k == kTensors)) {
         if (blocks > kMaxBlocks256)
-          return fail(SR_ERR_UNSUPPORTED, "%lld elements exceed one launch's grid",
-                      (long long)(blocks * kWaves * kBlock));
+          return fail(SR_ERR_UNSUPPORTED, "%lld elements exceed one launch's grid", (long long)(blocks * kPer));
         if (pass == 1) {
-          hipLaunchKernelGGL(adamw_kernel, dim3(uint32_t(blocks)), dim3(64 * kWaves), 0, rq.stream, P);
+          for (; k < kTensors; ++k) P.first[k] = UINT32_MAX;
+          if (rq.m_scale != nullptr)
+            hipLaunchKernelGGL(adamw_kernel<true>, dim3(uint32_t(blocks)), dim3(64 * kWaves), 0, rq.stream, P);
+          else
+            hipLaunchKernelGGL(adamw_kernel<false>, dim3(uint32_t(blocks)), dim3(64 * kWaves), 0, rq.stream, P);
           const hipError_t err = hipGetLastError();
           if (err != hipSuccess) return fail(SR_ERR_HIP, "AdamW launch: %s", hipGetErrorString(err));
         }
-        P.n_tensors = 0;
+        k = 0;
         blocks = 0;
       }
       if (i == rq.n_tensors) break;
       const sr_adamw_tensor& t = rq.tensors[i];
       if (t.n > 0 && t.grad != nullptr) {
-        const int k = P.n_tensors++;
+        const bool p16 = t.param_dtype == SR_BF16, g16 = t.grad_dtype == SR_BF16;
+        const bool wide = aligned(t.param, p16 ? 8 : 16) && aligned(t.grad, g16 ? 8 : 16);
         P.t[k] = Tensor{t.param, t.grad, t.n, state};
         P.first[k] = uint32_t(blocks);
-        P.types[k] = uint8_t((t.param_dtype == SR_BF16 ? 1 : 0) | (t.grad_dtype == SR_BF16 ? 2 : 0));
-        blocks += (t.n + kWaves * kBlock - 1) / (kWaves * kBlock);
+        P.types[k] = uint32_t((p16 ? 1 : 0) | (g16 ? 2 : 0) | (wide ? 4 : 0));
+        blocks += (t.n + kPer - 1) / kPer;
+        ++k;
       }
       state += adamw_span(t.n);
     }

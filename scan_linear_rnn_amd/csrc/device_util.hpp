@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace sr {
 
@@ -26,14 +27,20 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 // Bits of |x|: ordered like the values, infinities and then NaNs on top.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// The largest value of a wave, in every lane.
+// The largest value of a wave (uniform): lane 15 of each row of 16 collects
+// the row, rows 1 and 3 their predecessor, lane 63 the first half.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_xor(v, d);
+  auto take = [&](auto ctrl) {
+    const uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), decltype(ctrl)::value, 0xF, 0xF, false));
     v = v > o ? v : o;
-  }
-  return v;
+  };
+  take(std::integral_constant<int, 0x111>{});  // row_shr 1, 2, 4, 8
+  take(std::integral_constant<int, 0x112>{});
+  take(std::integral_constant<int, 0x114>{});
+  take(std::integral_constant<int, 0x118>{});
+  take(std::integral_constant<int, 0x142>{});  // row_bcast 15, 31
+  take(std::integral_constant<int, 0x143>{});
+  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
 }
 
 }  // namespace sr

@@ -122,7 +122,7 @@ def test_adamw_calls_without_work_launch_nothing():
 
 
 def test_adamw_grid_limit_is_checked_before_any_launch():
-    big = 1 << 35
+    big = 1 << 40   # more workgroups than one launch holds
     tensors = tuple((0x10000, 0x20000, 4, 0, 0) for _ in range(100)) + ((0x10000, 0x20000, big, 0, 0),)
     assert _adamw(tensors=tensors, n=big * 2) == UNSUP
 
