@@ -35,11 +35,120 @@ __device__ __forceinline__ uint32_t code(float x, float s, bool live) {
   return live ? uint32_t(c) & 0xFFu : 0u;
 }
 
-// One row per workgroup, its elements read twice (the second time from the
-// caches).
+// x / s for a scale s away from the ends of the fp32 range, r = 1 / s
+// correctly rounded: the first correction brings the product within an ulp,
+// the second makes it the IEEE quotient (P. Markstein, Computation of
+// elementary functions on the IBM RISC System/6000, 1990), in five
+// instructions instead of the division's ten.
+__device__ __forceinline__ float divided(float x, float s, float r) {
+  float q = x * r;
+  q = fmaf(fmaf(-q, s, x), r, q);
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+__device__ __forceinline__ bool divides_plainly(float s) { return s > 0x1p-96f && s < 0x1p96f; }
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+// Elements of a 16-byte chunk, and the largest magnitude of one.
 template <typename T>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t ldx, int64_t K,
-                                                            int64_t Kp, int8_t* q, float* scale) {
+struct Chunk {
+  static constexpr int kSize = 16 / sizeof(T);
+  static __device__ __forceinline__ float get(u32x4 w, int e) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    return __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+  }
+};
+
+// WPR waves per row, NV 16-byte chunks per lane: the row is read once and
+// stays in registers.  Loads go through a descriptor that ends with the row,
+// so chunks past its end are zeros and become the padding.  Bound by the
+// bytes of a large x (131072 x 2048 fp32: see the launch), by latency for a
+// few rows, which is why those take four waves each.
+template <typename T, int WPR, int NV>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t ldx, int64_t M, int K,
+                                                            int Kp, int8_t* q, float* scale) {
+  using C = Chunk<T>;
+  __shared__ uint32_t s_top[4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t row = int64_t(blockIdx.x) * (4 / WPR) + wave / WPR;
+  if (row >= M) return;  // (WPR == 4: never)
+  const int c0 = wave % WPR * 64 + lane;
+  // bf16 rows of odd length end within a dword, whose other half is masked.
+  const int bytes = (K * int(sizeof(T)) + 3) & ~3;
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(x + row * ldx), 0, bytes, 0x00020000);
+  u32x4 w[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    w[j] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (c0 + j * 64 * WPR) * 16, 0, 2);
+  if (sizeof(T) == 2 && (K & 1)) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        if ((c0 + j * 64 * WPR) * 8 + d * 2 + 1 == K) w[j][d] &= 0xFFFFu;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int e = 0; e < C::kSize; ++e) {
+      const uint32_t b = abs_bits(C::get(w[j], e));
+      top = top > b ? top : b;
+    }
+  }
+  top = wave_max(top);
+  if constexpr (WPR == 4) {
+    if (lane == 0) s_top[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < 4; ++v) top = top > s_top[v] ? top : s_top[v];
+  }
+  const float s = row_scale(top);
+  const bool live = s > 0.0f;
+  if (c0 == 0) scale[row] = s;
+  int8_t* dst = q + row * int64_t(Kp);
+  // The quotients of the two paths are the same numbers.
+  const bool plain = divides_plainly(s);
+  const float r = plain ? __fdiv_rn(1.0f, s) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int k = (c0 + j * 64 * WPR) * C::kSize;
+    uint32_t codes[C::kSize / 4];
+    if (plain) {
+#pragma unroll
+      for (int d = 0; d < C::kSize / 4; ++d) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          // |x| <= 127 s (1 + 2^-24), so the quotient rounds to 127 at most.
+          const int c = int(rintf(divided(C::get(w[j], d * 4 + e), s, r)));
+          v = (v << 8) | (uint32_t(c) & 0xFFu);
+        }
+        codes[d] = v;
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < C::kSize / 4; ++d) {
+        codes[d] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) codes[d] |= code(C::get(w[j], d * 4 + e), s, live) << (8 * e);
+      }
+    }
+    if (k < Kp) {
+      if constexpr (C::kSize == 8)
+        __builtin_nontemporal_store(u32x2{codes[0], codes[1]}, reinterpret_cast<u32x2*>(dst + k));
+      else
+        __builtin_nontemporal_store(codes[0], reinterpret_cast<uint32_t*>(dst + k));
+    }
+  }
+}
+
+// Rows too long for registers, or of bf16 at odd elements: one per workgroup,
+// read twice (the second time from the caches).
+template <typename T>
+__global__ __launch_bounds__(256) void quantize_any_rows_kernel(const T* x, int64_t ldx, int64_t K,
+                                                                int64_t Kp, int8_t* q, float* scale) {
   __shared__ uint32_t s_top[4];
   const int64_t row = blockIdx.x;
   const T* src = x + row * ldx;
@@ -51,9 +160,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t 
   top = wave_max(top);
   if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
   __syncthreads();
-  top = s_top[0];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) top = top > s_top[w] ? top : s_top[w];
+  for (int w = 0; w < 4; ++w) top = top > s_top[w] ? top : s_top[w];
   const float s = row_scale(top);
   const bool live = s > 0.0f;
   if (threadIdx.x == 0) scale[row] = s;
@@ -67,13 +175,100 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t 
   }
 }
 
-// Columns of W [K, N] (row-major) become rows of codes: a workgroup owns
-// kColTile columns, finds their largest magnitudes over all K rows, then
-// reads the rows again and writes four codes of a column at a time.
+// Columns of W [K, N] (row-major) become rows of codes.  A workgroup of 1024
+// threads owns 64 bytes of columns, four threads to a row; a thread holds four
+// consecutive rows of a pass of 1024, so that it writes four codes of a
+// column as one dword, and all of W is read once.  Neighbouring workgroups
+// share the other half of each line, so each XCD takes a contiguous range.
+template <typename T, int NP>
+__global__ __launch_bounds__(1024) void quantize_columns_kernel(const T* W, int64_t ldw, int K, int64_t N,
+                                                                int Kp, int8_t* q, float* scale) {
+  using C = Chunk<T>;
+  constexpr int V = C::kSize, kCols = 4 * V;
+  __shared__ uint32_t s_top[16][kCols];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t per = gridDim.x / 8;
+  const uint32_t tile = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
+  const int64_t n0 = int64_t(tile) * kCols;
+  const int c = (threadIdx.x & 3) * V, g = threadIdx.x >> 2;
+  // Rows past K fall behind the descriptor's end and read as zeros; columns
+  // past N read the next row's and are not stored.
+  const int64_t elements = int64_t(K - 1) * ldw + (N - n0);
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<T*>(W + n0), 0, int(uint32_t((elements * int64_t(sizeof(T)) + 3) & ~int64_t(3))), 0x00020000);
+  u32x4 w[NP][4];
+  const uint32_t row_bytes = uint32_t(ldw * int64_t(sizeof(T)));
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = p * 1024 + 4 * g + i;
+      const uint32_t off = uint32_t(k) * row_bytes + uint32_t(c * int(sizeof(T)));
+      w[p][i] = u32x4{};
+      if (k < K) w[p][i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, int(off), 0, 0);
+    }
+  uint32_t top[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    top[e] = 0;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = abs_bits(C::get(w[p][i], e));
+        top[e] = top[e] > b ? top[e] : b;
+      }
+#pragma unroll
+    for (int d = 4; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_xor(top[e], d);
+      top[e] = top[e] > o ? top[e] : o;
+    }
+  }
+  if (lane < 4) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_top[wave][c + e] = top[e];
+  }
+  __syncthreads();
+  if (threadIdx.x < kCols) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) t = t > s_top[v][threadIdx.x] ? t : s_top[v][threadIdx.x];
+    s_top[0][threadIdx.x] = t;  // (only this thread reads the column)
+    if (n0 + threadIdx.x < N) scale[n0 + threadIdx.x] = row_scale(t);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if (n0 + c + e >= N) break;
+    const float s = row_scale(s_top[0][c + e]);
+    const bool live = s > 0.0f, plain = divides_plainly(s);
+    const float r = plain ? __fdiv_rn(1.0f, s) : 0.0f;
+    int8_t* dst = q + (n0 + c + e) * int64_t(Kp);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int k = p * 1024 + 4 * g;
+      if (k >= Kp) break;
+      uint32_t v = 0;
+      if (plain) {
+#pragma unroll
+        for (int i = 3; i >= 0; --i)
+          v = (v << 8) | (uint32_t(int(rintf(divided(C::get(w[p][i], e), s, r)))) & 0xFFu);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v |= code(C::get(w[p][i], e), s, live) << (8 * i);
+      }
+      *reinterpret_cast<uint32_t*>(dst + k) = v;
+    }
+  }
+}
+
+// Columns that the kernel above does not take (K beyond its registers, bf16
+// at odd elements, 4 GiB and more): a workgroup owns kColTile columns, finds
+// their largest magnitudes over all K rows, then reads the rows again.
 constexpr int kColTile = 16;
 
 template <typename T>
-__global__ __launch_bounds__(256) void quantize_columns_kernel(const T* W, int64_t ldw, int64_t K,
+__global__ __launch_bounds__(256) void quantize_any_columns_kernel(const T* W, int64_t ldw, int64_t K,
                                                                int64_t N, int64_t Kp, int8_t* q,
                                                                float* scale) {
   constexpr int kGroups = 256 / kColTile;  // row groups
@@ -112,6 +307,42 @@ sr_status launched(const char* what) {
   return SR_OK;
 }
 
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <typename T, int WPR>
+void launch_rows(int nv, int64_t M, int K, int Kp, const T* x, int64_t ldx, int8_t* q, float* scale,
+                 hipStream_t stream) {
+  const dim3 grid{uint32_t((M + 4 / WPR - 1) / (4 / WPR))}, block{256};
+#define SR_ROWS(NV)                                                                                       \
+  hipLaunchKernelGGL((quantize_rows_kernel<T, WPR, NV>), grid, block, 0, stream, x, ldx, M, K, Kp, q, scale)
+  if (nv <= 1) SR_ROWS(1);
+  else if (nv <= 2) SR_ROWS(2);
+  else if (nv <= 4) SR_ROWS(4);
+  else if (nv <= 8) SR_ROWS(8);
+  else SR_ROWS(16);
+#undef SR_ROWS
+}
+
+// Chunks per lane that the kernels for whole rows go up to.
+constexpr int kMaxChunks = 16;
+// Fewer rows than this take four waves each: a wave per row would leave SIMDs idle.
+constexpr int64_t kFewRows = 1024;
+
+template <typename T>
+void launch_rows(int64_t M, int64_t K, const T* x, int64_t ldx, int8_t* q, float* scale,
+                 hipStream_t stream) {
+  const int64_t Kp = quantized_row_bytes(K);
+  const int64_t chunks = (Kp * int64_t(sizeof(T)) + 15) / 16;  // Kp: the padding is written too
+  const bool dwords = sizeof(T) == 4 || (ldx % 2 == 0 && aligned(x, 4)) || (M == 1 && aligned(x, 4));
+  if (K == 0 || !dwords || chunks > 4 * 64 * kMaxChunks)
+    hipLaunchKernelGGL(quantize_any_rows_kernel<T>, dim3(uint32_t(M)), dim3(256), 0, stream, x, ldx, K, Kp, q,
+                       scale);
+  else if (M < kFewRows || chunks > 64 * kMaxChunks)
+    launch_rows<T, 4>(int((chunks + 255) / 256), M, int(K), int(Kp), x, ldx, q, scale, stream);
+  else
+    launch_rows<T, 1>(int((chunks + 63) / 64), M, int(K), int(Kp), x, ldx, q, scale, stream);
+}
+
 }  // namespace
 
 sr_status launch_quantize_rows(int64_t M, int64_t K, const void* x, int64_t ldx, sr_dtype dtype,
@@ -120,31 +351,46 @@ sr_status launch_quantize_rows(int64_t M, int64_t K, const void* x, int64_t ldx,
   if (M > kMaxBlocks256)
     return fail(SR_ERR_UNSUPPORTED, "%lld rows exceed one launch's grid", (long long)M);
   if (check_only) return SR_OK;
-  const int64_t Kp = quantized_row_bytes(K);
-  const dim3 grid{uint32_t(M)};
   if (dtype == SR_BF16)
-    hipLaunchKernelGGL(quantize_rows_kernel<uint16_t>, grid, dim3(256), 0, stream,
-                       static_cast<const uint16_t*>(x), ldx, K, Kp, q, scale);
+    launch_rows(M, K, static_cast<const uint16_t*>(x), ldx, q, scale, stream);
   else
-    hipLaunchKernelGGL(quantize_rows_kernel<float>, grid, dim3(256), 0, stream,
-                       static_cast<const float*>(x), ldx, K, Kp, q, scale);
+    launch_rows(M, K, static_cast<const float*>(x), ldx, q, scale, stream);
   return launched("row quantisation");
 }
+
+namespace {
+
+template <typename T>
+void launch_columns(int64_t K, int64_t N, const T* W, int64_t ldw, int8_t* q, float* scale,
+                    hipStream_t stream) {
+  const int64_t Kp = quantized_row_bytes(K);
+  const bool dwords = sizeof(T) == 4 || ((ldw % 2 == 0 || K == 1) && aligned(W, 4));
+  if (K == 0 || K > 4096 || !dwords || K * ldw * int64_t(sizeof(T)) > int64_t(0xFFFFFFFF) - 256) {
+    hipLaunchKernelGGL(quantize_any_columns_kernel<T>, dim3(uint32_t((N + kColTile - 1) / kColTile)), dim3(256), 0,
+                       stream, W, ldw, K, N, Kp, q, scale);
+    return;
+  }
+  constexpr int kCols = 4 * Chunk<T>::kSize;
+  const dim3 grid{uint32_t((N + kCols - 1) / kCols)}, block{1024};
+  if (K <= 1024)
+    hipLaunchKernelGGL((quantize_columns_kernel<T, 1>), grid, block, 0, stream, W, ldw, int(K), N, int(Kp), q, scale);
+  else if (K <= 2048)
+    hipLaunchKernelGGL((quantize_columns_kernel<T, 2>), grid, block, 0, stream, W, ldw, int(K), N, int(Kp), q, scale);
+  else
+    hipLaunchKernelGGL((quantize_columns_kernel<T, 4>), grid, block, 0, stream, W, ldw, int(K), N, int(Kp), q, scale);
+}
+
+}  // namespace
 
 sr_status launch_quantize_columns(int64_t K, int64_t N, const void* W, int64_t ldw, sr_dtype dtype,
                                   int8_t* q, float* scale, hipStream_t stream) {
   if (N == 0) return SR_OK;
-  const int64_t blocks = (N + kColTile - 1) / kColTile;
-  if (blocks > kMaxBlocks256)
+  if (N > kMaxBlocks256)
     return fail(SR_ERR_UNSUPPORTED, "%lld columns exceed one launch's grid", (long long)N);
-  const int64_t Kp = quantized_row_bytes(K);
-  const dim3 grid{uint32_t(blocks)};
   if (dtype == SR_BF16)
-    hipLaunchKernelGGL(quantize_columns_kernel<uint16_t>, grid, dim3(256), 0, stream,
-                       static_cast<const uint16_t*>(W), ldw, K, N, Kp, q, scale);
+    launch_columns(K, N, static_cast<const uint16_t*>(W), ldw, q, scale, stream);
   else
-    hipLaunchKernelGGL(quantize_columns_kernel<float>, grid, dim3(256), 0, stream,
-                       static_cast<const float*>(W), ldw, K, N, Kp, q, scale);
+    launch_columns(K, N, static_cast<const float*>(W), ldw, q, scale, stream);
   return launched("column quantisation");
 }
 
