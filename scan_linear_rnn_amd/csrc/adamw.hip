@@ -9,8 +9,9 @@
 // in fp32 whatever the tensors' types; p is rounded once when it is bf16.
 //
 // 8-bit states.  A block of kStateBlock consecutive elements of a tensor
-// shares one fp32 scale for m and one for r = sqrt(v): s = max |.| / 448,
-// codes are the OCP float8 e4m3 nearest to m / s and to r / s.  The root
+// shares one fp32 scale for m and one for r = sqrt(v): s = max |.| / 448 (times
+// the fp32 nearest to 1 / 448), codes are the OCP float8 e4m3 nearest to m / s
+// and to r / s.  The root
 // halves the range that the second moment spans, so that e4m3's 17.8 octaves
 // hold 35 of v; a positive r is never stored as zero (it is raised to the
 // smallest positive code, 2^-9), since the update divides by it.  The update
@@ -127,17 +128,16 @@ __device__ __forceinline__ uint32_t encode4(f32x4 x, float* scale) {
     *scale = __uint_as_float(0x7FC00000u);
     return 0;
   }
-  const float s = __uint_as_float(top) / kTop;
+  const float s = __uint_as_float(top) * (1.0f / kTop);
   *scale = s;
   if (s == 0.0f) return 0;
-  // A tiny scale is brought up first: its reciprocal would overflow.
-  const float up = s < 0x1p-64f ? 0x1p64f : 1.0f;
-  const float inv = 1.0f / (s * up);
+  const bool plain = divides_plainly(s);
+  const float inv = plain ? __fdiv_rn(1.0f, s) : 0.0f;
   float y[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     // A subnormal scale may have been rounded down: the clamp keeps its block's top a number.
-    const float q = x[j] * up * inv;
+    const float q = plain ? divided(x[j], s, inv) : __fdiv_rn(x[j], s);
     y[j] = kPositive ? (x[j] > 0.0f ? __builtin_amdgcn_fmed3f(q, kTiny, kTop) : 0.0f)
                      : __builtin_amdgcn_fmed3f(q, -kTop, kTop);
   }
@@ -145,12 +145,16 @@ __device__ __forceinline__ uint32_t encode4(f32x4 x, float* scale) {
   return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true));
 }
 
-// One element: p, m and v after the step, and r = sqrt(v).  The root and the
-// reciprocal are good to an ulp, a 2^-23 of the update each.
+// One element: p, m and v after the step, and r = sqrt(v).  What becomes a
+// state is rounded operation by operation, as written, never fused, and the
+// root is the IEEE one: where an element lies on the tie of two 8-bit codes,
+// the code is then a function of the formula and not of what the compiler
+// contracts.  The reciprocal in p's update is good to an ulp, 2^-23 of it.
 __device__ __forceinline__ void update(const AdamWParams& P, float g, float& p, float& m, float& v, float& r) {
-  m = P.b1 * m + P.one_b1 * g;
-  v = P.b2 * v + P.one_b2 * (g * g);
-  r = __builtin_amdgcn_sqrtf(v);
+#pragma clang fp contract(off)
+  m = m * P.b1 + g * P.one_b1;
+  v = v * P.b2 + g * g * P.one_b2;
+  r = sqrtf(v);
   p = p * P.decay - P.rate * (m * __builtin_amdgcn_rcpf(r * P.inv_root_c2 + P.eps));
 }
 

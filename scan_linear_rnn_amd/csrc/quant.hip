@@ -35,18 +35,6 @@ __device__ __forceinline__ uint32_t code(float x, float s, bool live) {
   return live ? uint32_t(c) & 0xFFu : 0u;
 }
 
-// x / s for a scale s away from the ends of the fp32 range, r = 1 / s
-// correctly rounded: the first correction brings the product within an ulp,
-// the second makes it the IEEE quotient (P. Markstein, Computation of
-// elementary functions on the IBM RISC System/6000, 1990), in five
-// instructions instead of the division's ten.
-__device__ __forceinline__ float divided(float x, float s, float r) {
-  float q = x * r;
-  q = fmaf(fmaf(-q, s, x), r, q);
-  return fmaf(fmaf(-q, s, x), r, q);
-}
-__device__ __forceinline__ bool divides_plainly(float s) { return s > 0x1p-96f && s < 0x1p96f; }
-
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 

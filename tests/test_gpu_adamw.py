@@ -117,6 +117,47 @@ def test_8bit_states(p_type, g_type):
             _check_codes(v[o:end], vs[b], np.concatenate([np.sqrt(vi), pad]), True)
 
 
+def test_8bit_states_are_the_formula_operation_by_operation():
+    """Codes on ties are decided by float32 roundings: NumPy's float32, one
+    operation at a time, gives the same codes and scales bit for bit, two
+    steps on (the second step starts from the first one's codes)."""
+    say("adamw 8-bit codes")
+    f = np.float32
+    n, (b1, b2) = 40 * 256, HYPER["betas"]
+    g = torch.Generator()
+    g.manual_seed(4015)
+    p = torch.randn(n, generator=g).cuda()
+    opt = sr.AdamW([p], state_bits=8, **HYPER)
+    vals = adamw.e4m3_values().astype(f)
+    mid = (vals[1:].astype(np.float64) + vals[:-1]) / 2          # ties go to the even code
+
+    def nearest(y):
+        i = np.searchsorted(mid, np.abs(y).astype(np.float64), side="left")
+        tie = (i < len(mid)) & (np.abs(y).astype(np.float64) == mid[np.minimum(i, len(mid) - 1)])
+        i = np.where(tie & (i % 2 == 1), i + 1, i)
+        return np.where(y < 0, -vals[i], vals[i]).astype(f)
+
+    def encode(x, positive):
+        x = x.reshape(-1, 256)
+        s = np.abs(x).max(1) * (f(1) / f(448))
+        y = x / s[:, None]
+        y = np.where(x > 0, np.maximum(y, f(adamw.TINY)), y) if positive else y
+        return nearest(np.minimum(np.maximum(y, f(-448)), f(448))), s
+
+    m = v = np.zeros((40, 256), f)
+    for step in (1, 2):
+        grad = torch.randn(n, generator=g) * 0.01
+        opt.step([grad.cuda()])
+        gn = grad.numpy().reshape(-1, 256)
+        m = m * f(b1) + gn * f(1 - b1)
+        v = v * f(b2) + gn * gn * f(1 - b2)
+        assert m.dtype == v.dtype == f
+        (mc, ms), (vc, vs) = encode(m, False), encode(np.sqrt(v), True)
+        for name, want, got in (("m", mc, opt.m), ("v", vc, opt.v), ("ms", ms, opt.m_scale), ("vs", vs, opt.v_scale)):
+            assert np.array_equal(got.float().cpu().numpy().reshape(want.shape), want), (step, name)
+        m, v = mc * ms[:, None], (vc * vs[:, None]) ** 2
+
+
 @pytest.mark.parametrize("bits", [8, 32])
 def test_many_tensors_and_skipped_gradients(bits):
     """More tensors than one launch's table holds, some without a gradient:

@@ -146,6 +146,41 @@ def test_large_product_every_element(M, K, N, dtype):
     assert bool(((y - ref).abs() <= tol * ref.abs()).all())
 
 
+@pytest.mark.parametrize("M,K,N", [(5000, 1024, 3001), (1000, 640, 4097), (9000, 384, 4000), (16390, 128, 2055),
+                                   (300, 128, 4100), (2047, 1024, 1537), (700, 2048, 2600)])
+def test_odd_widths_and_line_counts_every_element(M, K, N):
+    """Rows of results at odd elements, tiles that end inside, one, three and
+    five lines of depth: each kernel against float64, and the bytes around the
+    results untouched."""
+    say(f"i8 odd product {M}x{K}x{N}")
+    a, sa, b, sb = (dev(t, torch.int8 if t.dtype == np.int8 else torch.float32)
+                    for t in _operands(np.random.default_rng([3115, M, K, N]), M, K, N))
+    ref = (a.double() @ b.double().t().contiguous()) * (sa.double()[:, None] * sb.double())
+    for dtype, tol in ((torch.float32, F32_TOL), (torch.bfloat16, BF16_TOL)):
+        big = torch.full(((M + 2) * N + 1,), -7.0, device="cuda", dtype=dtype)
+        y = big[N + 1:N + 1 + M * N].view(M, N)      # starts at an odd element
+        sr.matmul_i8(a, sa, b, sb, out=y)
+        assert bool(((y.double() - ref).abs() <= tol * ref.abs()).all())
+        assert bool((big[:N + 1] == -7).all() and (big[N + 1 + M * N:] == -7).all())
+
+
+@pytest.mark.parametrize("M,K,N", [(64, 2048, 4096), (256, 2048, 4096), (1500, 2048, 1000), (4096, 1024, 4096),
+                                   (3000, 1152, 3000)])
+def test_products_repeat_bit_for_bit(M, K, N):
+    """Forty calls in a row on alternating operands: a stage read before it
+    has landed, or loaded before it has been read, would differ now and then."""
+    say(f"i8 repeat {M}x{K}x{N}")
+    sets = [[dev(t, torch.int8 if t.dtype == np.int8 else torch.float32)
+             for t in _operands(np.random.default_rng([3118, M, i]), M, K, N)] for i in range(2)]
+    refs = [(a.double() @ b.double().t().contiguous() * (sa.double()[:, None] * sb.double())).float()
+            for a, sa, b, sb in sets]
+    first = [sr.matmul_i8(*s) for s in sets]
+    for y, ref in zip(first, refs):
+        assert bool(((y - ref).abs() <= 2 * F32_TOL * ref.abs()).all())
+    for rep in range(40):
+        assert torch.equal(sr.matmul_i8(*sets[rep % 2]), first[rep % 2]), rep
+
+
 def test_product_extreme_codes_at_the_deepest_k():
     """All codes 127 at K = 131072: the sum 127^2 K is just below 2^31."""
     say("i8 deepest product")
@@ -236,7 +271,8 @@ def _h_close(h, k, p, h_prev, decay=1.0):
 
 
 STEPS = [(1, 16, 16, 16), (2, 512, 512, 512), (16, 100, 33, 7), (17, 192, 200, 130), (33, 300, 64, 65),
-         (64, 128, 65, 1), (130, 257, 100, 64), (256, 1024, 512, 700), (600, 64, 190, 33)]
+         (64, 128, 65, 1), (130, 257, 100, 64), (256, 1024, 512, 700), (600, 64, 190, 33),
+         (1030, 384, 1100, 200), (4100, 200, 513, 130)]
 
 
 @pytest.mark.parametrize("B,D_in,D_h,D_out", STEPS)
