@@ -39,6 +39,7 @@ constexpr bool is_step(int out) { return out >= kStep; }
 
 constexpr int kDepth = 128;             // bytes of K per stage: whole lines
 constexpr int kRsrcWord3 = 0x00020000;  // raw buffer, gfx9 format
+constexpr int kNonTemporal = 2;         // cache policy of a store
 constexpr int kCus = 256;
 
 struct I8Params {
@@ -51,7 +52,7 @@ struct I8Params {
   const float* b_scale;  // [N]
   void* C;               // [M, N], rows of ldc elements
   int64_t ldc;
-  bool vec4;             // rows of C start at multiples of 4 bytes
+  bool vec4, lines;      // rows of C start at multiples of 4 bytes, of 128 bytes
   uint32_t tiles_m, tiles_n, n_tiles;
   // step: k and p are columns d and D_h + d
   int64_t D_h;
@@ -351,9 +352,12 @@ struct LargeTile {
   i32x4 fa[2][MB], fb[2][NB];
   i32x16 acc[MB][NB];
 
-  // Tiles in groups of kGroupM tile rows, column by column within a group.
+  // Tiles in groups of kGroupM tile rows, column by column within a group: the
+  // 32 tiles that run on an XCD at a time share 8 row and 4 column tiles.
+  // Measured (131072 x 2048 x 4096, bf16 results): groups of 2, 4, 8, 16 rows
+  // 1185, 1094, 1062, 1069 us.
   __device__ __forceinline__ void origin(uint32_t t, int64_t& m0, int64_t& n0) const {
-    constexpr uint32_t kGroupM = 4;
+    constexpr uint32_t kGroupM = 8;
     const uint32_t per_group = kGroupM * P.tiles_n;
     const uint32_t g = t / per_group, in = t % per_group;
     const uint32_t left = P.tiles_m - g * kGroupM;
@@ -515,6 +519,10 @@ struct LargeTile {
         t[j][g] = load4(rt, (j * R + 8 * g + 4 * (lane / R)) * 4);
     // 16-byte stores need 4-byte alignment only.
     const bool wide = P.vec4 && P.ldc <= (int64_t(1) << 20);
+    // The largest products' results leave the caches to the operands (131072 x
+    // 512 x 1024 fp32: 164 -> 134 us); where lines are shared by two rows of
+    // results, that would write them twice (20000 x 2048 x 1000: 55 -> 65 us).
+    const bool stream = S::MB == 4 && P.lines;
     const int row = lane % R, swz = row % kChunks;
     const int c = lane % kChunks, r0 = lane / kChunks;
     char* dst = static_cast<char*>(P.C) + (m0 * P.ldc + n0) * kSize;
@@ -547,9 +555,13 @@ struct LargeTile {
           for (int q = 0; q < R / kRowsPer; ++q) {
             const int r = q * kRowsPer + r0;
             const u32x4 v = *reinterpret_cast<const u32x4*>(out + r * S::kOutRow + ((c ^ (r % kChunks)) << 4));
-            if (i * R + r < rows && n + kPer <= cols)
-              __builtin_amdgcn_raw_buffer_store_b128(v, rc, voff_c + pass * S::kOutRow,
-                                                     (i * R + q * kRowsPer) * row_bytes, 0);
+            const int voff = voff_c + pass * S::kOutRow, soff = (i * R + q * kRowsPer) * row_bytes;
+            if (i * R + r < rows && n + kPer <= cols) {
+              if (stream)
+                __builtin_amdgcn_raw_buffer_store_b128(v, rc, voff, soff, kNonTemporal);
+              else
+                __builtin_amdgcn_raw_buffer_store_b128(v, rc, voff, soff, 0);
+            }
           }
         }
         // What a 16-byte store cannot hold: the columns past the last whole
@@ -817,6 +829,7 @@ sr_status launch_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64
   P.C = C; P.ldc = ldc;
   const int64_t row_bytes = ldc * (c_dtype == SR_BF16 ? 2 : 4);
   P.vec4 = row_bytes % 4 == 0 && aligned(C, 4);
+  P.lines = row_bytes % 128 == 0 && aligned(C, 128);
   return c_dtype == SR_BF16 ? launch<kBF16>(P, stream, check_only) : launch<kF32>(P, stream, check_only);
 }
 
