@@ -22,9 +22,7 @@ caller can train through the scan (autograd only records the call).
 
 from __future__ import annotations
 
-import array
 import ctypes
-import operator
 import os
 
 import torch
@@ -232,12 +230,6 @@ def _operand(t):
 
 def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _stream_of(t) -> int:
-    """The current stream's handle on a GPU tensor's device (without the
-    Stream object that current_stream makes: 2 us of a call's 10)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _dev(t: torch.Tensor, name: str, dtype=torch.float32, ndim=None, shape=None):
@@ -586,65 +578,21 @@ def minmax_scan_backward(r, s, x0, x_out, dx, dx_last=None, workspace=None):
     return dr, ds, dx0
 
 
-_DTYPES = {torch.float32: SR_F32, torch.bfloat16: SR_BF16}
-
-
-def _gpu(t, name, dtype=None):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if dtype is None:
-        if t.dtype not in _DTYPES:
-            raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
-    elif t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-
-
-def _same_device(device: int, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"{name} must be on cuda:{device} (got {t.device})")
-
-
-def _scales(t, name, n):
-    """n contiguous fp32 scales."""
-    _gpu(t, name, torch.float32)
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements (got shape {tuple(t.shape)})")
-    return t if t.is_contiguous() else t.contiguous()
-
-
-def _rows(t, name, ndim=None):
-    """A GPU tensor of fp32 or bf16 as rows of its last dimension: (tensor,
-    rows, width, row stride); a view when it can be one."""
-    _gpu(t, name)
-    dims = t.dim()
-    if dims < 1 or (ndim is not None and dims != ndim):
-        raise ValueError(f"{name} must have {ndim or 'at least one'} dims (got shape {tuple(t.shape)})")
-    K = t.shape[-1]
-    if dims == 2 and not t.is_contiguous() and t.stride(1) == 1 and t.stride(0) >= K and t.shape[0] > 1:
-        return t, t.shape[0], K, t.stride(0)
-    M = t.shape[0] if dims == 2 else t.shape[:-1].numel()
-    return (t if t.is_contiguous() else t.contiguous()), M, K, K
-
-
-def _codes(t, name, dims=None):
-    """An int8 GPU tensor of codes [.., K] as rows: (tensor, rows, row stride)."""
-    _gpu(t, name, torch.int8)
-    nd = t.dim()
-    if nd < 2 or (dims is not None and nd != dims):
-        raise ValueError(f"{name} must have {dims or 'at least 2'} dims (got shape {tuple(t.shape)})")
-    K = t.shape[-1]
-    if K % 128:
-        raise ValueError(f"{name} must have rows of a multiple of 128 codes, zeros behind the data (got {K})")
-    M = t.shape[0] if nd == 2 else t.shape[:-1].numel()
-    if not t.is_contiguous():
-        if nd == 2 and t.stride(1) == 1 and t.stride(0) >= K and t.stride(0) % 16 == 0 \
-                and t.data_ptr() % 16 == 0 and M > 1:
-            return t, M, t.stride(0)
-        t = t.contiguous()
-    return (t if t.data_ptr() % 16 == 0 else t.clone()), M, K
+# The 8-bit and AdamW calls are marshalled in C++ (csrc/binding.cpp): their small
+# calls take 3 us on the GPU, which Python's checks would double.
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError("the compiled binding is missing or does not load: build it first "
+                      f"(python scan_linear_rnn_amd/build.py): {e}") from e
+_binding.init({name: ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in EXPORTED},
+              ScanRNNError)
+quantize_rows = _binding.quantize_rows
+quantize_columns = _binding.quantize_columns
+matmul_i8 = _binding.matmul_i8
+mingru_step_i8 = _binding.mingru_step_i8
+mingru_forward_i8 = _binding.mingru_forward_i8
+adamw_step = _binding.adamw_step
 
 
 def quantized_row_bytes(K: int) -> int:
@@ -652,283 +600,10 @@ def quantized_row_bytes(K: int) -> int:
     return _lib.quantized_row_bytes(K)
 
 
-def _code_out(q, scale, rows, width, like):
-    if q is None:
-        q = like.new_empty((rows, width), dtype=torch.int8)
-    elif _dev(q, "q", dtype=torch.int8, shape=(rows, width)) is not q or q.device != like.device:
-        raise ValueError(f"q must be contiguous and on {like.device}")
-    if scale is None:
-        scale = like.new_empty((rows,), dtype=torch.float32)
-    elif _dev(scale, "scale", shape=(rows,)) is not scale or scale.device != like.device:
-        raise ValueError(f"scale must be contiguous and on {like.device}")
-    return q, scale
-
-
-def quantize_rows(x, q=None, scale=None):
-    """Symmetric 8-bit codes of the rows (last dimension) of ``x`` [.., K],
-    fp32 or bf16, with a scale each: scale = max|x| / 127, q = rint(x / scale).
-
-    Returns (q [.., quantized_row_bytes(K)] int8, zeros behind the K codes,
-    scale [..] fp32).  A row of zeros has scale 0; a row with a NaN or an
-    infinity has scale NaN and codes 0.  ``q`` [rows, ..] and ``scale`` [rows]
-    may be given to avoid the allocations."""
-    src, M, K, ldx = _rows(x, "x")
-    given = q is not None or scale is not None
-    q, scale = _code_out(q, scale, M, (K + 127) // 128 * 128, src)
-    st = _lib.quantize_rows(M, K, src.data_ptr(), ldx, _DTYPES[src.dtype], q.data_ptr(),
-                            scale.data_ptr(), _stream_of(src))
-    if st:
-        _check("quantize_rows", st)
-    if given or x.dim() == 2:
-        return q, scale
-    return q.view(*x.shape[:-1], q.shape[1]), scale.view(x.shape[:-1])
-
-
-def quantize_columns(W, q=None, scale=None):
-    """8-bit codes of the columns of a weight ``W`` [K, N] (an output channel
-    each), laid out for matmul_i8: (q [N, quantized_row_bytes(K)] int8, scale
-    [N] fp32), as quantize_rows of its transpose."""
-    src, K, N, ldw = _rows(W, "W", ndim=2)
-    q, scale = _code_out(q, scale, N, (K + 127) // 128 * 128, src)
-    st = _lib.quantize_columns(K, N, src.data_ptr(), ldw, _DTYPES[src.dtype], q.data_ptr(),
-                               scale.data_ptr(), _stream_of(src))
-    if st:
-        _check("quantize_columns", st)
-    return q, scale
-
-
-def matmul_i8(a, a_scale, b, b_scale, out_dtype=torch.float32, out=None):
-    """y[.., n] = (sum_k a[.., k] b[n, k]) (a_scale[..] b_scale[n]): the product
-    of codes ``a`` [.., K] (quantize_rows) and ``b`` [N, K] (quantize_columns),
-    summed exactly in 32-bit integers.  K is the stored width, a multiple of
-    128.  Returns y [.., N] in ``out_dtype`` (float32 or bfloat16)."""
-    rows, M, lda = _codes(a, "a")
-    cols, N, ldb = _codes(b, "b", 2)
-    K = rows.shape[-1]
-    if cols.shape[1] != K:
-        raise ValueError(f"a and b must have rows of the same width (got {K} and {cols.shape[1]})")
-    a_scale = _scales(a_scale, "a_scale", M)
-    b_scale = _scales(b_scale, "b_scale", N)
-    _same_device(a.get_device(), a_scale=a_scale, b=b, b_scale=b_scale)
-    shape = (M, N) if a.dim() == 2 else (*a.shape[:-1], N)
-    if out is None:
-        if out_dtype not in _DTYPES:
-            raise TypeError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
-        out = rows.new_empty(shape, dtype=out_dtype)
-    else:
-        _gpu(out, "out")
-        if out.device != a.device or tuple(out.shape) != shape or not out.is_contiguous():
-            raise ValueError(f"out must be contiguous, of shape {shape}, on {a.device}")
-    st = _lib.matmul_i8(M, N, K, rows.data_ptr(), lda, a_scale.data_ptr(), cols.data_ptr(), ldb,
-                        b_scale.data_ptr(), out.data_ptr(), N, _DTYPES[out.dtype], _stream_of(a))
-    if st:
-        _check("matmul_i8", st)
-    return out
-
-
-def _operand_ptr(t) -> int:
-    """_operand of a tensor or None, as an integer (0: absent)."""
-    if t is None:
-        return 0
-    return t.data_ptr() if t.numel() else _operand(t).value
-
-
-def _weight_codes(t, name, scale, width, rows=None):
-    """Codes [rows, width] of a weight, contiguous, and their scales."""
-    t, n, stride = _codes(t, name, 2)
-    if t.shape[1] != width or (rows is not None and n != rows):
-        raise ValueError(f"{name} must be codes [{'rows' if rows is None else rows}, {width}] "
-                         f"(got {tuple(t.shape)})")
-    if stride != width:
-        t = t.contiguous()
-    return t, _scales(scale, name + "_scale", n), n
-
-
-def _i8_weights(D_in, W_in, W_in_scale, W_out, W_out_scale, device):
-    """Checks the codes and scales of a layer; returns them with D_h and D_out."""
-    W_in, W_in_scale, n = _weight_codes(W_in, "W_in", W_in_scale, (D_in + 127) // 128 * 128)
-    if n % 2:
-        raise ValueError(f"W_in must have 2*D_h rows (got {n})")
-    D_h = D_out = n // 2
-    if (W_out is None) != (W_out_scale is None):
-        raise ValueError("W_out and W_out_scale go together")
-    if W_out is not None:
-        W_out, W_out_scale, D_out = _weight_codes(W_out, "W_out", W_out_scale, (D_h + 127) // 128 * 128)
-    _same_device(device, W_in=W_in, W_in_scale=W_in_scale, W_out=W_out, W_out_scale=W_out_scale)
-    return W_in, W_in_scale, W_out, W_out_scale, D_h, D_out
-
-
-def _state(t, name, B, D_h, device):
-    """A contiguous fp32 state [B, D_h] as it is."""
-    _gpu(t, name, torch.float32)
-    if t.dim() != 2 or t.shape[0] != B or t.shape[1] != D_h:
-        raise ValueError(f"{name} must have shape {(B, D_h)} (got {tuple(t.shape)})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on cuda:{device}")
-
-
-def _i8_workspace(workspace, nbytes, like):
-    if workspace is None:
-        return like.new_empty((max(nbytes, 1),), dtype=torch.uint8)
-    return _use_workspace(workspace, nbytes, like.device)
-
-
-def _optional_decay(decay_rate, delta_t, log1p_delta, saturated, D_h, gap_shape, device):
-    if decay_rate is None:
-        if delta_t is not None or saturated is not None:
-            raise ValueError("delta_t and saturated need decay_rate")
-        return None, None, 0, None
-    if delta_t is None:
-        raise ValueError("decay_rate and delta_t go together")
-    return _decay_args((decay_rate, delta_t, log1p_delta, saturated), D_h, gap_shape, device)
-
-
-def mingru_step_i8(x_t, W_in, W_in_scale, W_out=None, W_out_scale=None, h_prev=None, h_next=None,
-                   workspace=None, *, decay_rate=None, delta_t=None, log1p_delta=False,
-                   saturated=None):
-    """``mingru_step`` on 8-bit weights: x_t [B,D_in] fp32 or bf16 -> (y_t
-    [B,D_out] in x_t's type, h_t [B,D_h] fp32).
-
-    ``W_in`` and ``W_out`` are the codes of the layer's weights with their
-    scales (quantize_columns); x_t and the new state are quantised row by row
-    inside the call.  Without ``W_out`` the output is the new state (the same
-    tensor is returned twice).  ``decay_rate`` [D_h] with ``delta_t`` [B]: time
-    decay as in ``mingru_step_decayed``."""
-    _gpu(x_t, "x_t")
-    if x_t.dim() != 2:
-        raise ValueError(f"x_t must have 2 dims (got shape {tuple(x_t.shape)})")
-    if not x_t.is_contiguous():
-        x_t = x_t.contiguous()
-    B, D_in = x_t.shape
-    device = x_t.get_device()
-    W_in, W_in_scale, W_out, W_out_scale, D_h, D_out = _i8_weights(D_in, W_in, W_in_scale, W_out,
-                                                                   W_out_scale, device)
-    if h_prev is not None:
-        _state(h_prev, "h_prev", B, D_h, device)
-    if h_next is None:
-        h_next = x_t.new_empty((B, D_h), dtype=torch.float32)
-    else:
-        _state(h_next, "h_next", B, D_h, device)
-    y_t = None if W_out is None else x_t.new_empty((B, D_out))
-    rate, gap, log1p, sat = _optional_decay(decay_rate, delta_t, log1p_delta, saturated, D_h, (B,),
-                                            x_t.device if decay_rate is not None else None)
-    ws = _i8_workspace(workspace, _lib.mingru_step_i8_workspace_size(B, D_in, D_h, D_out), x_t)
-    st = _lib.mingru_step_i8(B, D_in, D_h, D_out, x_t.data_ptr(), _DTYPES[x_t.dtype],
-                             _operand_ptr(W_in), _operand_ptr(W_in_scale), _operand_ptr(W_out),
-                             _operand_ptr(W_out_scale), _ptr(rate), _ptr(gap), log1p, _ptr(sat),
-                             None if h_prev is None else h_prev.data_ptr(), h_next.data_ptr(),
-                             None if y_t is None else y_t.data_ptr(), ws.data_ptr(), ws.numel(),
-                             _stream_of(x_t))
-    if st:
-        _check("mingru_step_i8", st)
-    return (h_next if y_t is None else y_t), h_next
-
-
-def mingru_forward_i8(x, W_in, W_in_scale, W_out=None, W_out_scale=None, h0=None,
-                      return_last=False, workspace=None, *, decay_rate=None, delta_t=None,
-                      log1p_delta=False, saturated=None):
-    """``mingru_forward`` on 8-bit weights: x [B,T,D_in] fp32 or bf16 -> y
-    [B,T,D_out] in x's type (without ``W_out`` the states, in fp32), and h_T
-    [B,D_h] fp32 when ``return_last``.  Arguments as in ``mingru_step_i8``; the
-    gate logits and candidates reach the scan in x's type."""
-    _gpu(x, "x")
-    if x.dim() != 3:
-        raise ValueError(f"x must have 3 dims (got shape {tuple(x.shape)})")
-    x = x.contiguous()
-    B, T, D_in = x.shape
-    device = x.get_device()
-    W_in, W_in_scale, W_out, W_out_scale, D_h, D_out = _i8_weights(D_in, W_in, W_in_scale, W_out,
-                                                                   W_out_scale, device)
-    if h0 is not None:
-        h0 = h0.contiguous()
-        _state(h0, "h0", B, D_h, device)
-    y = x.new_empty((B, T, D_out), dtype=torch.float32 if W_out is None else x.dtype)
-    h_last = x.new_empty((B, D_h), dtype=torch.float32) if return_last else None
-    rate, gap, log1p, sat = _optional_decay(decay_rate, delta_t, log1p_delta, saturated, D_h, (B, T),
-                                            x.device)
-    nbytes = _lib.mingru_forward_i8_workspace_size(B, T, D_in, D_h, D_out, _DTYPES[x.dtype],
-                                                   int(W_out is not None))
-    ws = _i8_workspace(workspace, nbytes, x)
-    st = _lib.mingru_forward_i8(B, T, D_in, D_h, D_out, _ptr(x), _DTYPES[x.dtype],
-                                _operand_ptr(W_in), _operand_ptr(W_in_scale), _operand_ptr(W_out),
-                                _operand_ptr(W_out_scale), _ptr(rate), _ptr(gap), log1p, _ptr(sat),
-                                _ptr(h0), _ptr(y), _ptr(h_last), _ptr(ws), ws.numel(), _stream_of(x))
-    if st:
-        _check("mingru_forward_i8", st)
-    return (y, h_last) if return_last else y
-
-
 def adamw_state_elements(n: int) -> int:
     """Span of a tensor of n elements in the AdamW state buffers: n rounded up
     to a multiple of 256."""
     return _lib.adamw_state_elements(n)
-
-
-def adamw_step(params, grads, m, v, *, step, m_scale=None, v_scale=None, lr=1e-3,
-               betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, grad_scale=None):
-    """One AdamW step over many tensors, in place on ``params`` and the states.
-
-    ``params`` and ``grads``: lists of contiguous GPU tensors of the same
-    shapes, fp32 or bf16 each; a gradient may be None (that tensor is left as
-    it is).  ``step`` counts from 1.  ``m`` and ``v`` hold the states of all
-    tensors one after another, each tensor's span rounded up to 256 elements
-    (``adamw_state_elements``): fp32 without scales, or float8_e4m3fn codes (of
-    m and of sqrt(v)) with one fp32 scale for each 256 elements in ``m_scale``
-    and ``v_scale``.  Zeros are the states before the first step.
-    ``grad_scale``: an fp32 GPU scalar multiplied onto every gradient."""
-    if len(params) != len(grads):
-        raise ValueError(f"{len(params)} params but {len(grads)} grads")
-    if not params:
-        return
-    _gpu(params[0], "params[0]")
-    device = params[0].get_device()
-    eight = m_scale is not None or v_scale is not None
-    # Column by column over the lists: a few dozen tensors would otherwise
-    # spend more time here than on the GPU.
-    live, with_grad = [g for g in grads if g is not None], params
-    if len(live) < len(grads):
-        with_grad = [p for p, g in zip(params, grads) if g is not None]
-    for tensors, name in ((params, "params"), (live, "grads")):
-        if set(map(torch.Tensor.get_device, tensors)) - {device} \
-                or not all(map(torch.Tensor.is_contiguous, tensors)):
-            raise ValueError(f"{name} must be contiguous tensors on cuda:{device}")
-    if not all(map(torch.Tensor.is_same_size, with_grad, live)):
-        raise ValueError("each gradient must have its parameter's shape")
-    try:
-        kinds = [_DTYPES[p.dtype] for p in params]
-        live_kinds = [_DTYPES[g.dtype] << 32 for g in live]
-    except KeyError as e:
-        raise TypeError(f"params and grads must be float32 or bfloat16 (got {e.args[0]})") from None
-    live_ptrs = list(map(torch.Tensor.data_ptr, live))
-    if with_grad is not params:
-        ptrs, more = iter(live_ptrs), iter(live_kinds)
-        live_ptrs, live_kinds = ([0 if g is None else next(it) for g in grads] for it in (ptrs, more))
-    table = array.array("q", bytes(32 * len(params)))   # sr_adamw_tensor each
-    table[0::4] = array.array("q", map(torch.Tensor.data_ptr, params))
-    table[1::4] = array.array("q", live_ptrs)
-    table[2::4] = array.array("q", map(torch.Tensor.numel, params))
-    table[3::4] = array.array("q", map(operator.or_, kinds, live_kinds))
-    kind = torch.float8_e4m3fn if eight else torch.float32
-    for t, name, want in ((m, "m", kind), (v, "v", kind), (m_scale, "m_scale", torch.float32),
-                          (v_scale, "v_scale", torch.float32)):
-        if t is None and not eight:
-            continue
-        _gpu(t, name, want)
-        if t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 1-D tensor on cuda:{device}")
-    n = m.numel()
-    if v.numel() != n or (eight and not m_scale.numel() == v_scale.numel() == n // 256):
-        raise ValueError("m and v must have the same length, and m_scale and v_scale one scale for "
-                         "each 256 elements")
-    if grad_scale is not None:
-        _same_device(device, grad_scale=_scales(grad_scale, "grad_scale", 1))
-    st = _lib.adamw_step(len(params), table.buffer_info()[0], m.data_ptr(), v.data_ptr(), _ptr(m_scale),
-                         _ptr(v_scale), 8 if eight else 32, n, step, lr, betas[0], betas[1], eps,
-                         weight_decay, _ptr(grad_scale), _stream_of(m))
-    if st:
-        _check("adamw_step", st)
 
 
 def set_lookback_spin_limit(polls: int) -> None:

@@ -1,4 +1,5 @@
-"""Builds libscanrnn.so (HIP, gfx950) in the package directory.
+"""Builds libscanrnn.so (HIP, gfx950) and the compiled Python binding in the
+package directory.
 
     python scan_linear_rnn_amd/build.py        # or __graft_entry__.build()
 
@@ -6,7 +7,9 @@
 
 Every HIP source is compiled for gfx950 only, with packed-FP32 instruction
 generation switched off (-packed-fp32-ops), and linked into one shared
-library exporting the C ABI declared in include/scanrnn.h.
+library exporting the C ABI declared in include/scanrnn.h.  The binding
+(csrc/binding.cpp, host code against PyTorch's headers) is a Python extension
+module that is given the library's entry points when the package loads.
 
 build_host_sanitized(out_dir) makes a second copy whose HOST code (argument
 validation, sizing, launch set-up) is built with AddressSanitizer and
@@ -29,6 +32,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libscanrnn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = "gfx950"
 SOURCES = ["scan.hip", "scan_bwd.hip", "gemm.hip", "fused.hip", "noalloc.hip", "quant.hip",
@@ -65,10 +69,32 @@ def _compile(src: str, obj_dir: str = OBJ, extra=()) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    rocm = os.path.dirname(os.path.dirname(_hipcc()))
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+                os.path.join(rocm, "include"), INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-DTORCH_EXTENSION_NAME=_binding", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in includes), os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
+           *(f"-L{p}" for p in cpp_extension.library_paths()),
+           "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-ltorch"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
