@@ -684,18 +684,23 @@ sr_status mingru_step_i8(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out, co
   // Checked first, then launched (as in forward_impl).
   auto run = [&](bool check_only) -> sr_status {
     sr_status st2;
+    // Single tokens of a few streams: the products quantise their rows themselves.
+    const Tokens x{x_t, D_in, x_dtype}, h{h_next, D_h, SR_F32};
+    const Tokens* x_tokens = tokens_apply(B, D_in, x_t, x_dtype) ? &x : nullptr;
+    const Tokens* h_tokens = tokens_apply(B, D_h, h_next, SR_F32) ? &h : nullptr;
     if (D_h > 0) {
-      st2 = launch_quantize_rows(B, D_in, x_t, D_in, x_dtype, q, scale, s, check_only);
+      st2 = x_tokens ? SR_OK
+                     : launch_quantize_rows(B, D_in, x_t, D_in, x_dtype, q, scale, s, check_only);
       if (st2 != SR_OK) return st2;
       st2 = launch_step_i8(B, Ki, D_h, q, scale, W_in, W_in_scale, h_prev, h_next, s,
-                           dec.rate != nullptr ? &sd : nullptr, check_only);
+                           dec.rate != nullptr ? &sd : nullptr, check_only, x_tokens);
       if (st2 != SR_OK) return st2;
     }
     if (!w_out || D_out == 0) return SR_OK;
-    st2 = launch_quantize_rows(B, D_h, h_next, D_h, SR_F32, q, scale, s, check_only);
+    st2 = h_tokens ? SR_OK : launch_quantize_rows(B, D_h, h_next, D_h, SR_F32, q, scale, s, check_only);
     if (st2 != SR_OK) return st2;
     return launch_gemm_i8(B, D_out, Kh, q, Kh, scale, W_out, Kh, W_out_scale, y_t, D_out, x_dtype, s,
-                          check_only);
+                          check_only, h_tokens);
   };
   st = run(true);
   return st != SR_OK ? st : run(false);

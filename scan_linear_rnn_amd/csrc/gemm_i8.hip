@@ -18,10 +18,11 @@
 // i8_narrow_kernel  tiles of up to 64 x 64, the depth split over the waves:
 //                   products that 128 x 128 tiles would leave CUs without
 //                   (a step over up to a few hundred streams).
+// i8_token_kernel   the same for up to four rows that are not quantised yet.
 // i8_large_kernel   tiles of 128 x 128 and 256 x 256, persistent.
 
-#include "device_util.hpp"
 #include "internal.hpp"
+#include "quant.hpp"
 #include "step_gate.hpp"
 
 namespace sr {
@@ -30,8 +31,6 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 using rsrc_t = __amdgpu_buffer_rsrc_t;
 
 enum Out { kF32 = 0, kBF16 = 1, kStep = 2, kStepDecay = 3 };
@@ -54,6 +53,9 @@ struct I8Params {
   int64_t ldc;
   bool vec4, lines;      // rows of C start at multiples of 4 bytes, of 128 bytes
   uint32_t tiles_m, tiles_n, n_tiles;
+  // tokens: the rows of X are quantised by the kernel, A and a_scale are unused
+  const void* X;  // [M, Kx], contiguous
+  int Kx;
   // step: k and p are columns d and D_h + d
   int64_t D_h;
   const float* h_prev;
@@ -83,12 +85,18 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float scaled(int acc, float s, float t) { return float(acc) * (s * t); }
+// (Products here and in decayed() are rounded on their own, never joined with
+// a later sum: a row's results do not depend on the kernel that makes them.)
+__device__ __forceinline__ float scaled(int acc, float s, float t) {
+#pragma clang fp contract(off)
+  return float(acc) * (s * t);
+}
 
 // The states h entering the step at row m, four channels from d, of a tile
 // whose rows start at m0 (h: what was read of h_prev).  With time decay each
 // is scaled by exp(-min(rate gap, 1e4)).
 __device__ __forceinline__ f32x4 decayed(const I8Params& P, int64_t m, int64_t d, f32x4 h) {
+#pragma clang fp contract(off)
   if (m >= P.M) return h;
   constexpr float kClamp = 1.0e4f, kLog2e = 1.4426950408889634f;
   const float gap = P.log1p_gap ? log1pf(P.gap[m]) : P.gap[m];
@@ -313,6 +321,154 @@ __global__ __launch_bounds__(64 * kSplitWaves) void i8_narrow_kernel(const I8Par
     }
     store4<OUT>(P, m0 + pm[q], n0 + pn[q], v);
   }
+}
+
+// ------------------------------------------------------------------ tokens
+
+// Up to four rows (single tokens of a few streams) against 16 columns (step:
+// eight channels) per workgroup, where a launch of its own for the codes would
+// cost as much as the product.  Every weight is used by one wave only, so each
+// wave loads its share, every fourth 128-byte line, straight to registers, all
+// of it before anything else is done; meanwhile the workgroup quantises the
+// rows into LDS.  The codes are those of the quantisation kernels.  Bound by
+// the latency of the launch and of the weights, from D = 4096 by their bytes.
+// Measured (us, a step's state alone, D x 2 D weights from four alternating
+// buffers, one launch after the other):
+//   rows x D                    1 x 512  4 x 512  1 x 2048  4 x 2048  1 x 4096  4 x 4096
+//   codes, then their product     4.7      5.0      6.2       6.5      10.0      10.4
+//   this kernel                   3.2      3.1      4.6       5.1       8.3       9.8
+//   with 32 columns               3.4      3.3      6.2       6.8       8.6       9.7
+constexpr int kMaxTokens = 4;
+constexpr int kMaxTokenDepth = 4096;
+
+// DEPTH: the longest row.
+template <int OUT, typename TX, int DEPTH>
+__global__ __launch_bounds__(64 * kSplitWaves) void i8_token_kernel(const I8Params P) {
+  using C = Chunk<TX>;
+  constexpr int W = kSplitWaves, R = kMaxTokens, kLines = DEPTH / kDepth / W;
+  constexpr int kChunks = DEPTH / C::kSize / 64;  // of a row, for one wave's lanes
+  constexpr int kCols = is_step(OUT) ? 8 : 16;
+  constexpr int kPair = is_step(OUT) ? 2 : 1;
+  __shared__ __align__(16) int8_t s_codes[R * DEPTH];
+  __shared__ i32x4 s_sums[W * 64];
+  __shared__ uint32_t s_top[W];
+  __shared__ float s_scale[W];
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = int64_t(xcd_tile(gridDim.x)) * kCols;
+
+  // A row is quantised by four waves (one row), by two (two) or by one.  The
+  // lane's chunks of it, zeros past its end; loads end in order, so these come
+  // first.
+  const int wpr_log = P.M == 1 ? 2 : P.M == 2 ? 1 : 0;
+  const int row = wave >> wpr_log, c0 = ((wave & ((1 << wpr_log) - 1)) << 6) + lane;
+  const bool quantises = row < P.M;
+  const rsrc_t rx = buffer(static_cast<const TX*>(P.X) + int64_t(row) * P.Kx,
+                           quantises ? P.Kx * int(sizeof(TX)) : 0);
+  u32x4 x[kChunks];
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j)
+    x[j] = __builtin_amdgcn_raw_buffer_load_b128(rx, (c0 + (j << (6 + wpr_log))) * 16, 0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+
+  // This wave's weights: line i * W + wave; zeros for lines past the last.
+  // Step: eight rows of k, then the eight of p.
+  u32x4 b[kLines][2];
+  const int brow = is_step(OUT) && (lane & 8) ? int(P.D_h) + (lane & 7) : (lane & 15);
+  const int boff = int(uint32_t(brow) * uint32_t(P.ldb)) + g * 16;
+  const int64_t b_bytes = (P.N - n0 - 1) * P.ldb + P.K;
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) {
+    const int k = (i * W + wave) * kDepth;
+    const rsrc_t rb = buffer(P.B + n0 * P.ldb, k < P.K ? b_bytes : 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) b[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, boff, k + h * 64, 0);
+  }
+  // Scales and states of the results this lane finishes: row m, four columns from n.
+  const int m = lane & 15;
+  const int64_t n = n0 + (is_step(OUT) ? g % 2 : g) * 4;
+  f32x4 sb[kPair], hp{};
+  const rsrc_t rt = buffer(P.b_scale + n0, (P.N - n0) * 4);
+#pragma unroll
+  for (int h = 0; h < kPair; ++h) sb[h] = load4(rt, int(n - n0 + h * P.D_h) * 4);
+  if (is_step(OUT) && P.h_prev != nullptr)
+    hp = load4(buffer(P.h_prev + n0, (P.M * P.D_h - n0) * 4), int(m * P.D_h + n - n0) * 4);
+  __builtin_amdgcn_sched_barrier(0);
+
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) {
+    const uint32_t t = C::top(x[j]);
+    top = top > t ? top : t;
+  }
+  top = wave_max(top);
+  if (lane == 0) s_top[wave] = top;
+  __syncthreads();
+  if (quantises) {
+    for (int w = 1; w < 1 << wpr_log; ++w) {
+      const uint32_t t = s_top[wave ^ w];
+      top = top > t ? top : t;
+    }
+    const float s = row_scale(top);
+    if (lane == 0) s_scale[row] = s;
+    const bool plain = divides_plainly(s);
+    const float rs = plain ? __fdiv_rn(1.0f, s) : 0.0f;
+    // 128 bytes of a line a row, row r's 16-byte chunk c at c ^ 4 (r / 2), so
+    // that the halves of four rows lie in different banks.
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int k = (c0 + (j << (6 + wpr_log))) * C::kSize;
+      if (((j * 64) << wpr_log) * C::kSize < P.K) {
+        uint32_t c[C::kSize / 4];
+        C::codes(x[j], s, rs, plain, c);
+        if (k < P.K) {
+          int8_t* at = s_codes + (k / kDepth * R + row) * kDepth + (((k % kDepth / 16) ^ (row / 2 * 4)) << 4) + k % 16;
+#pragma unroll
+          for (int d = 0; d < C::kSize / 4; ++d) reinterpret_cast<uint32_t*>(at)[d] = c[d];
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  // The tile's 16 rows are the four over and over; only the first M are stored.
+  i32x4 acc{};
+  const int arow = lane % R;
+  const float s_row = s_scale[arow];
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) {
+    const int line = i * W + wave;
+    if (line * kDepth < P.K) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const i32x4 a = *reinterpret_cast<const i32x4*>(s_codes + (line * R + arow) * kDepth +
+                                                        (((h * 4 + g) ^ (arow / 2 * 4)) << 4));
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4(b[i][h]), a, acc, 0, 0, 0);
+      }
+    }
+  }
+  s_sums[threadIdx.x] = acc;
+  __syncthreads();
+  if (wave > 0 || m >= P.M || g >= 4 / kPair) return;
+  i32x4 sum[kPair];  // step: k's, and p's from the lanes 32 on
+#pragma unroll
+  for (int h = 0; h < kPair; ++h) {
+    const i32x4* from = s_sums + lane + h * 32;
+    sum[h] = from[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum[h] += from[w * 64];
+  }
+  f32x4 v;
+  if constexpr (is_step(OUT)) {
+    if constexpr (OUT == kStepDecay) hp = decayed(P, m, n, hp);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      v[r] = step_value(scaled(sum[0][r], s_row, sb[0][r]), scaled(sum[1][r], s_row, sb[1][r]), hp[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = scaled(sum[0][r], s_row, sb[0][r]);
+  }
+  store4<OUT>(P, m, n, v);
 }
 
 // ------------------------------------------------------------- large product
@@ -759,6 +915,29 @@ void large(I8Params& P, hipStream_t stream) {
                      dim3(64 * S::kWaves), 0, stream, P);
 }
 
+// What the kernels' 32-bit offsets and one launch's grid allow.
+template <int OUT>
+sr_status check_sizes(const I8Params& P) {
+  const int64_t n = is_step(OUT) ? 2 * P.D_h : P.N;
+  if (P.M > kMaxBlocks256 || n > kMaxBlocks256 || ((P.M + 127) / 128) * ((n + 127) / 128) > kMaxBlocks256)
+    return fail(SR_ERR_UNSUPPORTED, "8-bit product of %lld x %lld results too large for one launch",
+                (long long)P.M, (long long)n);
+  constexpr int64_t kMaxStride = int64_t(1) << 23;
+  if (P.lda > kMaxStride || P.ldb > kMaxStride)
+    return fail(SR_ERR_UNSUPPORTED, "rows of codes %lld bytes apart are too far apart",
+                (long long)(P.lda > P.ldb ? P.lda : P.ldb));
+  if (is_step(OUT) && (P.D_h > kMaxStride / 2 || n * P.ldb > int64_t(0xFFFFFFFF)))
+    return fail(SR_ERR_UNSUPPORTED, "8-bit weights of %lld x %lld are too large for a step",
+                (long long)n, (long long)P.ldb);
+  return SR_OK;
+}
+
+sr_status launched() {
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return fail(SR_ERR_HIP, "8-bit product launch: %s", hipGetErrorString(err));
+  return SR_OK;
+}
+
 // Which kernel.  Measured in us (one launch in a replayed graph, weights from
 // four alternating buffers; narrow 64 x 64 / 32 x 32 / 16 x 32, deep and
 // persistent 128 x 128, 256 x 256):
@@ -778,20 +957,10 @@ void large(I8Params& P, hipStream_t stream) {
 // round alone only with a depth that carries it).
 template <int OUT>
 sr_status launch(I8Params P, hipStream_t stream, bool check_only) {
+  const sr_status st = check_sizes<OUT>(P);
+  if (st != SR_OK || check_only) return st;
   const int64_t n = is_step(OUT) ? 2 * P.D_h : P.N;
   auto tiles = [&](int64_t rows, int64_t cols) { return ((P.M + rows - 1) / rows) * ((n + cols - 1) / cols); };
-  if (P.M > kMaxBlocks256 || n > kMaxBlocks256 || tiles(128, 128) > kMaxBlocks256)
-    return fail(SR_ERR_UNSUPPORTED, "8-bit product of %lld x %lld results too large for one launch",
-                (long long)P.M, (long long)n);
-  // Offsets within a tile are 32-bit.
-  constexpr int64_t kMaxStride = int64_t(1) << 23;
-  if (P.lda > kMaxStride || P.ldb > kMaxStride)
-    return fail(SR_ERR_UNSUPPORTED, "rows of codes %lld bytes apart are too far apart",
-                (long long)(P.lda > P.ldb ? P.lda : P.ldb));
-  if (is_step(OUT) && (P.D_h > kMaxStride / 2 || n * P.ldb > int64_t(0xFFFFFFFF)))
-    return fail(SR_ERR_UNSUPPORTED, "8-bit weights of %lld x %lld are too large for a step",
-                (long long)n, (long long)P.ldb);
-  if (check_only) return SR_OK;
   const int64_t t128 = tiles(128, 128), t256 = tiles(256, 256);
   const int64_t rounds128 = (t128 + 2 * kCus - 1) / (2 * kCus), rounds256 = (t256 + kCus - 1) / kCus;
   if (P.K > 0 && t128 >= kCus / 2) {
@@ -808,19 +977,46 @@ sr_status launch(I8Params P, hipStream_t stream, bool check_only) {
   } else {
     narrow<OUT, 1, 2>(P, stream);
   }
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(SR_ERR_HIP, "8-bit product launch: %s", hipGetErrorString(err));
-  return SR_OK;
+  return launched();
+}
+
+template <int OUT>
+sr_status launch_tokens(I8Params P, const Tokens& x, hipStream_t stream, bool check_only) {
+  P.X = x.x;
+  P.Kx = int(x.K);
+  const sr_status st = check_sizes<OUT>(P);
+  if (st != SR_OK || check_only) return st;
+  set_tiles<OUT>(P, 16, 16);
+  const dim3 grid{P.n_tiles}, block{64 * kSplitWaves};
+  auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, P); };
+  const bool shallow = P.K <= kMaxTokenDepth / 4;
+  if constexpr (is_step(OUT)) {  // the rows of a product are states, in fp32
+    if (x.dtype == SR_BF16) {
+      shallow ? run(i8_token_kernel<OUT, uint16_t, kMaxTokenDepth / 4>)
+              : run(i8_token_kernel<OUT, uint16_t, kMaxTokenDepth>);
+      return launched();
+    }
+  }
+  shallow ? run(i8_token_kernel<OUT, float, kMaxTokenDepth / 4>)
+          : run(i8_token_kernel<OUT, float, kMaxTokenDepth>);
+  return launched();
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
 
+// Whether the rows are few and short enough for the token kernel, and made of
+// whole dwords.
+bool tokens_apply(int64_t M, int64_t K, const void* x, sr_dtype dtype) {
+  return M <= kMaxTokens && K > 0 && K <= kMaxTokenDepth &&
+         aligned(x, 4) && (dtype == SR_F32 || K % 2 == 0);
+}
+
 sr_status launch_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,
                          const float* a_scale, const int8_t* B, int64_t ldb, const float* b_scale,
                          void* C, int64_t ldc, sr_dtype c_dtype, hipStream_t stream,
-                         bool check_only) {
+                         bool check_only, const Tokens* tokens) {
   if (M == 0 || N == 0) return SR_OK;
   I8Params P{};
   P.M = M; P.N = N; P.K = K;
@@ -830,13 +1026,16 @@ sr_status launch_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64
   const int64_t row_bytes = ldc * (c_dtype == SR_BF16 ? 2 : 4);
   P.vec4 = row_bytes % 4 == 0 && aligned(C, 4);
   P.lines = row_bytes % 128 == 0 && aligned(C, 128);
+  if (tokens != nullptr)
+    return c_dtype == SR_BF16 ? launch_tokens<kBF16>(P, *tokens, stream, check_only)
+                              : launch_tokens<kF32>(P, *tokens, stream, check_only);
   return c_dtype == SR_BF16 ? launch<kBF16>(P, stream, check_only) : launch<kF32>(P, stream, check_only);
 }
 
 sr_status launch_step_i8(int64_t Bsz, int64_t K, int64_t D_h, const int8_t* x, const float* x_scale,
                          const int8_t* W_in, const float* w_scale, const float* h_prev,
                          float* h_next, hipStream_t stream, const StepDecay* decay,
-                         bool check_only) {
+                         bool check_only, const Tokens* tokens) {
   if (Bsz == 0 || D_h == 0) return SR_OK;
   I8Params P{};
   P.M = Bsz; P.N = 2 * D_h; P.K = K;
@@ -849,6 +1048,9 @@ sr_status launch_step_i8(int64_t Bsz, int64_t K, int64_t D_h, const int8_t* x, c
     P.log1p_gap = decay->log1p_gap;
     P.saturated = decay->saturated;
   }
+  if (tokens != nullptr)
+    return decay != nullptr ? launch_tokens<kStepDecay>(P, *tokens, stream, check_only)
+                            : launch_tokens<kStep>(P, *tokens, stream, check_only);
   return decay != nullptr ? launch<kStepDecay>(P, stream, check_only) : launch<kStep>(P, stream, check_only);
 }
 

@@ -173,19 +173,28 @@ sr_status launch_quantize_rows(int64_t M, int64_t K, const void* x, int64_t ldx,
 sr_status launch_quantize_columns(int64_t K, int64_t N, const void* W, int64_t ldw, sr_dtype dtype,
                                   int8_t* q, float* scale, hipStream_t stream);
 
+// Rows that a product quantises itself, instead of codes and scales in A and
+// a_scale: at most a few, contiguous (see tokens_apply).
+struct Tokens {
+  const void* x;  // [M, K]
+  int64_t K;
+  sr_dtype dtype;
+};
+bool tokens_apply(int64_t M, int64_t K, const void* x, sr_dtype dtype);
+
 // C[M,N] = (A B^T) a_scale b_scale over codes A [M,K], B [N,K] (K a multiple
 // of kI8Align, rows 16-byte aligned).
 sr_status launch_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,
                          const float* a_scale, const int8_t* B, int64_t ldb, const float* b_scale,
                          void* C, int64_t ldc, sr_dtype c_dtype, hipStream_t stream,
-                         bool check_only = false);
+                         bool check_only = false, const Tokens* tokens = nullptr);
 
 // The step on codes: [k|p] = the product of x [Bsz,K] and W_in [2 D_h, K],
 // h_next as in launch_step_in.
 sr_status launch_step_i8(int64_t Bsz, int64_t K, int64_t D_h, const int8_t* x, const float* x_scale,
                          const int8_t* W_in, const float* w_scale, const float* h_prev,
                          float* h_next, hipStream_t stream, const StepDecay* decay,
-                         bool check_only = false);
+                         bool check_only = false, const Tokens* tokens = nullptr);
 
 // ---------------------------------------------------------------- AdamW
 

@@ -14,39 +14,14 @@
 // codes: the product then reads whole 128-byte lines, and the zeros add
 // nothing to its integer sums.
 
-#include "device_util.hpp"
 #include "internal.hpp"
+#include "quant.hpp"
 
 namespace sr {
 namespace {
 
 __device__ __forceinline__ float load_f32(const float* p) { return *p; }
 __device__ __forceinline__ float load_f32(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
-
-// The scale of a row whose largest magnitude has the bits `top`.
-__device__ __forceinline__ float row_scale(uint32_t top) {
-  return top < kF32InfBits ? __fdiv_rn(__uint_as_float(top), 127.0f) : __uint_as_float(0x7FC00000u);
-}
-
-// One code as a byte; `live` says that s is finite and above zero.
-__device__ __forceinline__ uint32_t code(float x, float s, bool live) {
-  const float q = rintf(__fdiv_rn(x, s));
-  const int c = int(fminf(fmaxf(q, -127.0f), 127.0f));
-  return live ? uint32_t(c) & 0xFFu : 0u;
-}
-
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-
-// Elements of a 16-byte chunk, and the largest magnitude of one.
-template <typename T>
-struct Chunk {
-  static constexpr int kSize = 16 / sizeof(T);
-  static __device__ __forceinline__ float get(u32x4 w, int e) {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
-    return __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-  }
-};
 
 // WPR waves per row, NV 16-byte chunks per lane: the row is read once and
 // stays in registers.  Loads go through a descriptor that ends with the row,
@@ -79,11 +54,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t 
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-#pragma unroll
-    for (int e = 0; e < C::kSize; ++e) {
-      const uint32_t b = abs_bits(C::get(w[j], e));
-      top = top > b ? top : b;
-    }
+    const uint32_t t = C::top(w[j]);
+    top = top > t ? top : t;
   }
   top = wave_max(top);
   if constexpr (WPR == 4) {
@@ -93,36 +65,15 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t 
     for (int v = 0; v < 4; ++v) top = top > s_top[v] ? top : s_top[v];
   }
   const float s = row_scale(top);
-  const bool live = s > 0.0f;
   if (c0 == 0) scale[row] = s;
   int8_t* dst = q + row * int64_t(Kp);
-  // The quotients of the two paths are the same numbers.
   const bool plain = divides_plainly(s);
   const float r = plain ? __fdiv_rn(1.0f, s) : 0.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int k = (c0 + j * 64 * WPR) * C::kSize;
     uint32_t codes[C::kSize / 4];
-    if (plain) {
-#pragma unroll
-      for (int d = 0; d < C::kSize / 4; ++d) {
-        uint32_t v = 0;
-#pragma unroll
-        for (int e = 3; e >= 0; --e) {
-          // |x| <= 127 s (1 + 2^-24), so the quotient rounds to 127 at most.
-          const int c = int(rintf(divided(C::get(w[j], d * 4 + e), s, r)));
-          v = (v << 8) | (uint32_t(c) & 0xFFu);
-        }
-        codes[d] = v;
-      }
-    } else {
-#pragma unroll
-      for (int d = 0; d < C::kSize / 4; ++d) {
-        codes[d] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) codes[d] |= code(C::get(w[j], d * 4 + e), s, live) << (8 * e);
-      }
-    }
+    C::codes(w[j], s, r, plain, codes);
     if (k < Kp) {
       if constexpr (C::kSize == 8)
         __builtin_nontemporal_store(u32x2{codes[0], codes[1]}, reinterpret_cast<u32x2*>(dst + k));

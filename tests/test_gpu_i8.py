@@ -298,6 +298,54 @@ def test_step(B, D_in, D_h, D_out, dtype):
     assert torch.equal(z, sr.mingru_step_i8(x, *wi, h_prev=torch.zeros_like(h))[0])
 
 
+@pytest.mark.parametrize("B,D_in,D_h,D_out", [(1, 1, 1, 1), (2, 129, 100, 33), (3, 1000, 1023, 64), (4, 1024, 1025, 130),
+                                              (4, 1030, 2048, 1000), (1, 2048, 4095, 17), (2, 4096, 4097, 96),
+                                              (3, 4100, 64, 4100)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_step_of_few_tokens_equals_quantising_first(B, D_in, D_h, D_out, dtype):
+    """Bit for bit: the same rows in a batch of more, and the output's product
+    on codes of the state made by quantize_rows."""
+    say(f"i8 tokens B={B} {D_in}->{D_h}->{D_out} {dtype}")
+    rng = np.random.default_rng([3205, B, D_in, D_h])
+    W_in, W_out = _layer(rng, D_in, D_h, D_out)
+    wi, wo = sr.quantize_columns(dev(W_in)), sr.quantize_columns(dev(W_out))
+    rows = _activations(rng, 21, D_in)
+    rows[0] *= 1e-33      # a scale that takes the slow division
+    h0 = rng.standard_normal((21, D_h)).astype(np.float32)
+    decay = dict(decay_rate=dev(rng.uniform(0, 0.5, D_h).astype(np.float32)))
+    gap = dev(rng.exponential(2.0, 21).astype(np.float32))
+    for kw, gaps in ((dict(), None), (decay, gap)):
+        if gaps is not None:
+            kw = dict(kw, delta_t=gaps)
+        many = sr.mingru_step_i8(dev(rows, dtype), *wi, h_prev=dev(h0), **kw)[0]
+        if gaps is not None:
+            kw = dict(kw, delta_t=gaps[:B])
+        y, h = sr.mingru_step_i8(dev(rows[:B], dtype), *wi, *wo, h_prev=dev(h0[:B]), **kw)
+        assert torch.equal(h, many[:B])
+        assert torch.equal(y, sr.matmul_i8(*sr.quantize_rows(h), *wo, out_dtype=dtype))
+    # a start of the rows that no dword begins at (bf16), and sums past a tile's rows
+    held = torch.zeros(B * D_in + 1, device="cuda", dtype=dtype)
+    held[1:] = dev(rows[:B], dtype).reshape(-1)
+    h = sr.mingru_step_i8(held[1:].view(B, D_in), *wi, h_prev=dev(h0[:B]))[0]
+    assert torch.equal(h, sr.mingru_step_i8(dev(rows, dtype), *wi, h_prev=dev(h0))[0][:B])
+
+
+def test_few_tokens_with_empty_and_not_finite_rows():
+    say("i8 tokens special rows")
+    rng = np.random.default_rng(3206)
+    D = 200
+    W_in, W_out = _layer(rng, D, D, D)
+    wi, wo = sr.quantize_columns(dev(W_in)), sr.quantize_columns(dev(W_out))
+    x = _activations(rng, 4, D)
+    x[0], x[1, 7], x[2, 199] = 0, np.nan, -np.inf
+    h0 = np.zeros((4, D), np.float32)
+    h0[3, 5] = np.nan
+    y, h = sr.mingru_step_i8(dev(x), *wi, *wo, h_prev=dev(h0))
+    assert torch.isfinite(h[0]).all() and torch.isnan(h[1:3]).all()
+    assert torch.isnan(h[3, 5]) and torch.isfinite(h[3, :5]).all()
+    assert torch.isfinite(y[0]).all() and torch.isnan(y[1:]).all()
+
+
 def test_step_with_time_decay():
     say("i8 step with decay")
     rng = np.random.default_rng(3210)
