@@ -92,24 +92,27 @@ __device__ __forceinline__ float scaled(int acc, float s, float t) {
   return float(acc) * (s * t);
 }
 
-// The states h entering the step at row m, four channels from d, of a tile
-// whose rows start at m0 (h: what was read of h_prev).  With time decay each
-// is scaled by exp(-min(rate gap, 1e4)).
-__device__ __forceinline__ f32x4 decayed(const I8Params& P, int64_t m, int64_t d, f32x4 h) {
+// The states h entering the step at four channels whose decay rates are rate
+// (zero past the last), of a row with this time gap: with time decay each is
+// scaled by exp(-min(rate gap, 1e4)).
+__device__ __forceinline__ f32x4 decayed(const I8Params& P, float gap, f32x4 rate, f32x4 h) {
 #pragma clang fp contract(off)
-  if (m >= P.M) return h;
   constexpr float kClamp = 1.0e4f, kLog2e = 1.4426950408889634f;
-  const float gap = P.log1p_gap ? log1pf(P.gap[m]) : P.gap[m];
+  if (P.log1p_gap) gap = log1pf(gap);
   bool saturated = false;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const float e = d + r < P.D_h ? P.rate[d + r] * gap : 0.0f;
+    const float e = rate[r] * gap;
     saturated |= e > kClamp;
     h[r] *= __builtin_amdgcn_exp2f(fminf(e, kClamp) * -kLog2e);
   }
   if (saturated && P.saturated != nullptr)
     __hip_atomic_fetch_or(P.saturated, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return h;
+}
+// The same of row m < M, channels from d.
+__device__ __forceinline__ f32x4 decayed(const I8Params& P, int64_t m, int64_t d, f32x4 h) {
+  return decayed(P, P.gap[m], load4(buffer(P.rate, P.D_h * 4), int(d) * 4), h);
 }
 
 // Four consecutive results of row m from column n (step: channel n).
@@ -311,7 +314,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void i8_narrow_kernel(const I8Par
     }
     f32x4 v;
     if constexpr (is_step(OUT)) {
-      if constexpr (OUT == kStepDecay) hp[q] = decayed(P, m0 + pm[q], n0 + pn[q], hp[q]);
+      if constexpr (OUT == kStepDecay)
+        if (m0 + pm[q] < P.M) hp[q] = decayed(P, m0 + pm[q], n0 + pn[q], hp[q]);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         v[r] = step_value(scaled(sum[0][r], sa[q], sb[q][0][r]), scaled(sum[1][r], sa[q], sb[q][1][r]), hp[q][r]);
@@ -492,7 +496,6 @@ struct LargeShape {
   static constexpr int kOutBytes = R * kOutRow;  // per wave
   static constexpr int kLds = 2 * kStageBytes + kWaves * kOutBytes;
   static constexpr int kPerCu = 160 * 1024 / kLds;
-  static constexpr int kDeepLds = 4 * kStageBytes + kWaves * kOutBytes;
   static_assert(kWaves == 4, "the order of the loads");
 };
 
@@ -609,38 +612,95 @@ struct LargeTile {
     aim(next);
     stage(p0, p1, 0);
     stage(p1, p0, 1);
-    if constexpr (is_step(OUT))
-      update(tile);
-    else
+    if constexpr (is_step(OUT)) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          States<1, 1> st;
+          load_states(st, tile, i, j);
+          update(out, st, i, j);
+        }
+    } else {
       store(out, tile);
+    }
   }
-  __device__ __forceinline__ void update(uint32_t tile) {
+  // What the states of a step come from, but the sums: h_prev, scales (and
+  // decay) of MBP x NBP blocks of 32 rows x 16 channels from block (i, j) on, for
+  // one row and four channels per lane and iteration, a row's by lanes side by
+  // side.
+  template <int MBP, int NBP>
+  struct States {
+    static constexpr int kPerRow = 4 * NBP, kRows = 64 / kPerRow, kIts = MBP * R / kRows;
+    int64_t m, n;  // of this lane's first row and channel
+    f32x4 h[kIts], tk, tp, rate;
+    float s[kIts], gap[kIts];
+  };
+  template <int MBP, int NBP>
+  __device__ __forceinline__ void load_states(States<MBP, NBP>& st, uint32_t tile, int i, int j) const {
+    using St = States<MBP, NBP>;
     int64_t m0, n0;
     origin(tile, m0, n0);
-    m0 += wm * (MB * R);
-    n0 += wn * (NB * R / 2);
-    const rsrc_t rs = buffer(P.a_scale + m0, (P.M - m0) * 4);
-    const rsrc_t rt = buffer(P.b_scale + n0, (P.N - n0) * 4);
+    m0 += wm * (MB * R) + i * R;
+    n0 += wn * (NB * R / 2) + j * 16;
+    const int r = lane / St::kPerRow, c = lane % St::kPerRow * 4;
+    st.m = m0 + r;
+    st.n = n0 + c;
+    const rsrc_t rs = buffer(P.a_scale + m0, (P.M - m0) * 4), rt = buffer(P.b_scale + n0, (P.N - n0) * 4);
+    const rsrc_t rh = buffer(P.h_prev + m0 * P.D_h + n0, P.h_prev == nullptr ? 0 : ((P.M - m0) * P.D_h - n0) * 4);
+    st.tk = load4(rt, c * 4);
+    st.tp = load4(rt, (c + int(P.D_h)) * 4);
+    if constexpr (OUT == kStepDecay) st.rate = load4(buffer(P.rate + n0, (P.D_h - n0) * 4), c * 4);
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int64_t m = m0 + i * R + lane % R;
-      const float s = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (i * R + lane % R) * 4, 0, 0));
+    for (int it = 0; it < St::kIts; ++it) {
+      const int row = r + it * St::kRows;
+      st.h[it] = load4(rh, int(uint32_t(row) * uint32_t(P.D_h) + uint32_t(c)) * 4);
+      st.s[it] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, row * 4, 0, 0));
+      if constexpr (OUT == kStepDecay)
+        st.gap[it] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(buffer(P.gap + m0, (P.M - m0) * 4), row * 4, 0, 0));
+    }
+  }
+  // The new states of those blocks.  The sums pass through LDS, a block's k and
+  // p side by side in 128 bytes a row, so that the gates are one short loop and
+  // a row's states are stored by lanes side by side: unrolled over the sums'
+  // registers they were 16 KB of instructions (1024 x 2048: 24.3 -> 22.7 us with
+  // its quantisation).  A gate is 24 instructions, four of them transcendental:
+  // 2 us per tile of 128 x 128.  Place c ^ row % 8 of a row holds its 16-byte
+  // chunk c.
+  template <int MBP, int NBP>
+  __device__ __forceinline__ void update(int8_t* __restrict__ out, States<MBP, NBP>& st, int i, int j) {
+    using St = States<MBP, NBP>;
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
+    for (int ii = 0; ii < MBP; ++ii)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int in = j * 16 + 8 * g + 4 * (lane / R);
-          const f32x4 tk = load4(rt, in * 4), tp = load4(rt, (in + int(P.D_h)) * 4);
-          const int64_t d = n0 + in;
-          f32x4 h{}, v;
-          if (P.h_prev != nullptr && m < P.M) h = load4(buffer(P.h_prev + m0 * P.D_h, (P.M - m0) * P.D_h * 4),
-                                                        int(uint32_t((m - m0) * P.D_h + d) * 4u));
-          if constexpr (OUT == kStepDecay) h = decayed(P, m, d, h);
+      for (int jj = 0; jj < NBP; ++jj)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            v[r] = step_value(scaled(acc[i][j][4 * g + r], s, tk[r]), scaled(acc[i][j][4 * (g + 2) + r], s, tp[r]), h[r]);
-          store4<OUT>(P, m, d, v);
+        for (int g = 0; g < 4; ++g) {
+          const int row = lane % R, chunk = 2 * g + lane / R;
+          const i32x16& a = acc[i + ii][j + jj];
+          *reinterpret_cast<i32x4*>(out + ((ii * NBP + jj) * R + row) * 128 + ((chunk ^ (row & 7)) << 4)) =
+              i32x4{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
         }
+    const int jj = lane % St::kPerRow / 4, chunk = lane % 4;
+#pragma unroll 1
+    for (int it = 0; it < St::kIts; ++it) {
+      const int by = it * St::kRows, r = lane / St::kPerRow + by, row = r % R;
+      const int8_t* from = out + ((r / R * NBP + jj) * R + row) * 128;
+      const i32x4 k = *reinterpret_cast<const i32x4*>(from + ((chunk ^ (row & 7)) << 4));
+      const i32x4 p = *reinterpret_cast<const i32x4*>(from + (((chunk + 4) ^ (row & 7)) << 4));
+      f32x4 h = st.h[0], v;
+      if constexpr (OUT == kStepDecay)
+        if (st.m + by < P.M) h = decayed(P, st.gap[0], st.rate, h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = step_value(scaled(k[e], st.s[0], st.tk[e]), scaled(p[e], st.s[0], st.tp[e]), h[e]);
+      store4<OUT>(P, st.m + by, st.n, v);
+#pragma unroll
+      for (int q = 0; q + 1 < St::kIts; ++q) {
+        st.h[q] = st.h[q + 1];
+        st.s[q] = st.s[q + 1];
+        if constexpr (OUT == kStepDecay) st.gap[q] = st.gap[q + 1];
       }
     }
   }
@@ -847,12 +907,13 @@ struct DeepTile : LargeTile<OUT, S> {
     }
   }
   __device__ __forceinline__ void run(int8_t* __restrict__ p0, int8_t* __restrict__ p1,
-                                      int8_t* __restrict__ p2, int8_t* __restrict__ p3,
-                                      int8_t* __restrict__ out, uint32_t n, uint32_t tile) {
+                                      int8_t* __restrict__ p2, int8_t* __restrict__ p3, uint32_t n,
+                                      typename T::template States<S::MB, S::NB>& st, uint32_t tile) {
     T::load_stage(p0, 0);
     if (n > 1) T::load_stage(p1, 1);
     if (n > 2) T::load_stage(p2, 2);
     if (n > 3) T::load_stage(p3, 3);
+    if constexpr (is_step(OUT)) T::load_states(st, tile, 0, 0);
     wait_oldest(n - 1);
     read_stage(0, p0);
     for (uint32_t s = 0; s < n; s += 4) {
@@ -861,16 +922,15 @@ struct DeepTile : LargeTile<OUT, S> {
       if (s + 2 < n) stage<0>(p2, p3, s + 2, n);
       if (s + 3 < n) stage<1>(p3, p0, s + 3, n);
     }
-    if constexpr (is_step(OUT))
-      T::update(tile);
-    else
-      T::store(out, tile);
   }
 };
 
 template <int OUT, class S>
 __global__ __launch_bounds__(64 * S::kWaves, 1) void i8_deep_kernel(const I8Params P) {
-  __shared__ __align__(1024) int8_t smem[S::kDeepLds];
+  // A wave's sums (step) or its results of 32 rows at a time, where the stages were.
+  constexpr int kOut = is_step(OUT) ? S::MB * S::NB * S::R * 128 : S::kOutBytes;
+  static_assert(S::kWaves * kOut <= 4 * S::kStageBytes);
+  __shared__ __align__(1024) int8_t smem[4 * S::kStageBytes];
   const uint32_t tile = xcd_tile(gridDim.x);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -881,8 +941,14 @@ __global__ __launch_bounds__(64 * S::kWaves, 1) void i8_deep_kernel(const I8Para
   for (int i = 0; i < S::MB; ++i)
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) T.acc[i][j] = i32x16{};
-  T.run(smem, smem + S::kStageBytes, smem + 2 * S::kStageBytes, smem + 3 * S::kStageBytes,
-        smem + 4 * S::kStageBytes + wave * S::kOutBytes, uint32_t(P.K / kDepth), tile);
+  typename LargeTile<OUT, S>::template States<S::MB, S::NB> st;
+  T.run(smem, smem + S::kStageBytes, smem + 2 * S::kStageBytes, smem + 3 * S::kStageBytes, uint32_t(P.K / kDepth), st,
+        tile);
+  __syncthreads();  // every wave has read the last stage
+  if constexpr (is_step(OUT))
+    T.update(smem + wave * kOut, st, 0, 0);
+  else
+    T.store(smem + wave * kOut, tile);
 }
 
 template <int OUT>
@@ -950,8 +1016,10 @@ sr_status launched() {
 //   8192 x 1024 x 2048  70.4      -      -  37.9     30.9     28.6
 //   20000 x 2048 x 1000    -      -      -     -     57.4     66.7
 //   131072 x 512 x 1024    -      -      -     -      210      166
-// So: 128 x 128 tiles from half as many as there are CUs, in the deep form
-// while a CU has one at most; below that the largest narrow tile that still
+// So: 128 x 128 tiles from half as many as there are CUs (a step, whose gates
+// want every CU: from one more; 512 streams, D = 2048, with their quantisation
+// 19.0 us deep, 17.6 narrow; 640: 19.7, 23.9), in the deep form while a CU has
+// one at most; below that the largest narrow tile that still
 // gives every CU one.  256 x 256 tiles do an area's work in about 5/6 of the
 // time, so they are taken where they need at most 6/5 of the rounds (one
 // round alone only with a depth that carries it).
@@ -963,7 +1031,7 @@ sr_status launch(I8Params P, hipStream_t stream, bool check_only) {
   auto tiles = [&](int64_t rows, int64_t cols) { return ((P.M + rows - 1) / rows) * ((n + cols - 1) / cols); };
   const int64_t t128 = tiles(128, 128), t256 = tiles(256, 256);
   const int64_t rounds128 = (t128 + 2 * kCus - 1) / (2 * kCus), rounds256 = (t256 + kCus - 1) / kCus;
-  if (P.K > 0 && t128 >= kCus / 2) {
+  if (P.K > 0 && t128 >= kCus / 2 + is_step(OUT)) {
     if (t128 <= kCus)
       deep<OUT>(P, stream);
     else if (!is_step(OUT) && 5 * rounds256 <= 3 * rounds128 && (rounds256 > 1 || P.K >= 1024))

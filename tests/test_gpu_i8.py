@@ -370,6 +370,30 @@ def test_step_with_time_decay():
         _h_close(h_log, *_gates(x, W_in, D), h0, np.exp(-rate.astype(np.float64)))
 
 
+@pytest.mark.parametrize("B,D_in,D_h", [(200, 100, 90), (700, 256, 520), (1030, 384, 1100), (4100, 130, 513)])
+@pytest.mark.parametrize("decay", [False, True])
+def test_rows_of_a_large_step_equal_those_of_small_ones(B, D_in, D_h, decay):
+    """Bit for bit: a row's state does not depend on the rows beside it."""
+    say(f"i8 large step B={B} {D_in}->{D_h} decay={decay}")
+    rng = np.random.default_rng([3215, B, D_in, D_h])
+    W_in, _ = _layer(rng, D_in, D_h, 0)
+    wi = sr.quantize_columns(dev(W_in))
+    x = dev(_activations(rng, B, D_in))
+    h0 = dev(rng.standard_normal((B, D_h)).astype(np.float32))
+    rate = dev(rng.uniform(0, 0.5, D_h).astype(np.float32))
+    gap = dev(rng.exponential(2.0, B).astype(np.float32))
+
+    def step(rows):
+        kw = dict(decay_rate=rate, delta_t=gap[rows]) if decay else {}
+        return sr.mingru_step_i8(x[rows], *wi, h_prev=h0[rows], **kw)[0]
+
+    h = step(slice(None))
+    for at in sorted({0, 100, B // 2, B - 37}):
+        assert torch.equal(h[at:at + 37], step(slice(at, at + 37)))
+    _h_close(h, *_gates(_host(x), W_in, D_h), _host(h0),
+             np.exp(-_host(rate)[None, :].astype(np.float64) * _host(gap)[:, None]) if decay else 1.0)
+
+
 @pytest.mark.parametrize("B,T,D_in,D_h,D_out", [(2, 64, 16, 16, 16), (1, 1, 20, 30, 10),
                                                 (3, 301, 100, 130, 70), (2, 1024, 512, 512, 512),
                                                 (4, 0, 16, 16, 16)])
