@@ -51,7 +51,7 @@ struct I8Params {
   const float* b_scale;  // [N]
   void* C;               // [M, N], rows of ldc elements
   int64_t ldc;
-  bool vec4, lines;      // rows of C start at multiples of 4 bytes, of 128 bytes
+  bool lines;            // rows of C start at multiples of 128 bytes
   uint32_t tiles_m, tiles_n, n_tiles;
   // tokens: the rows of X are quantised by the kernel, A and a_scale are unused
   const void* X;  // [M, Kx], contiguous
@@ -122,11 +122,11 @@ __device__ __forceinline__ void store4(const I8Params& P, int64_t m, int64_t n, 
   if (m >= P.M || n >= end) return;
   if constexpr (OUT == kBF16) {
     uint16_t* dst = static_cast<uint16_t*>(P.C) + m * P.ldc + n;
-    if (P.vec4 && n + 4 <= end) {
+    if (n + 4 <= end) {
       u32x2 w;
       w.x = bf16_pair(v[0], v[1]);
       w.y = bf16_pair(v[2], v[3]);
-      __builtin_memcpy(__builtin_assume_aligned(dst, 4), &w, 8);
+      __builtin_memcpy(__builtin_assume_aligned(dst, 2), &w, 8);  // one store at any even address
     } else {
 #pragma unroll 1
       for (int j = 0; j < 4 && n + j < end; ++j) {
@@ -733,13 +733,13 @@ struct LargeTile {
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         t[j][g] = load4(rt, (j * R + 8 * g + 4 * (lane / R)) * 4);
-    // 16-byte stores need 4-byte alignment only.
-    const bool wide = P.vec4 && P.ldc <= (int64_t(1) << 20);
+    const bool wide = P.ldc <= (int64_t(1) << 20);  // 32-bit offsets
     // The largest products' results leave the caches to the operands (131072 x
     // 512 x 1024 fp32: 164 -> 134 us); where lines are shared by two rows of
     // results, that would write them twice (20000 x 2048 x 1000: 55 -> 65 us).
     const bool stream = S::MB == 4 && P.lines;
     const int row = lane % R, swz = row % kChunks;
+    const int tail = cols % kPer * kSize, tail_n = cols - cols % kPer;  // bytes past the last whole chunk, its end
     const int c = lane % kChunks, r0 = lane / kChunks;
     char* dst = static_cast<char*>(P.C) + (m0 * P.ldc + n0) * kSize;
     const rsrc_t rc = buffer(dst, int64_t(0xFFFFFFFF));
@@ -775,18 +775,23 @@ struct LargeTile {
             if (i * R + r < rows && n + kPer <= cols) {
               if (stream)
                 __builtin_amdgcn_raw_buffer_store_b128(v, rc, voff, soff, kNonTemporal);
-              else
-                __builtin_amdgcn_raw_buffer_store_b128(v, rc, voff, soff, 0);
+              else  // rows may start at odd bf16 elements: a global store takes any even address
+                __builtin_memcpy(__builtin_assume_aligned(dst + soff + voff, 2), &v, 16);
             }
           }
-        }
-        // What a 16-byte store cannot hold: the columns past the last whole
-        // chunk, or all where rows start at odd bf16 elements.
-        if (!wide || cols % kPer != 0) {
+          // The columns past the last whole chunk, a lane per row.
+          if (tail != 0 && pass == tail_n / (kPassN * R) && lane < R && i * R + row < rows) {
+            const int8_t* from = out + row * S::kOutRow + (((tail_n / kPer % kChunks) ^ swz) << 4);
+            char* to = dst + (int64_t(i * R + row) * row_bytes + tail_n * kSize);
+            if (tail & 8) __builtin_memcpy(__builtin_assume_aligned(to, 2), from, 8);
+            if (tail & 4) __builtin_memcpy(__builtin_assume_aligned(to + (tail & 8), 2), from + (tail & 8), 4);
+            if (tail & 2) __builtin_memcpy(__builtin_assume_aligned(to + (tail & 12), 2), from + (tail & 12), 2);
+          }
+        } else {  // offsets pass 32 bits
 #pragma unroll 1
           for (int q = 0; q < R / kRowsPer; ++q) {
             const int r = q * kRowsPer + r0, m = i * R + r;
-            if (m >= rows || (wide && n + kPer <= cols)) continue;
+            if (m >= rows) continue;
             const int8_t* from = out + r * S::kOutRow + ((c ^ (r % kChunks)) << 4);
             char* to = dst + (int64_t(m) * P.ldc + n) * kSize;
 #pragma unroll 1
@@ -1092,7 +1097,6 @@ sr_status launch_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64
   P.B = B; P.ldb = ldb; P.b_scale = b_scale;
   P.C = C; P.ldc = ldc;
   const int64_t row_bytes = ldc * (c_dtype == SR_BF16 ? 2 : 4);
-  P.vec4 = row_bytes % 4 == 0 && aligned(C, 4);
   P.lines = row_bytes % 128 == 0 && aligned(C, 128);
   if (tokens != nullptr)
     return c_dtype == SR_BF16 ? launch_tokens<kBF16>(P, *tokens, stream, check_only)

@@ -230,6 +230,43 @@ def test_product_writes_only_its_rows(M, K, N):
         assert bool((big[0] == -7).all() and (big[M + 1] == -7).all() and (big[:, N:] == -7).all())
 
 
+@pytest.mark.parametrize("N", range(1017, 1024))
+def test_every_width_of_the_last_columns(N):
+    """One to seven columns past the last 16 bytes, in tiles of 128 x 128 and
+    of 256 x 256, against the narrow product's rows."""
+    say(f"i8 last columns N={N}")
+    M, K = 40000, 1024
+    a, sa, b, sb = (dev(t, torch.int8 if t.dtype == np.int8 else torch.float32)
+                    for t in _operands(np.random.default_rng([3140, N]), M, K, N))
+    for dtype in (torch.float32, torch.bfloat16):
+        for rows in (M, 2100):
+            big = torch.full((rows * N + 9,), -7.0, device="cuda", dtype=dtype)
+            y = big[4:4 + rows * N].view(rows, N)
+            sr.matmul_i8(a[:rows], sa[:rows], b, sb, out=y)
+            for at in (0, 1000, rows - 60):
+                assert torch.equal(y[at:at + 60], sr.matmul_i8(a[at:at + 60], sa[at:at + 60], b, sb, out_dtype=dtype))
+            ref = (a[:rows].float() @ b.float().t().contiguous()) * sa[:rows, None] * sb
+            assert bool(((y.float() - ref).abs() <= 2.0 ** -7 * ref.abs() + 2.0 ** -20 * K * 127 * 127 * sa[:rows, None] * sb).all())
+            assert bool((big[:4] == -7).all() and (big[4 + rows * N:] == -7).all())
+
+
+@pytest.mark.parametrize("M,N", [(40, 700), (300, 8195)])
+def test_rows_of_results_more_than_2_20_elements_apart(M, N):
+    say(f"i8 far rows {M}x{N}")
+    import ctypes
+    K, far = 256, (1 << 20) + 3
+    a, sa, b, sb = _operands(np.random.default_rng([3145, M]), M, K, N)
+    A, B, SA, SB = dev(a, torch.int8), dev(b, torch.int8), dev(sa), dev(sb)
+    for dtype, code in ((torch.float32, sr.SR_F32), (torch.bfloat16, sr.SR_BF16)):
+        ref = sr.matmul_i8(A, SA, B, SB, out_dtype=dtype)
+        big = torch.full((M, far), -7.0, device="cuda", dtype=dtype)
+        st = sr.raw_library().matmul_i8(M, N, K, A.data_ptr(), K, SA.data_ptr(), B.data_ptr(), K,
+                                        SB.data_ptr(), big.data_ptr(), far, code,
+                                        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert st == 0
+        assert torch.equal(big[:, :N], ref) and bool((big[:, N:] == -7).all())
+
+
 def test_outputs_past_2_31_elements():
     say("i8 product past 2^31 outputs")
     M, K, N = 70000, 128, 32768
