@@ -64,6 +64,46 @@ def test_columns(K, N, dtype):
     _same_codes(q, s, _host(W).T.copy())
 
 
+@pytest.mark.parametrize("M,K", [(3, 7), (2, 8), (5, 9), (40, 1001), (2100, 777), (7, 2049), (3, 4103), (2, 32767), (2, 33001)])
+@pytest.mark.parametrize("start", [0, 1])
+def test_bf16_rows_at_odd_elements(M, K, start):
+    """Odd lengths, odd distances and odd starts, at the end of their memory."""
+    say(f"i8 odd rows {M}x{K}+{start}")
+    rng = np.random.default_rng([3011, M, K])
+    held = torch.zeros(start + M * K, device="cuda", dtype=torch.bfloat16)
+    held[start:] = dev(rng.standard_normal((M, K)).astype(np.float32), torch.bfloat16).reshape(-1)
+    x = held[start:].view(M, K)
+    _same_codes(*sr.quantize_rows(x), _host(x))
+
+
+@pytest.mark.parametrize("K,N", [(1, 8), (5, 9), (300, 7), (1000, 1001), (2049, 50), (4097, 70), (4096, 515), (9000, 33), (513, 4100)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_columns_at_odd_elements(K, N, dtype):
+    say(f"i8 odd columns {K}x{N} {dtype}")
+    rng = np.random.default_rng([3021, K, N])
+    held = torch.zeros(1 + K * N, device="cuda", dtype=dtype)
+    held[1:] = dev(rng.standard_normal((K, N)).astype(np.float32), dtype).reshape(-1)
+    W = held[1:].view(K, N)
+    _same_codes(*sr.quantize_columns(W), _host(W).T)
+    wide = dev(rng.standard_normal((K, N + 3)).astype(np.float32), dtype)[:, 2:2 + N]
+    _same_codes(*sr.quantize_columns(wide), _host(wide).T)
+
+
+@pytest.mark.parametrize("K", [130, 3000, 5000])
+def test_columns_of_zeros_not_finite_and_at_the_ends_of_the_range(K):
+    say(f"i8 special columns K={K}")
+    rng = np.random.default_rng([3022, K])
+    W = rng.standard_normal((K, 200)).astype(np.float32)
+    W[:, 3] = 0
+    W[:, 64:96] = 0
+    W[:, 100] *= 1e-38
+    W[:, 101] *= 1e36
+    W[K - 1, 120] = np.nan
+    W[0, 130] = -np.inf
+    W[:, 140] *= 1e-44
+    _same_codes(*sr.quantize_columns(dev(W)), W.T)
+
+
 def test_rows_special_values_and_ties():
     say("i8 rows special values")
     K = 300
