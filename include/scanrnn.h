@@ -328,6 +328,8 @@ sr_status quantize_columns(int64_t K, int64_t N, const void* W, int64_t ldw, sr_
  *   a, b    [M,K] and [N,K] codes in [-127, 127], rows of lda / ldb >= K
  *           bytes; a, b, lda and ldb multiples of 16.
  *   y       [M,N] in y_dtype, rows of ldy >= N elements.
+ * SR_ERR_UNSUPPORTED: M or N above 16777215, M N above about 2^38, rows of
+ * codes more than 8 MiB apart.
  */
 sr_status matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda,
                     const float* a_scale, const int8_t* b, int64_t ldb, const float* b_scale,
@@ -352,7 +354,9 @@ sr_status matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t ld
  * mingru_forward_i8 hands [k|p] to the scan in x_dtype: with bf16 activations
  * the gates are rounded to bf16, which halves the staged bytes and is below
  * the rounding of the 8-bit codes.  Everything else as in mingru_step / mingru_forward;
- * codes 16-byte aligned.
+ * codes 16-byte aligned; W_in below 4 GiB (else SR_ERR_UNSUPPORTED).
+ * mingru_step_i8: h_next may be the same buffer as h_prev, and must not overlap
+ * x_t.  A row's results do not depend on the rows beside it.
  */
 size_t mingru_step_i8_workspace_size(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out);
 sr_status mingru_step_i8(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out,
@@ -396,7 +400,8 @@ sr_status mingru_forward_i8(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int
  *               8: m and v hold one float8 e4m3 (OCP) code per element, of m and
  *               of sqrt(v), each block of 256 elements with one fp32 scale in m_scale /
  *               v_scale [state_elements / 256]: value = code * scale, scale = the
- *               block's largest magnitude / 448, codes to nearest; a positive sqrt(v)
+ *               block's largest magnitude times the fp32 nearest to 1 / 448, codes to
+ *               nearest; a positive sqrt(v)
  *               never gets the code 0 (it is raised to 2^-9).  A block whose state
  *               holds a NaN or an infinity gets the scale NaN.  Zeroed buffers are
  *               the states before the first step.

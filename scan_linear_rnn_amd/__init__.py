@@ -18,6 +18,12 @@ return_next_prev_hidden=True and keep the returned state).
 mingru_scan is the one convenience beyond the C names: the scan-only
 forward and its backward kernel in a torch.autograd.Function, so that a
 caller can train through the scan (autograd only records the call).
+
+The calls on 8-bit codes and AdamW (quantize_rows, quantize_columns,
+matmul_i8, mingru_step_i8, mingru_forward_i8, adamw_step) marshal their
+arguments in a compiled module, _binding, since a single-token call would
+spend more time in Python than on the GPU; MinGRU.quantized() and AdamW are
+the objects that hold their codes and states.
 """
 
 from __future__ import annotations

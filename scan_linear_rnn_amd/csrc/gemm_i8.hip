@@ -164,8 +164,10 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t n) {
 // on its own loads only; two lines per wave, the next one loading while one
 // is multiplied.  Each byte is read once per workgroup, and nobody meets at a
 // barrier until the waves' sums do in LDS (integers: their order does not
-// matter).  v_mfma_i32_16x16x64_i8: lane l supplies 16 consecutive bytes of
-// row l % 16 from 16 (l / 16); accumulator r of lane l is D[4 (l / 16) + r][l % 16].
+// matter).  256 x 2048 x 4096 takes 7.2 us, 600 TOP/s: 256 tiles of 64 x 64 move
+// 64 MB from L2, at 22 TB/s.
+// v_mfma_i32_16x16x64_i8: lane l supplies 16 consecutive bytes of row l % 16
+// from 16 (l / 16); accumulator r of lane l is D[4 (l / 16) + r][l % 16].
 constexpr int kSplitWaves = 4;
 
 template <int OUT, int MT, int NT>
@@ -483,6 +485,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void i8_token_kernel(const I8Para
 // leaves, across tiles too, so that a tile's results are stored under the
 // next one's first loads.  With MB = NB = 4 a lane holds 256 sums, a CU one
 // workgroup, and an operand byte that a wave reads from LDS is used 128 times.
+// 131072 x 2048 x 4096 with bf16 results takes 1055 to 1077 us, 2.0 to 2.1 POP/s:
+// bound by power (8192^3 runs at 1.47 GHz, the matrix cores 64% busy).
 // v_mfma_i32_32x32x32_i8: lane l supplies 16 consecutive bytes of row l % 32
 // from 16 (l / 32); accumulator r of lane l is D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
 template <int MB_, int NB_>
@@ -860,7 +864,9 @@ __global__ __launch_bounds__(64 * S::kWaves, S::kPerCu) void i8_large_kernel(con
 // The 128 x 128 tile for grids that give a CU one workgroup at most, where
 // only the wave itself can hide its latencies: four stages in LDS, three of
 // them on their way, and the operands of a whole stage read into registers
-// while the previous one is multiplied.
+// while the previous one is multiplied.  1024 x 2048 x 4096, 16.1 us: 256 tiles
+// are one round whose first loads (3.5 us with the launch) and stores (2.5)
+// nothing covers.
 template <int OUT, class S>
 struct DeepTile : LargeTile<OUT, S> {
   using T = LargeTile<OUT, S>;
@@ -1012,22 +1018,22 @@ sr_status launched() {
 // Which kernel.  Measured in us (one launch in a replayed graph, weights from
 // four alternating buffers; narrow 64 x 64 / 32 x 32 / 16 x 32, deep and
 // persistent 128 x 128, 256 x 256):
-//   M x K x N          64x64  32x32  16x32  deep  128x128  256x256
-//   32 x 2048 x 4096     6.4    4.0    3.7     -     14.4     31.3
-//   256 x 2048 x 2048    6.6    5.2    6.7     -     10.9     27.7
-//   256 x 2048 x 4096    7.5    9.4   11.9  12.0     13.5     28.4
-//   512 x 2048 x 4096   13.0   16.0   20.0  12.8     14.3     28.9
-//   1024 x 2048 x 4096  23.1   28.1   36.7  16.1     16.9     30.5
-//   8192 x 1024 x 2048  70.4      -      -  37.9     30.9     28.6
-//   20000 x 2048 x 1000    -      -      -     -     57.4     66.7
-//   131072 x 512 x 1024    -      -      -     -      210      166
-// So: 128 x 128 tiles from half as many as there are CUs (a step, whose gates
-// want every CU: from one more; 512 streams, D = 2048, with their quantisation
-// 19.0 us deep, 17.6 narrow; 640: 19.7, 23.9), in the deep form while a CU has
-// one at most; below that the largest narrow tile that still
-// gives every CU one.  256 x 256 tiles do an area's work in about 5/6 of the
-// time, so they are taken where they need at most 6/5 of the rounds (one
-// round alone only with a depth that carries it).
+//   M x K x N          64x64  32x32  16x32  deep  128x128  256x256   (fp32 results)
+//   32 x 2048 x 4096     6.4    3.9    3.6     -     13.0     29.0
+//   256 x 2048 x 2048    6.6    5.1    6.6     -     11.1     30.8
+//   256 x 2048 x 4096    7.4    9.2   11.6  12.8     14.0     31.2
+//   512 x 2048 x 4096   12.7   15.3   19.4  13.6     14.6     31.3
+//   1024 x 2048 x 4096  22.9   26.8   34.7  16.1     17.3     31.5
+//   8192 x 1024 x 2048  70.3      -      -  37.5     30.5     29.4
+//   20000 x 2048 x 1000    -      -      -     -     56.3     68.5
+//   131072 x 512 x 1024    -      -      -     -      188      140
+// (a step with its quantisation, D = 2048: 512 streams 17.6 in 64 x 64, 19.0
+// deep; 640 streams 23.9, 19.7).  So: 128 x 128 tiles where they are more than
+// half as many as there are CUs, in the deep form while a CU has one at most;
+// below that the largest narrow tile that still gives every CU one.  256 x 256
+// tiles do an area's work in about 5/6 of the time, so they are taken where
+// they need at most 6/5 of the rounds (one round alone only with a depth that
+// carries it).
 template <int OUT>
 sr_status launch(I8Params P, hipStream_t stream, bool check_only) {
   const sr_status st = check_sizes<OUT>(P);
@@ -1036,7 +1042,7 @@ sr_status launch(I8Params P, hipStream_t stream, bool check_only) {
   auto tiles = [&](int64_t rows, int64_t cols) { return ((P.M + rows - 1) / rows) * ((n + cols - 1) / cols); };
   const int64_t t128 = tiles(128, 128), t256 = tiles(256, 256);
   const int64_t rounds128 = (t128 + 2 * kCus - 1) / (2 * kCus), rounds256 = (t256 + kCus - 1) / kCus;
-  if (P.K > 0 && t128 >= kCus / 2 + is_step(OUT)) {
+  if (P.K > 0 && t128 > kCus / 2) {
     if (t128 <= kCus)
       deep<OUT>(P, stream);
     else if (!is_step(OUT) && 5 * rounds256 <= 3 * rounds128 && (rounds256 > 1 || P.K >= 1024))
