@@ -354,7 +354,8 @@ sr_status matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t ld
  * mingru_forward_i8 hands [k|p] to the scan in x_dtype: with bf16 activations
  * the gates are rounded to bf16, which halves the staged bytes and is below
  * the rounding of the 8-bit codes.  Everything else as in mingru_step / mingru_forward;
- * codes 16-byte aligned; W_in below 4 GiB (else SR_ERR_UNSUPPORTED).
+ * codes 16-byte aligned; D_in and D_h at most 131072, W_in below 4 GiB (else
+ * SR_ERR_UNSUPPORTED).
  * mingru_step_i8: h_next may be the same buffer as h_prev, and must not overlap
  * x_t.  A row's results do not depend on the rows beside it.
  */
@@ -407,6 +408,8 @@ sr_status mingru_forward_i8(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int
  *               the states before the first step.
  *   grad_scale  device fp32 scalar multiplied onto every gradient (clipping, loss
  *               scaling), or NULL.
+ * The step and the hyperparameters travel with the launch: a captured graph
+ * replays those of its capture.
  */
 typedef struct {
   void* param;

@@ -535,6 +535,42 @@ def test_layer_object_modes_agree():
     assert torch.equal(q.W_in_scale, sr.quantize_columns(layer.W_in)[1])
 
 
+def test_operands_past_4_gib():
+    """Codes of 4.6 GiB and a step's weights of just under 4 GiB: rows at
+    their ends against the same rows alone."""
+    say("i8 operands past 4 GiB")
+    K = 4096
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3240)
+    big = torch.randint(-127, 128, (1_200_000, K), dtype=torch.int8, device="cuda", generator=g)
+    scale = torch.rand(big.shape[0], device="cuda", generator=g) + 0.1
+    few, few_scale = big[1_000_000:1_000_003].clone(), scale[:3].clone()
+    ends = (0, 524_280, big.shape[0] - 40)
+    y = sr.matmul_i8(few, few_scale, big, scale)          # the weights are large
+    for at in ends:
+        assert torch.equal(y[:, at:at + 40], sr.matmul_i8(few, few_scale, big[at:at + 40], scale[at:at + 40]))
+    y = sr.matmul_i8(big, scale, few, few_scale)          # the rows are
+    for at in ends:
+        assert torch.equal(y[at:at + 40], sr.matmul_i8(big[at:at + 40], scale[at:at + 40], few, few_scale))
+    D, D_in = 131_000, 4 * K
+    W, ws = big.view(-1, D_in)[:2 * D], scale[:2 * D] * 1e-4
+    for B in (2, 40, 300):
+        x = torch.randn(B, D_in, device="cuda", generator=g)
+        h0 = torch.randn(B, D, device="cuda", generator=g)
+        h = sr.mingru_step_i8(x, W, ws, h_prev=h0)[0]
+        for at in (0, 65_530, D - 40):
+            part = slice(at, at + 40)
+            Wp = torch.cat([W[part], W[D + at:D + at + 40]])
+            wsp = torch.cat([ws[part], ws[D + at:D + at + 40]])
+            assert torch.equal(h[:, part], sr.mingru_step_i8(x, Wp, wsp, h_prev=h0[:, part].contiguous())[0])
+    del big, W
+    x = torch.randn(1_100_000, K, device="cuda", generator=g, dtype=torch.bfloat16)  # 8.4 GiB
+    q, s = sr.quantize_rows(x)
+    at = x.shape[0] - 50
+    q_end, s_end = sr.quantize_rows(x[at:].clone())
+    assert torch.equal(q[at:], q_end) and torch.equal(s[at:], s_end)
+
+
 def test_another_stream_and_repeatability():
     say("i8 streams")
     rng = np.random.default_rng(3240)
