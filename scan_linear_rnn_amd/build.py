@@ -82,7 +82,7 @@ def _build_binding() -> None:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{i}" for i in includes), os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
            *(f"-L{p}" for p in cpp_extension.library_paths()),
-           "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-ltorch"]
+           "-lc10", "-lc10_hip", "-ltorch_hip", "-ltorch_cpu", "-ltorch_python", "-ltorch"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
