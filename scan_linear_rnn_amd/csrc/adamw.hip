@@ -39,6 +39,11 @@ constexpr int kBlock = int(kStateBlock);
 constexpr int kWaves = 4;
 constexpr int kBlocks = 4;         // per wave
 constexpr int kTensors = 64;       // per launch: one lane each finds a workgroup's tensor
+// Tensors up to this long take one block per wave: their ends go block by
+// block, each at a load's latency.  Measured (us, one block / four, 8-bit states):
+// 60 tensors of 4096 elements 5.1 / 7.0, 49 of 1 to 73728 4.9 / 7.9; 60 of 65536
+// 18.0 / 14.6.
+constexpr int64_t kShort = 16384;
 constexpr float kTop = 448.0f;     // largest e4m3 value
 constexpr float kTiny = 0.001953125f;  // smallest positive one, 2^-9
 
@@ -52,7 +57,7 @@ struct Tensor {
 struct AdamWParams {
   Tensor t[kTensors];
   uint32_t first[kTensors];  // first workgroup of each tensor; past the last: none
-  uint32_t types[kTensors];  // bit 0: bf16 param, bit 1: bf16 grad, bit 2: aligned for vector accesses
+  uint32_t types[kTensors];  // bit 0: bf16 param, bit 1: bf16 grad, bit 2: aligned for vector accesses, bit 3: short
   void* m;
   void* v;
   float* m_scale;  // null: fp32 states
@@ -270,8 +275,9 @@ __global__ __launch_bounds__(64 * kWaves) void adamw_kernel(const AdamWParams P)
   const uint32_t types = P.types[t];
   const float gs = P.grad_scale != nullptr ? *P.grad_scale : 1.0f;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t first = int64_t(blockIdx.x - P.first[t]) * (kWaves * kBlocks), block0 = first + wave;
-  if ((first + kWaves * kBlocks) * kBlock <= T.n && (types & 4)) {
+  const int blocks = types & 8 ? 1 : kBlocks;
+  const int64_t first = int64_t(blockIdx.x - P.first[t]) * (kWaves * blocks), block0 = first + wave;
+  if (blocks == kBlocks && (first + kWaves * kBlocks) * kBlock <= T.n && (types & 4)) {
     switch (types & 3) {
       case 0: return run_blocks<kEight, false, false>(P, T, block0, gs);
       case 1: return run_blocks<kEight, true, false>(P, T, block0, gs);
@@ -280,7 +286,7 @@ __global__ __launch_bounds__(64 * kWaves) void adamw_kernel(const AdamWParams P)
     }
   }
 #pragma unroll 1
-  for (int u = 0; u < kBlocks; ++u)
+  for (int u = 0; u < blocks; ++u)
     if ((block0 + u * kWaves) * kBlock < T.n)
       run_any<kEight>(P, T, types & 1, types & 2, block0 + u * kWaves, gs);
 }
@@ -333,8 +339,10 @@ sr_status launch_adamw(const AdamWRequest& rq) {
         const bool wide = aligned(t.param, p16 ? 8 : 16) && aligned(t.grad, g16 ? 8 : 16);
         P.t[k] = Tensor{t.param, t.grad, t.n, state};
         P.first[k] = uint32_t(blocks);
-        P.types[k] = uint32_t((p16 ? 1 : 0) | (g16 ? 2 : 0) | (wide ? 4 : 0));
-        blocks += (t.n + kPer - 1) / kPer;
+        const bool brief = t.n <= kShort;
+        P.types[k] = uint32_t((p16 ? 1 : 0) | (g16 ? 2 : 0) | (wide ? 4 : 0) | (brief ? 8 : 0));
+        const int64_t per = brief ? kPer / kBlocks : kPer;
+        blocks += (t.n + per - 1) / per;
         ++k;
       }
       state += adamw_span(t.n);
