@@ -42,6 +42,14 @@ __device__ __forceinline__ u32x4 load16(const T* p) {
   return w;
 }
 
+// A chunk's codes: four or eight bytes.
+__device__ __forceinline__ void store_codes(const uint32_t (&c)[1], int8_t* dst) {
+  __builtin_nontemporal_store(c[0], reinterpret_cast<uint32_t*>(dst));
+}
+__device__ __forceinline__ void store_codes(const uint32_t (&c)[2], int8_t* dst) {
+  __builtin_nontemporal_store(u32x2{c[0], c[1]}, reinterpret_cast<u32x2*>(dst));
+}
+
 // WPR waves per row, NV 16-byte chunks per lane: the row is read once and
 // stays in registers; chunks past its end are zeros and become the padding.
 // DWORDS: rows of whole dwords, loaded through a descriptor that ends with the
@@ -102,17 +110,79 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t 
     const int k = (c0 + j * 64 * WPR) * C::kSize;
     uint32_t codes[C::kSize / 4];
     C::codes(w[j], s, r, plain, codes);
-    if (k < Kp) {
-      if constexpr (C::kSize == 8)
-        __builtin_nontemporal_store(u32x2{codes[0], codes[1]}, reinterpret_cast<u32x2*>(dst + k));
-      else
-        __builtin_nontemporal_store(codes[0], reinterpret_cast<uint32_t*>(dst + k));
-    }
+    if (k < Kp) store_codes(codes, dst + k);
   }
 }
 
-// Rows too long for registers, or of bf16 at odd elements and shorter than 16
-// bytes: one per workgroup, read twice (the second time from the caches).
+// Rows of up to NV x LPR x 16 bytes, padding included: LPR lanes each, two or
+// four rows to a wave.  Measured (us, this kernel / a wave per row): bf16
+// 131072 x 21 11.0 / 52, 131072 x 256 19.6 / 53, 131072 x 512 30.7 / 54, 256 x 256
+// 3.4 / 3.3; fp32 131072 x 128 16.4 / 33, 131072 x 256 25.2 / 35.
+template <typename T, int LPR, int NV>
+__global__ __launch_bounds__(256) void quantize_short_rows_kernel(const T* x, int64_t ldx, int64_t M, int K,
+                                                                  int Kp, int8_t* q, float* scale) {
+  using C = Chunk<T>;
+  constexpr int V = C::kSize;
+  const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR;
+  const int c = threadIdx.x % LPR;
+  const T* src = x + (row < M ? row : M - 1) * ldx;
+  u32x4 w[NV] = {};
+  if (K >= V) {
+    const int last = K - V;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = (c + j * LPR) * V;
+      w[j] = load16(src + (k < last ? k : last));
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int past = (c + j * LPR) * V - last;
+      if (past > 0) w[j] = past < V ? from_element<T>(w[j], past) : u32x4{};
+    }
+  } else if (c == 0) {
+#pragma unroll
+    for (int e = 0; e < V - 1; ++e) {
+      const uint32_t x = __float_as_uint(load_f32(src + (e < K ? e : 0)));  // bf16: its bits on top
+      if constexpr (sizeof(T) == 4)
+        w[0][e] = e < K ? x : 0;
+      else
+        w[0][e / 2] |= (e < K ? x : 0) >> (e % 2 ? 0 : 16);
+    }
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const uint32_t t = C::top(w[j]);
+    top = top > t ? top : t;
+  }
+#pragma unroll
+  for (int d = 1; d < LPR; d <<= 1) {
+    const uint32_t o = __shfl_xor(top, d);
+    top = top > o ? top : o;
+  }
+  const float s = row_scale(top), d = s == 0.0f ? 1.0f : s;
+  const bool plain = __builtin_amdgcn_ballot_w64(!divides_plainly(d)) == 0;  // all of the wave's rows
+  const float r = plain ? __fdiv_rn(1.0f, d) : 0.0f;
+  if (row >= M) return;
+  if (c == 0) scale[row] = s;
+  const int width = NV == 1 ? LPR * V : Kp;
+  auto emit = [&](float by, bool fast) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = (c + j * LPR) * V;
+      uint32_t codes[V / 4];
+      C::codes(w[j], by, r, fast, codes);
+      if (k < width) store_codes(codes, q + row * width + k);
+    }
+  };
+  if (plain)  // the stores within, or the compiler computes both sides
+    emit(d, true);
+  else
+    emit(s, false);
+}
+
+// Rows too long for registers: one per workgroup, read twice (the second time
+// from the caches).  Also of rows without elements.
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_any_rows_kernel(const T* x, int64_t ldx, int64_t K,
                                                                 int64_t Kp, int8_t* q, float* scale) {
@@ -314,8 +384,7 @@ void launch_rows(int nv, int64_t M, int K, int Kp, const T* x, int64_t ldx, int8
                  hipStream_t stream) {
   const dim3 grid{uint32_t((M * WPR + 3) / 4)}, block{256};
   auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, x, ldx, M, K, Kp, q, scale); };
-  if (nv <= 1) run(quantize_rows_kernel<T, WPR, 1, DWORDS>);
-  else if (nv <= 2) run(quantize_rows_kernel<T, WPR, 2, DWORDS>);
+  if (nv <= 2) run(quantize_rows_kernel<T, WPR, 2, DWORDS>);
   else if (nv <= 4) run(quantize_rows_kernel<T, WPR, 4, DWORDS>);
   else if (nv <= 8) run(quantize_rows_kernel<T, WPR, 8, DWORDS>);
   else run(quantize_rows_kernel<T, WPR, 16, DWORDS>);
@@ -344,7 +413,21 @@ void launch_rows(int64_t M, int64_t K, const T* x, int64_t ldx, int8_t* q, float
   const int64_t Kp = quantized_row_bytes(K);
   const int64_t chunks = (Kp * int64_t(sizeof(T)) + 15) / 16;  // Kp: the padding is written too
   const bool dwords = sizeof(T) == 4 || ((ldx % 2 == 0 || M == 1) && K % 2 == 0 && aligned(x, 4));
-  if (K == 0 || (!dwords && K < Chunk<T>::kSize) || chunks > 4 * 64 * kMaxChunks) {
+  if (K > 0 && chunks <= 64) {
+    auto run = [&](auto* kernel, int64_t lanes) {
+      hipLaunchKernelGGL(kernel, dim3(uint32_t((M * lanes + 255) / 256)), dim3(256), 0, stream, x, ldx, M, int(K),
+                         int(Kp), q, scale);
+    };
+    if (chunks == 32) {  // the chunks of 128 codes, once or twice
+      run(quantize_short_rows_kernel<T, 32, 1>, 32);
+    } else if (chunks > 32) {
+      run(quantize_short_rows_kernel<T, 32, 2>, 32);
+    } else if constexpr (sizeof(T) == 2) {
+      run(quantize_short_rows_kernel<T, 16, 1>, 16);
+    }
+    return;
+  }
+  if (K == 0 || chunks > 4 * 64 * kMaxChunks) {
     hipLaunchKernelGGL(quantize_any_rows_kernel<T>, dim3(uint32_t(M)), dim3(256), 0, stream, x, ldx, K, Kp, q,
                        scale);
     return;

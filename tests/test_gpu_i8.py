@@ -104,6 +104,25 @@ def test_columns_of_zeros_not_finite_and_at_the_ends_of_the_range(K):
     _same_codes(*sr.quantize_columns(dev(W)), W.T)
 
 
+@pytest.mark.parametrize("K", [1, 3, 4, 7, 8, 9, 127, 128, 129, 255, 256, 257, 383, 511, 512, 513])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_short_rows_of_all_kinds_side_by_side(K, dtype):
+    """Rows of zeros, of NaNs and infinities and at the ends of the range among
+    ordinary ones."""
+    say(f"i8 short rows K={K} {dtype}")
+    rng = np.random.default_rng([3015, K])
+    x = rng.standard_normal((1003, K)).astype(np.float32)
+    x[5:9] = 0
+    x[17, K - 1], x[40, 0], x[41, K // 2] = np.nan, np.inf, -np.inf
+    x[60] *= 1e-37
+    x[61] *= 1e35
+    x[1002] *= 1e-30
+    t = dev(x, dtype)
+    _same_codes(*sr.quantize_rows(t), _host(t))
+    wide = dev(np.hstack([x, x[:, :1], x[:, :1], x[:, :1]]), dtype)[:, 1:1 + K]  # rows K + 3 apart
+    _same_codes(*sr.quantize_rows(wide), _host(wide))
+
+
 def test_rows_special_values_and_ties():
     say("i8 rows special values")
     K = 300
