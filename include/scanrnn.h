@@ -410,6 +410,12 @@ sr_status mingru_forward_i8(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int
  *               scaling), or NULL.
  * The step and the hyperparameters travel with the launch: a captured graph
  * replays those of its capture.
+ *
+ * adamw_step_each: the same with a step number of its own for each tensor,
+ * steps[i] >= 1 in HOST memory (read before the call returns; not read where
+ * grad is NULL).  A tensor whose first gradient comes late, or that is left out of
+ * some steps, counts its own: its states start from zero then, and the
+ * corrections by c1 and c2 belong to them.
  */
 typedef struct {
   void* param;
@@ -424,6 +430,10 @@ sr_status adamw_step(int64_t n_tensors, const sr_adamw_tensor* tensors, void* m,
                      float* m_scale, float* v_scale, int state_bits, int64_t state_elements,
                      int64_t step, double lr, double beta1, double beta2, double eps,
                      double weight_decay, const float* grad_scale, void* stream);
+sr_status adamw_step_each(int64_t n_tensors, const sr_adamw_tensor* tensors, void* m, void* v,
+                          float* m_scale, float* v_scale, int state_bits, int64_t state_elements,
+                          const int64_t* steps, double lr, double beta1, double beta2, double eps,
+                          double weight_decay, const float* grad_scale, void* stream);
 
 /* Text of the last non-OK status returned on this thread ("" if none). */
 const char* scanrnn_last_error(void);

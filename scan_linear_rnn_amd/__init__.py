@@ -101,6 +101,7 @@ EXPORTED = (
     "mingru_forward_i8",
     "adamw_state_elements",
     "adamw_step",
+    "adamw_step_each",
     "scanrnn_last_error",
     "scanrnn_set_lookback_spin_limit",
     "scanrnn_workspace_status",
@@ -187,6 +188,9 @@ def _load() -> ctypes.CDLL:
     f64 = ctypes.c_double
     lib.adamw_step.argtypes = [i64, vp, vp, vp, vp, vp, i32, i64, i64, f64, f64, f64, f64, f64, vp,
                                vp]
+    lib.adamw_step_each.restype = i32
+    lib.adamw_step_each.argtypes = [i64, vp, vp, vp, vp, vp, i32, i64, vp, f64, f64, f64, f64, f64, vp,
+                                    vp]
     lib.scanrnn_last_error.restype = ctypes.c_char_p
     lib.scanrnn_last_error.argtypes = []
     lib.scanrnn_set_lookback_spin_limit.restype = i32
@@ -799,7 +803,9 @@ class AdamW:
     ``params``: contiguous GPU tensors, fp32 or bf16.  ``state_bits``: 32, or 8
     for float8 states with a scale for each 256 elements (2.06 instead of 8
     bytes per parameter).  ``step()`` uses the parameters' ``.grad``; ``step(grads)``
-    the given ones.  A parameter without a gradient is left as it is.
+    the given ones.  A parameter without a gradient is left as it is, and its step
+    is not counted: ``tensor_steps`` holds each parameter's own count, which its
+    bias corrections go by.  ``steps`` is the largest of them; set, it sets them all.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
@@ -808,7 +814,7 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32 (got {state_bits})")
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
-        self.steps = 0
+        self.tensor_steps = [0] * len(self.params)
         total = sum(adamw_state_elements(p.numel()) for p in self.params)
         device = self.params[0].device if self.params else "cuda"
         self.m_scale = self.v_scale = None
@@ -819,14 +825,21 @@ class AdamW:
         else:
             self.m, self.v = torch.zeros((2, total), device=device)
 
+    @property
+    def steps(self) -> int:
+        return max(self.tensor_steps, default=0)
+
+    @steps.setter
+    def steps(self, n: int) -> None:
+        self.tensor_steps = [n] * len(self.params)
+
     @torch.no_grad()
     def step(self, grads=None, grad_scale=None) -> None:
-        if grads is None:
-            grads = [p.grad for p in self.params]
+        grads = [p.grad for p in self.params] if grads is None else list(grads)
         adamw_step(self.params, grads, self.m, self.v, m_scale=self.m_scale, v_scale=self.v_scale,
-                   step=self.steps + 1, lr=self.lr, betas=self.betas, eps=self.eps,
+                   step=[n + 1 for n in self.tensor_steps], lr=self.lr, betas=self.betas, eps=self.eps,
                    weight_decay=self.weight_decay, grad_scale=grad_scale)
-        self.steps += 1
+        self.tensor_steps = [n + (g is not None) for n, g in zip(self.tensor_steps, grads)]
 
     def zero_grad(self) -> None:
         for p in self.params:

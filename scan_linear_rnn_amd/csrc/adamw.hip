@@ -1,6 +1,6 @@
 // One AdamW step over many tensors in few launches, states in fp32 or in 8
-// bits.  For each element, with the step's number t and c1 = 1 - b1^t,
-// c2 = 1 - b2^t:
+// bits.  For each element, with the number t of its tensor's step and
+// c1 = 1 - b1^t, c2 = 1 - b2^t:
 //
 //     g = grad * grad_scale
 //     m = b1 m + (1 - b1) g        v = b2 v + (1 - b2) g^2
@@ -54,16 +54,22 @@ struct Tensor {
   int64_t state;  // first element of its states
 };
 
+// What a tensor's step number makes of the rate and of the root: lr / c1, 1 / sqrt(c2).
+struct Correction {
+  float rate, inv_root_c2;
+};
+
 struct AdamWParams {
   Tensor t[kTensors];
   uint32_t first[kTensors];  // first workgroup of each tensor; past the last: none
   uint32_t types[kTensors];  // bit 0: bf16 param, bit 1: bf16 grad, bit 2: aligned for vector accesses, bit 3: short
+  Correction bias[kTensors];
   void* m;
   void* v;
   float* m_scale;  // null: fp32 states
   float* v_scale;
   const float* grad_scale;  // or null
-  float b1, b2, one_b1, one_b2, decay, rate, inv_root_c2, eps;
+  float b1, b2, one_b1, one_b2, decay, eps;
 };
 static_assert(sizeof(AdamWParams) <= 4096, "kernel arguments");
 
@@ -157,12 +163,13 @@ __device__ __forceinline__ uint32_t encode4(f32x4 x, float* scale) {
 // root is the IEEE one: where an element lies on the tie of two 8-bit codes,
 // the code is then a function of the formula and not of what the compiler
 // contracts.  The reciprocal in p's update is good to an ulp, 2^-23 of it.
-__device__ __forceinline__ void update(const AdamWParams& P, float g, float& p, float& m, float& v, float& r) {
+__device__ __forceinline__ void update(const AdamWParams& P, Correction c, float g, float& p, float& m, float& v,
+                                       float& r) {
 #pragma clang fp contract(off)
   m = m * P.b1 + g * P.one_b1;
   v = v * P.b2 + g * g * P.one_b2;
   r = sqrtf(v);
-  p = p * P.decay - P.rate * (m * __builtin_amdgcn_rcpf(r * P.inv_root_c2 + P.eps));
+  p = p * P.decay - c.rate * (m * __builtin_amdgcn_rcpf(r * c.inv_root_c2 + P.eps));
 }
 
 // The states of a block, as loaded: fp32, or codes and scales.
@@ -211,7 +218,8 @@ struct RawStates<true> {
 
 // kBlocks whole blocks of an aligned tensor, from block0 in steps of kWaves.
 template <bool kEight, bool kP16, bool kG16>
-__device__ __forceinline__ void run_blocks(const AdamWParams& P, const Tensor& T, int64_t block0, float gs) {
+__device__ __forceinline__ void run_blocks(const AdamWParams& P, const Tensor& T, Correction c, int64_t block0,
+                                           float gs) {
   const int lane = threadIdx.x & 63;
   f32x4 p[kBlocks], g[kBlocks];
   RawStates<kEight> s[kBlocks];
@@ -230,7 +238,7 @@ __device__ __forceinline__ void run_blocks(const AdamWParams& P, const Tensor& T
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float pj = p[u][j], mj = m[j], vj = v[j], rj;
-      update(P, g[u][j] * gs, pj, mj, vj, rj);
+      update(P, c, g[u][j] * gs, pj, mj, vj, rj);
       p[u][j] = pj;
       m[j] = mj;
       v[j] = vj;
@@ -243,8 +251,8 @@ __device__ __forceinline__ void run_blocks(const AdamWParams& P, const Tensor& T
 
 // One block that ends the tensor, or of one that is not aligned.
 template <bool kEight>
-__device__ __forceinline__ void run_any(const AdamWParams& P, const Tensor& T, bool p16, bool g16, int64_t block,
-                                        float gs) {
+__device__ __forceinline__ void run_any(const AdamWParams& P, const Tensor& T, Correction c, bool p16, bool g16,
+                                        int64_t block, float gs) {
   const int64_t i = block * kBlock + (threadIdx.x & 63) * 4, n = T.n;
   f32x4 p = load4_any(T.param, p16, i, n);
   const f32x4 g = load4_any(T.grad, g16, i, n);
@@ -255,7 +263,7 @@ __device__ __forceinline__ void run_any(const AdamWParams& P, const Tensor& T, b
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float pj = p[j], mj = m[j], vj = v[j], rj;
-    update(P, g[j] * gs, pj, mj, vj, rj);
+    update(P, c, g[j] * gs, pj, mj, vj, rj);
     const bool on = i + j < n;  // the span's tail keeps out of the block's scale, and stays zero
     p[j] = pj;
     m[j] = on ? mj : 0.0f;
@@ -273,22 +281,23 @@ __global__ __launch_bounds__(64 * kWaves) void adamw_kernel(const AdamWParams P)
   const int t = __builtin_popcountll(__builtin_amdgcn_ballot_w64(P.first[lane] <= blockIdx.x)) - 1;
   const Tensor T = P.t[t];
   const uint32_t types = P.types[t];
+  const Correction bias = P.bias[t];
   const float gs = P.grad_scale != nullptr ? *P.grad_scale : 1.0f;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = types & 8 ? 1 : kBlocks;
   const int64_t first = int64_t(blockIdx.x - P.first[t]) * (kWaves * blocks), block0 = first + wave;
   if (blocks == kBlocks && (first + kWaves * kBlocks) * kBlock <= T.n && (types & 4)) {
     switch (types & 3) {
-      case 0: return run_blocks<kEight, false, false>(P, T, block0, gs);
-      case 1: return run_blocks<kEight, true, false>(P, T, block0, gs);
-      case 2: return run_blocks<kEight, false, true>(P, T, block0, gs);
-      default: return run_blocks<kEight, true, true>(P, T, block0, gs);
+      case 0: return run_blocks<kEight, false, false>(P, T, bias, block0, gs);
+      case 1: return run_blocks<kEight, true, false>(P, T, bias, block0, gs);
+      case 2: return run_blocks<kEight, false, true>(P, T, bias, block0, gs);
+      default: return run_blocks<kEight, true, true>(P, T, bias, block0, gs);
     }
   }
 #pragma unroll 1
   for (int u = 0; u < blocks; ++u)
     if ((block0 + u * kWaves) * kBlock < T.n)
-      run_any<kEight>(P, T, types & 1, types & 2, block0 + u * kWaves, gs);
+      run_any<kEight>(P, T, bias, types & 1, types & 2, block0 + u * kWaves, gs);
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -307,9 +316,9 @@ sr_status launch_adamw(const AdamWRequest& rq) {
   P.one_b1 = float(1.0 - rq.beta1);
   P.one_b2 = float(1.0 - rq.beta2);
   P.decay = float(1.0 - rq.lr * rq.weight_decay);
-  P.rate = float(rq.lr / (1.0 - std::pow(rq.beta1, double(rq.step))));
-  P.inv_root_c2 = float(1.0 / std::sqrt(1.0 - std::pow(rq.beta2, double(rq.step))));
   P.eps = float(rq.eps);
+  int64_t step = 0;  // the one that bias belongs to: neighbours mostly share it
+  Correction bias{};
   // Fills tables of up to kTensors tensors; the first pass only checks that
   // every launch's grid fits.
   constexpr int64_t kPer = int64_t(kWaves) * kBlocks * kBlock;  // elements of a workgroup
@@ -339,6 +348,13 @@ sr_status launch_adamw(const AdamWRequest& rq) {
         const bool wide = aligned(t.param, p16 ? 8 : 16) && aligned(t.grad, g16 ? 8 : 16);
         P.t[k] = Tensor{t.param, t.grad, t.n, state};
         P.first[k] = uint32_t(blocks);
+        const int64_t now = rq.steps != nullptr ? rq.steps[i] : rq.step;
+        if (now != step) {
+          step = now;
+          bias.rate = float(rq.lr / (1.0 - std::pow(rq.beta1, double(now))));
+          bias.inv_root_c2 = float(1.0 / std::sqrt(1.0 - std::pow(rq.beta2, double(now))));
+        }
+        P.bias[k] = bias;
         const bool brief = t.n <= kShort;
         P.types[k] = uint32_t((p16 ? 1 : 0) | (g16 ? 2 : 0) | (wide ? 4 : 0) | (brief ? 8 : 0));
         const int64_t per = brief ? kPer / kBlocks : kPer;

@@ -381,6 +381,55 @@ sr_status check_optional_decay(const Decay& dec, int64_t n_rate, int64_t n_gap) 
   return check_decay(dec, n_rate, n_gap);
 }
 
+// The checks and the launches of an AdamW step; rq holds its step number or numbers.
+sr_status adamw_impl(AdamWRequest& rq, int64_t n_tensors, const sr_adamw_tensor* tensors, void* m,
+                     void* v, float* m_scale, float* v_scale, int state_bits,
+                     int64_t state_elements, double lr, double beta1, double beta2, double eps,
+                     double weight_decay, const float* grad_scale, void* stream) {
+  SR_REQUIRE(n_tensors >= 0, "n_tensors must be non-negative (got %lld)", (long long)n_tensors);
+  SR_REQUIRE(n_tensors == 0 || tensors != nullptr, "tensors is NULL");
+  SR_REQUIRE(state_bits == 8 || state_bits == 32, "state_bits must be 8 or 32 (got %d)", state_bits);
+  SR_REQUIRE(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1, "betas must be in [0, 1)");
+  SR_REQUIRE(lr >= 0 && eps >= 0 && weight_decay >= 0, "lr, eps and weight_decay must be non-negative");
+  int64_t total = 0;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const sr_adamw_tensor& t = tensors[i];
+    SR_REQUIRE(t.n >= 0 && t.n <= (int64_t(1) << 60), "tensor %lld has %lld elements", (long long)i,
+               (long long)t.n);
+    SR_REQUIRE(is_dtype(t.param_dtype) && is_dtype(t.grad_dtype), "tensor %lld: dtype unsupported",
+               (long long)i);
+    SR_REQUIRE(t.n == 0 || t.param != nullptr, "tensor %lld: param is NULL", (long long)i);
+    SR_REQUIRE(aligned(t.param, elem_size(t.param_dtype)) && aligned(t.grad, elem_size(t.grad_dtype)),
+               "tensor %lld: pointers must be aligned to their element size", (long long)i);
+    SR_REQUIRE(!__builtin_add_overflow(total, adamw_span(t.n), &total), "tensor sizes overflow int64");
+  }
+  SR_REQUIRE(state_elements >= total, "the states have %lld elements, %lld needed",
+             (long long)state_elements, (long long)total);
+  SR_REQUIRE(total == 0 || (m != nullptr && v != nullptr), "m or v is NULL");
+  SR_REQUIRE(aligned(m, 16) && aligned(v, 16), "m and v must be 16-byte aligned");
+  if (state_bits == 8)
+    SR_REQUIRE(total == 0 || (m_scale != nullptr && v_scale != nullptr),
+               "8-bit states need m_scale and v_scale");
+  else
+    SR_REQUIRE(m_scale == nullptr && v_scale == nullptr, "fp32 states have no scales");
+  SR_REQUIRE(aligned(m_scale, 4) && aligned(v_scale, 4) && aligned(grad_scale, 4),
+             "fp32 pointers must be 4-byte aligned");
+  rq.n_tensors = n_tensors;
+  rq.tensors = tensors;
+  rq.m = m;
+  rq.v = v;
+  rq.m_scale = m_scale;
+  rq.v_scale = v_scale;
+  rq.lr = lr;
+  rq.beta1 = beta1;
+  rq.beta2 = beta2;
+  rq.eps = eps;
+  rq.weight_decay = weight_decay;
+  rq.grad_scale = grad_scale;
+  rq.stream = as_stream(stream);
+  return launch_adamw(rq);
+}
+
 }  // namespace
 
 void clear_last_error() { g_last_error[0] = '\0'; }
@@ -799,51 +848,26 @@ sr_status adamw_step(int64_t n_tensors, const sr_adamw_tensor* tensors, void* m,
                      int64_t step, double lr, double beta1, double beta2, double eps,
                      double weight_decay, const float* grad_scale, void* stream) {
   g_last_error[0] = '\0';
-  SR_REQUIRE(n_tensors >= 0, "n_tensors must be non-negative (got %lld)", (long long)n_tensors);
-  SR_REQUIRE(n_tensors == 0 || tensors != nullptr, "tensors is NULL");
-  SR_REQUIRE(state_bits == 8 || state_bits == 32, "state_bits must be 8 or 32 (got %d)", state_bits);
   SR_REQUIRE(step >= 1, "step counts from 1 (got %lld)", (long long)step);
-  SR_REQUIRE(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1, "betas must be in [0, 1)");
-  SR_REQUIRE(lr >= 0 && eps >= 0 && weight_decay >= 0, "lr, eps and weight_decay must be non-negative");
-  int64_t total = 0;
-  for (int64_t i = 0; i < n_tensors; ++i) {
-    const sr_adamw_tensor& t = tensors[i];
-    SR_REQUIRE(t.n >= 0 && t.n <= (int64_t(1) << 60), "tensor %lld has %lld elements", (long long)i,
-               (long long)t.n);
-    SR_REQUIRE(is_dtype(t.param_dtype) && is_dtype(t.grad_dtype), "tensor %lld: dtype unsupported",
-               (long long)i);
-    SR_REQUIRE(t.n == 0 || t.param != nullptr, "tensor %lld: param is NULL", (long long)i);
-    SR_REQUIRE(aligned(t.param, elem_size(t.param_dtype)) && aligned(t.grad, elem_size(t.grad_dtype)),
-               "tensor %lld: pointers must be aligned to their element size", (long long)i);
-    SR_REQUIRE(!__builtin_add_overflow(total, adamw_span(t.n), &total), "tensor sizes overflow int64");
-  }
-  SR_REQUIRE(state_elements >= total, "the states have %lld elements, %lld needed",
-             (long long)state_elements, (long long)total);
-  SR_REQUIRE(total == 0 || (m != nullptr && v != nullptr), "m or v is NULL");
-  SR_REQUIRE(aligned(m, 16) && aligned(v, 16), "m and v must be 16-byte aligned");
-  if (state_bits == 8)
-    SR_REQUIRE(total == 0 || (m_scale != nullptr && v_scale != nullptr),
-               "8-bit states need m_scale and v_scale");
-  else
-    SR_REQUIRE(m_scale == nullptr && v_scale == nullptr, "fp32 states have no scales");
-  SR_REQUIRE(aligned(m_scale, 4) && aligned(v_scale, 4) && aligned(grad_scale, 4),
-             "fp32 pointers must be 4-byte aligned");
   AdamWRequest rq{};
-  rq.n_tensors = n_tensors;
-  rq.tensors = tensors;
-  rq.m = m;
-  rq.v = v;
-  rq.m_scale = m_scale;
-  rq.v_scale = v_scale;
   rq.step = step;
-  rq.lr = lr;
-  rq.beta1 = beta1;
-  rq.beta2 = beta2;
-  rq.eps = eps;
-  rq.weight_decay = weight_decay;
-  rq.grad_scale = grad_scale;
-  rq.stream = as_stream(stream);
-  return launch_adamw(rq);
+  return adamw_impl(rq, n_tensors, tensors, m, v, m_scale, v_scale, state_bits, state_elements, lr,
+                    beta1, beta2, eps, weight_decay, grad_scale, stream);
+}
+
+sr_status adamw_step_each(int64_t n_tensors, const sr_adamw_tensor* tensors, void* m, void* v,
+                          float* m_scale, float* v_scale, int state_bits, int64_t state_elements,
+                          const int64_t* steps, double lr, double beta1, double beta2, double eps,
+                          double weight_decay, const float* grad_scale, void* stream) {
+  g_last_error[0] = '\0';
+  SR_REQUIRE(n_tensors <= 0 || (tensors != nullptr && steps != nullptr), "tensors or steps is NULL");
+  for (int64_t i = 0; i < n_tensors; ++i)
+    SR_REQUIRE(tensors[i].grad == nullptr || steps[i] >= 1, "steps count from 1 (tensor %lld: %lld)",
+               (long long)i, (long long)steps[i]);
+  AdamWRequest rq{};
+  rq.steps = steps;
+  return adamw_impl(rq, n_tensors, tensors, m, v, m_scale, v_scale, state_bits, state_elements, lr,
+                    beta1, beta2, eps, weight_decay, grad_scale, stream);
 }
 
 sr_status scanrnn_set_lookback_spin_limit(uint32_t polls) {

@@ -34,6 +34,7 @@ struct Api {
   decltype(&::mingru_forward_i8_workspace_size) forward_workspace;
   decltype(&::mingru_forward_i8) forward;
   decltype(&::adamw_step) adamw_step;
+  decltype(&::adamw_step_each) adamw_step_each;
 } api;
 PyObject* error_class = nullptr;  // ScanRNNError(function, status, message)
 
@@ -52,6 +53,7 @@ void init(const py::dict& entries, py::object error) {
   entry(entries, "mingru_forward_i8_workspace_size", api.forward_workspace);
   entry(entries, "mingru_forward_i8", api.forward);
   entry(entries, "adamw_step", api.adamw_step);
+  entry(entries, "adamw_step_each", api.adamw_step_each);
   error_class = error.release().ptr();
 }
 
@@ -407,12 +409,35 @@ std::vector<Tensor> tensors_of(const py::handle& sequence, const char* name, boo
   return out;
 }
 
-void call_adamw_step(const py::object& params, const py::object& grads, const Tensor& m, const Tensor& v, int64_t step,
-                const MaybeTensor& m_scale, const MaybeTensor& v_scale, double lr, std::pair<double, double> betas,
-                double eps, double weight_decay, const MaybeTensor& grad_scale) {
+int64_t integer(const py::handle& x) {
+  const py::object index = py::reinterpret_steal<py::object>(PyNumber_Index(x.ptr()));
+  if (!index) throw py::error_already_set();
+  const int64_t n = PyLong_AsLongLong(index.ptr());
+  if (n == -1 && PyErr_Occurred()) throw py::error_already_set();
+  return n;
+}
+
+// The step numbers of n tensors.
+std::vector<int64_t> steps_of(const py::object& step, size_t n) {
+  const py::object fast =
+      py::reinterpret_steal<py::object>(PySequence_Fast(step.ptr(), "step must be an integer or a sequence of them"));
+  if (!fast) throw py::error_already_set();
+  if (size_t(PySequence_Fast_GET_SIZE(fast.ptr())) != n)
+    bad_value(std::to_string(n) + " params but " + std::to_string(PySequence_Fast_GET_SIZE(fast.ptr())) + " steps");
+  std::vector<int64_t> out(n);
+  for (size_t i = 0; i < n; ++i) out[i] = integer(PySequence_Fast_GET_ITEM(fast.ptr(), Py_ssize_t(i)));
+  return out;
+}
+
+void call_adamw_step(const py::object& params, const py::object& grads, const Tensor& m, const Tensor& v,
+                     const py::object& step, const MaybeTensor& m_scale, const MaybeTensor& v_scale, double lr,
+                     std::pair<double, double> betas, double eps, double weight_decay, const MaybeTensor& grad_scale) {
   const std::vector<Tensor> ps = tensors_of(params, "params", false), gs = tensors_of(grads, "grads", true);
   if (ps.size() != gs.size())
     bad_value(std::to_string(ps.size()) + " params but " + std::to_string(gs.size()) + " grads");
+  const bool one = PyIndex_Check(step.ptr());
+  const int64_t number = one ? integer(step) : 0;
+  const std::vector<int64_t> steps = one ? std::vector<int64_t>() : steps_of(step, ps.size());
   if (ps.empty()) return;
   std::vector<sr_adamw_tensor> table(ps.size());
   for (size_t i = 0; i < ps.size(); ++i) {
@@ -448,9 +473,12 @@ void call_adamw_step(const py::object& params, const py::object& grads, const Te
   sr_status st;
   {
     py::gil_scoped_release release;
-    st = api.adamw_step(int64_t(table.size()), table.data(), data(m), data(v), data<float>(m_scale),
-                        data<float>(v_scale), eight ? 8 : 32, n, step, lr, betas.first, betas.second, eps,
-                        weight_decay, data<float>(gs_value), stream_of(ps[0]));
+    const auto call = [&](auto* fn, auto which) {
+      return fn(int64_t(table.size()), table.data(), data(m), data(v), data<float>(m_scale), data<float>(v_scale),
+                eight ? 8 : 32, n, which, lr, betas.first, betas.second, eps, weight_decay, data<float>(gs_value),
+                stream_of(ps[0]));
+    };
+    st = one ? call(api.adamw_step, number) : call(api.adamw_step_each, steps.data());
   }
   check("adamw_step", st);
 }
@@ -503,7 +531,8 @@ One AdamW step over many tensors, in place on ``params`` and the states.
 
 ``params`` and ``grads``: lists of contiguous GPU tensors of the same shapes,
 fp32 or bf16 each; a gradient may be None (that tensor is left as it is).
-``step`` counts from 1.  ``m`` and ``v`` hold the states of all tensors one after
+``step`` counts from 1: a number for all of them, or a list of one for each.
+``m`` and ``v`` hold the states of all tensors one after
 another, each tensor's span rounded up to 256 elements
 (``adamw_state_elements``): fp32 without scales, or float8_e4m3fn codes (of m and
 of sqrt(v)) with one fp32 scale for each 256 elements in ``m_scale`` and

@@ -210,7 +210,8 @@ struct AdamWRequest {
   void* v;
   float* m_scale;  // null: fp32 states
   float* v_scale;
-  int64_t step;
+  int64_t step;          // of every tensor, where steps is null
+  const int64_t* steps;  // host memory: of each tensor
   double lr, beta1, beta2, eps, weight_decay;
   const float* grad_scale;
   hipStream_t stream;
