@@ -393,7 +393,8 @@ sr_status mingru_forward_i8(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int
  *   tensors     n_tensors descriptions in HOST memory, read before the call
  *               returns.  A tensor with grad NULL is left as it is, states
  *               included.  param and grad are contiguous and aligned to their
- *               element sizes.
+ *               element sizes.  No two params of a step may share memory (tied
+ *               weights are one tensor: SR_ERR_INVALID_ARGUMENT).
  *   m, v        device states of all tensors one after another, each tensor's span
  *               rounded up to 256 elements (adamw_state_elements(n)); state_elements
  *               is their length, at least the sum of the spans.  16-byte aligned.

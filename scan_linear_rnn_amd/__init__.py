@@ -800,7 +800,8 @@ class MinGRUInt8:
 class AdamW:
     """AdamW over a list of parameters: ``adamw_step`` with the states it needs.
 
-    ``params``: contiguous GPU tensors, fp32 or bf16.  ``state_bits``: 32, or 8
+    ``params``: contiguous GPU tensors, fp32 or bf16, each given once (tied weights are
+    one tensor).  ``state_bits``: 32, or 8
     for float8 states with a scale for each 256 elements (2.06 instead of 8
     bytes per parameter).  ``step()`` uses the parameters' ``.grad``; ``step(grads)``
     the given ones.  A parameter without a gradient is left as it is, and its step

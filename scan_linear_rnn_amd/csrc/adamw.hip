@@ -27,7 +27,10 @@
 // Measured (100.7 M fp32 parameters): fp32 states 465 us, 6.05 TB/s; bf16
 // gradients and 8-bit states 242 us, 5.8 TB/s.
 
+#include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "device_util.hpp"
 #include "internal.hpp"
@@ -302,6 +305,39 @@ __global__ __launch_bounds__(64 * kWaves) void adamw_kernel(const AdamWParams P)
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+bool takes_part(const sr_adamw_tensor& t) { return t.n > 0 && t.grad != nullptr; }
+
+// Workgroups of different tensors run in any order: no two tensors of a step
+// may share memory.  The host sorts their ranges (those that are in order already
+// are only looked through): 0.2 us of a call over 49 tensors (8.6 -> 8.8 us).
+sr_status check_disjoint(int64_t n_tensors, const sr_adamw_tensor* tensors) {
+  struct Range {
+    uintptr_t begin, end;
+  };
+  constexpr int64_t kOnStack = 256;
+  Range few[kOnStack];
+  std::unique_ptr<Range[]> many;
+  if (n_tensors > kOnStack) {
+    many.reset(new (std::nothrow) Range[size_t(n_tensors)]);
+    if (!many) return fail(SR_ERR_UNSUPPORTED, "no host memory for %lld tensors", (long long)n_tensors);
+  }
+  Range* r = many ? many.get() : few;
+  size_t n = 0;
+  bool ascending = true;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    if (!takes_part(tensors[i])) continue;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(tensors[i].param);
+    r[n] = Range{at, at + uintptr_t(tensors[i].n) * (tensors[i].param_dtype == SR_BF16 ? 2 : 4)};
+    ascending = ascending && (n == 0 || r[n - 1].begin <= at);
+    ++n;
+  }
+  if (!ascending) std::sort(r, r + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  for (size_t i = 1; i < n; ++i)
+    if (r[i].begin < r[i - 1].end)
+      return fail(SR_ERR_INVALID_ARGUMENT, "two tensors of the step share memory (a parameter given twice?)");
+  return SR_OK;
+}
+
 }  // namespace
 
 sr_status launch_adamw(const AdamWRequest& rq) {
@@ -323,6 +359,10 @@ sr_status launch_adamw(const AdamWRequest& rq) {
   // every launch's grid fits.
   constexpr int64_t kPer = int64_t(kWaves) * kBlocks * kBlock;  // elements of a workgroup
   for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) {
+      const sr_status st = check_disjoint(rq.n_tensors, rq.tensors);
+      if (st != SR_OK) return st;
+    }
     int64_t state = 0, blocks = 0;
     int k = 0;  // tensors in the table
     for (int64_t i = 0; i <= rq.n_tensors; ++i) {
@@ -343,7 +383,7 @@ sr_status launch_adamw(const AdamWRequest& rq) {
       }
       if (i == rq.n_tensors) break;
       const sr_adamw_tensor& t = rq.tensors[i];
-      if (t.n > 0 && t.grad != nullptr) {
+      if (takes_part(t)) {
         const bool p16 = t.param_dtype == SR_BF16, g16 = t.grad_dtype == SR_BF16;
         const bool wide = aligned(t.param, p16 ? 8 : 16) && aligned(t.grad, g16 ? 8 : 16);
         P.t[k] = Tensor{t.param, t.grad, t.n, state};

@@ -530,7 +530,8 @@ constexpr const char* kAdamWDoc =
 One AdamW step over many tensors, in place on ``params`` and the states.
 
 ``params`` and ``grads``: lists of contiguous GPU tensors of the same shapes,
-fp32 or bf16 each; a gradient may be None (that tensor is left as it is).
+fp32 or bf16 each; a gradient may be None (that tensor is left as it is).  A
+parameter is given once: tensors that share memory are refused.
 ``step`` counts from 1: a number for all of them, or a list of one for each.
 ``m`` and ``v`` hold the states of all tensors one after
 another, each tensor's span rounded up to 256 elements
