@@ -356,8 +356,9 @@ sr_status matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t ld
  * the rounding of the 8-bit codes.  Everything else as in mingru_step / mingru_forward;
  * codes 16-byte aligned; D_in and D_h at most 131072, W_in below 4 GiB (else
  * SR_ERR_UNSUPPORTED).
- * mingru_step_i8: h_next may be the same buffer as h_prev, and must not overlap
- * x_t.  A row's results do not depend on the rows beside it.
+ * mingru_step_i8: h_next may be the same buffer as h_prev; otherwise it must not
+ * overlap h_prev, and it must never overlap x_t or y_t (each is refused with
+ * SR_ERR_INVALID_ARGUMENT).  A row's results do not depend on the rows beside it.
  */
 size_t mingru_step_i8_workspace_size(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out);
 sr_status mingru_step_i8(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out,

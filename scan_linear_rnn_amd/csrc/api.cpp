@@ -371,6 +371,13 @@ sr_status check_i8_weights(int64_t D_in, int64_t D_h, int64_t D_out, const int8_
   return SR_OK;
 }
 
+// Whether two ranges of bytes (of any length, none of them NULL) share memory.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && a_bytes > 0 && b_bytes > 0 && x < y + uintptr_t(b_bytes) &&
+         y < x + uintptr_t(a_bytes);
+}
+
 // `dec.rate` null: no decay, and then nothing else of it may be given.
 sr_status check_optional_decay(const Decay& dec, int64_t n_rate, int64_t n_gap) {
   if (dec.rate == nullptr) {
@@ -718,6 +725,12 @@ sr_status mingru_step_i8(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out, co
   SR_REQUIRE(aligned(x_t, elem_size(x_dtype)) && aligned(y_t, elem_size(x_dtype)) &&
                  aligned(h_prev, 4) && aligned(h_next, 4),
              "pointers must be aligned to their element size");
+  // A workgroup writes states while others still read what theirs come from.
+  const int64_t x_size = int64_t(elem_size(x_dtype)), h_bytes = 4 * B * D_h;
+  SR_REQUIRE(!overlap(h_next, h_bytes, x_t, x_size * B * D_in), "h_next must not overlap x_t");
+  SR_REQUIRE(h_next == h_prev || !overlap(h_next, h_bytes, h_prev, h_bytes),
+             "h_next must be the same buffer as h_prev or not overlap it");
+  SR_REQUIRE(!overlap(h_next, h_bytes, y_t, x_size * B * D_out), "y_t must not overlap h_next");
   const Decay dec{decay_rate, delta_t, log1p_delta, saturated};
   st = check_optional_decay(dec, B * D_h > 0 ? D_h : 0, B * D_h > 0 ? B : 0);
   if (st != SR_OK) return st;

@@ -513,7 +513,8 @@ x_t's type, h_t [B,D_h] fp32).
 ``W_in`` and ``W_out`` are the codes of the layer's weights with their scales
 (quantize_columns); x_t and the new state are quantised row by row inside the
 call.  Without ``W_out`` the output is the new state (the same tensor is returned
-twice).  ``decay_rate`` [D_h] with ``delta_t`` [B]: time decay as in
+twice).  ``h_next`` may be ``h_prev`` (a step in place); it must not share memory with
+another part of it, nor with x_t.  ``decay_rate`` [D_h] with ``delta_t`` [B]: time decay as in
 ``mingru_step_decayed``.)";
 constexpr const char* kForwardDoc =
     R"(mingru_forward_i8(x, W_in, W_in_scale, W_out=None, W_out_scale=None, h0=None, return_last=False, workspace=None,
