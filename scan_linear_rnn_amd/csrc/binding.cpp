@@ -117,6 +117,16 @@ const T* operand(const MaybeTensor& t) {
   return t->numel() ? static_cast<const T*>(t->data_ptr()) : reinterpret_cast<const T*>(uintptr_t(4096));
 }
 
+// After a call has written them, tensors of the caller's count a version up, as
+// PyTorch's own in-place operations do: a backward pass that saved one of them
+// before is then refused.  (Tensors made in inference mode have no version.)
+void written(const Tensor& t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const MaybeTensor& t) {
+  if (t) written(*t);
+}
+
 void* stream_of(const Tensor& t) {
   return c10::hip::getCurrentHIPStream(t.device().index()).stream();
 }
@@ -207,6 +217,8 @@ std::pair<Tensor, Tensor> call_quantize_rows(const Tensor& x, const MaybeTensor&
                            stream_of(x));
   }
   check("quantize_rows", st);
+  written(q);
+  written(scale);
   if (q || scale || x.dim() == 2) return {out.q, out.scale};
   std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end() - 1);
   Tensor s = out.scale.view(shape);
@@ -225,6 +237,8 @@ std::pair<Tensor, Tensor> call_quantize_columns(const Tensor& W, const MaybeTens
                               stream_of(W));
   }
   check("quantize_columns", st);
+  written(q);
+  written(scale);
   return {out.q, out.scale};
 }
 
@@ -256,6 +270,7 @@ Tensor call_matmul_i8(const Tensor& a, const Tensor& a_scale, const Tensor& b, c
                        stream_of(a));
   }
   check("matmul_i8", st);
+  written(out);
   return y;
 }
 
@@ -355,6 +370,8 @@ std::pair<Tensor, Tensor> call_mingru_step_i8(const Tensor& x_t, const Tensor& W
                   ws.data_ptr(), size_t(ws.numel()), stream_of(x));
   }
   check("mingru_step_i8", st);
+  written(h_next);
+  written(saturated);
   return {y ? *y : h, h};
 }
 
@@ -387,6 +404,7 @@ py::object call_mingru_forward_i8(const Tensor& x_in, const Tensor& W_in, const 
                      ws.data_ptr(), size_t(ws.numel()), stream_of(x));
   }
   check("mingru_forward_i8", st);
+  written(saturated);
   if (!return_last) return py::cast(y);
   return py::make_tuple(y, *last);
 }
@@ -481,6 +499,12 @@ void call_adamw_step(const py::object& params, const py::object& grads, const Te
     st = one ? call(api.adamw_step, number) : call(api.adamw_step_each, steps.data());
   }
   check("adamw_step", st);
+  for (size_t i = 0; i < ps.size(); ++i)
+    if (gs[i].defined()) written(ps[i]);
+  written(m);
+  written(v);
+  written(m_scale);
+  written(v_scale);
 }
 
 constexpr const char* kRowsDoc = R"(quantize_rows(x, q=None, scale=None)
