@@ -723,6 +723,8 @@ class MinGRU:
     def _maybe_warn(self, dec):
         if dec is None or self._warned or not self.warn_saturation:
             return
+        if torch.cuda.is_current_stream_capturing():   # nothing can be read then
+            return
         if int(self._saturated.item()) != 0:
             import warnings
             self._warned = True
@@ -763,12 +765,19 @@ class MinGRUInt8:
     """A minGRU layer on 8-bit weights, made from a ``MinGRU``: the codes and
     scales of its W_in and W_out, laid out once.  Called like the layer it was
     made from, with fp32 or bf16 activations; hidden states stay fp32, outputs
-    have the activations' type.  ``requantize(layer)`` takes over the weights of a
+    have the activations' type.  Time decay and its saturation warning (one for
+    each object) are the layer's.  ``requantize(layer)`` takes over the weights of a
     layer that a training step changed, into the same buffers."""
+
+    SATURATION_WARNING = MinGRU.SATURATION_WARNING
+    _decay, _maybe_warn = MinGRU._decay, MinGRU._maybe_warn
 
     def __init__(self, layer: MinGRU):
         self.dim, self.dim_inner = layer.dim, layer.dim_inner
         self.decay_rate, self.log1p_delta = layer.decay_rate, layer.log1p_delta
+        self.warn_saturation = layer.warn_saturation
+        self._saturated = torch.zeros(1, dtype=torch.int32, device=layer.W_in.device)
+        self._warned = False
         self.W_in, self.W_in_scale = quantize_columns(layer.W_in)
         self.W_out = self.W_out_scale = None
         if layer.W_out is not None:
@@ -781,10 +790,7 @@ class MinGRUInt8:
 
     def __call__(self, x, prev_hidden=None, return_next_prev_hidden=False, delta_t=None):
         weights = (self.W_in, self.W_in_scale, self.W_out, self.W_out_scale)
-        dec = {}
-        if self.decay_rate is not None and delta_t is not None:
-            dec = dict(decay_rate=self.decay_rate, delta_t=delta_t.to(torch.float32),
-                       log1p_delta=self.log1p_delta)
+        dec = self._decay(delta_t) or {}
         h = None if prev_hidden is None else prev_hidden.reshape(x.shape[0], self.dim_inner)
         if x.dim() == 2 or (x.shape[1] == 1 and prev_hidden is not None):
             x_t = x.reshape(x.shape[0], x.shape[-1])
@@ -794,6 +800,7 @@ class MinGRUInt8:
             y = y.unsqueeze(1) if x.dim() == 3 else y
         else:
             y, h = mingru_forward_i8(x, *weights, h, return_last=True, **dec)
+        self._maybe_warn(dec or None)
         return (y, h) if return_next_prev_hidden else y
 
 
