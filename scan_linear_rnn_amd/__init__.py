@@ -766,8 +766,9 @@ class MinGRUInt8:
     scales of its W_in and W_out, laid out once.  Called like the layer it was
     made from, with fp32 or bf16 activations; hidden states stay fp32, outputs
     have the activations' type.  Time decay and its saturation warning (one for
-    each object) are the layer's.  ``requantize(layer)`` takes over the weights of a
-    layer that a training step changed, into the same buffers."""
+    each object) are the layer's.  ``requantize(layer)`` takes over a layer of
+    the same shape that a training step changed: its weights into the same buffers,
+    and its decay rates."""
 
     SATURATION_WARNING = MinGRU.SATURATION_WARNING
     _decay, _maybe_warn = MinGRU._decay, MinGRU._maybe_warn
@@ -778,12 +779,21 @@ class MinGRUInt8:
         self.warn_saturation = layer.warn_saturation
         self._saturated = torch.zeros(1, dtype=torch.int32, device=layer.W_in.device)
         self._warned = False
+        self._shapes = self._shapes_of(layer)
         self.W_in, self.W_in_scale = quantize_columns(layer.W_in)
         self.W_out = self.W_out_scale = None
         if layer.W_out is not None:
             self.W_out, self.W_out_scale = quantize_columns(layer.W_out)
 
+    @staticmethod
+    def _shapes_of(layer: MinGRU):
+        return tuple(None if W is None else tuple(W.shape) for W in (layer.W_in, layer.W_out))
+
     def requantize(self, layer: MinGRU) -> None:
+        if self._shapes_of(layer) != self._shapes:    # before anything is written
+            raise ValueError(f"the layer's W_in and W_out have shapes {self._shapes_of(layer)} "
+                             f"(expected {self._shapes})")
+        self.decay_rate, self.log1p_delta = layer.decay_rate, layer.log1p_delta
         quantize_columns(layer.W_in, self.W_in, self.W_in_scale)
         if self.W_out is not None:
             quantize_columns(layer.W_out, self.W_out, self.W_out_scale)

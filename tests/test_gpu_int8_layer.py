@@ -1,5 +1,4 @@
-"""MinGRUInt8 as the layer it was made from: its saturation warning, and what
-requantize takes over or refuses."""
+"""MinGRUInt8 as the layer it was made from: its saturation warning."""
 
 import warnings
 
