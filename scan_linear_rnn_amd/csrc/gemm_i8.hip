@@ -544,7 +544,7 @@ struct LargeTile {
       roff[ks] = (lane % R) * kDepth + (((ks * 2 + lane / R) ^ ((lane >> 1) & 7)) << 4);
   }
   // Stage kt of the tile aimed at.  A single-stage product has a second one
-  // past its end, of zeros: no descriptor reaches that far.
+  // past its end, of zeros (one without depth has two): no descriptor reaches that far.
   __device__ __forceinline__ void load_stage(int8_t* __restrict__ dst, uint32_t kt) {
     const bool past = int64_t(kt) * kDepth >= P.K;
     const rsrc_t a = past ? buffer(nullptr, 0) : ra, b = past ? buffer(nullptr, 0) : rb;
@@ -1042,7 +1042,9 @@ sr_status launch(I8Params P, hipStream_t stream, bool check_only) {
   auto tiles = [&](int64_t rows, int64_t cols) { return ((P.M + rows - 1) / rows) * ((n + cols - 1) / cols); };
   const int64_t t128 = tiles(128, 128), t256 = tiles(256, 256);
   const int64_t rounds128 = (t128 + 2 * kCus - 1) / (2 * kCus), rounds256 = (t256 + kCus - 1) / kCus;
-  if (P.K > 0 && t128 > kCus / 2) {
+  // (The deep form wants a stage; without any depth the persistent one stores zeros, and
+  // 64 x 64 tiles of the largest results would be more than one launch holds.)
+  if (t128 > (P.K > 0 ? kCus / 2 : kCus)) {
     if (t128 <= kCus)
       deep<OUT>(P, stream);
     else if (!is_step(OUT) && 5 * rounds256 <= 3 * rounds128 && (rounds256 > 1 || P.K >= 1024))
