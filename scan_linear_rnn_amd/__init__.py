@@ -589,20 +589,36 @@ def minmax_scan_backward(r, s, x0, x_out, dx, dx_last=None, workspace=None):
 
 
 # The 8-bit and AdamW calls are marshalled in C++ (csrc/binding.cpp): their small
-# calls take 3 us on the GPU, which Python's checks would double.
+# calls take 3 us on the GPU, which Python's checks would double.  The other calls
+# do without: where the module is missing (or was built against another PyTorch),
+# only these fail, each with the reason.
 try:
     from . import _binding
 except ImportError as e:
-    raise ImportError("the compiled binding is missing or does not load: build it first "
-                      f"(python scan_linear_rnn_amd/build.py): {e}") from e
-_binding.init({name: ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in EXPORTED},
-              ScanRNNError)
-quantize_rows = _binding.quantize_rows
-quantize_columns = _binding.quantize_columns
-matmul_i8 = _binding.matmul_i8
-mingru_step_i8 = _binding.mingru_step_i8
-mingru_forward_i8 = _binding.mingru_forward_i8
-adamw_step = _binding.adamw_step
+    _binding = None
+    _binding_error = str(e)
+else:
+    _binding.init({name: ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in EXPORTED},
+                  ScanRNNError)
+
+
+def _bound(name):
+    if _binding is not None:
+        return getattr(_binding, name)
+
+    def missing(*args, **kwargs):
+        raise ImportError(f"{name} needs the compiled binding, which is missing or does not load: build it "
+                          f"first (python scan_linear_rnn_amd/build.py): {_binding_error}")
+
+    return missing
+
+
+quantize_rows = _bound("quantize_rows")
+quantize_columns = _bound("quantize_columns")
+matmul_i8 = _bound("matmul_i8")
+mingru_step_i8 = _bound("mingru_step_i8")
+mingru_forward_i8 = _bound("mingru_forward_i8")
+adamw_step = _bound("adamw_step")
 
 
 def quantized_row_bytes(K: int) -> int:
