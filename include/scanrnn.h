@@ -408,6 +408,16 @@ sr_status mingru_forward_i8(int64_t B, int64_t T, int64_t D_in, int64_t D_h, int
  *               never gets the code 0 (it is raised to 2^-9).  A block whose state
  *               holds a NaN or an infinity gets the scale NaN.  Zeroed buffers are
  *               the states before the first step.
+ *               Limit of the 8-bit v: its codes are 6 to 12 % apart, and one step
+ *               moves sqrt(v) by less (by (1 - beta2) / 2 where a gradient stops), so
+ *               an element follows its block's largest one, which is held exactly.
+ *               While the gradients of a block keep their proportions, sqrt(v) stays
+ *               within about 0.7 to 1.7 of its fp32 value.  An element whose gradients
+ *               shrink against the rest of its block keeps its old sqrt(v), or rises
+ *               with the block, and its steps are too small by that factor; one whose
+ *               gradients grow falls behind by up to about 8 times (beta2 = 0.999;
+ *               3 times with 0.99), with steps too large by that.  beta2 below about
+ *               0.88 follows.  Use 32 bits where single elements change like that.
  *   grad_scale  device fp32 scalar multiplied onto every gradient (clipping, loss
  *               scaling), or NULL.
  * The step and the hyperparameters travel with the launch: a captured graph

@@ -836,7 +836,9 @@ class AdamW:
     ``params``: contiguous GPU tensors, fp32 or bf16, each given once (tied weights are
     one tensor).  ``state_bits``: 32, or 8
     for float8 states with a scale for each 256 elements (2.06 instead of 8
-    bytes per parameter).  ``step()`` uses the parameters' ``.grad``; ``step(grads)``
+    bytes per parameter; the second moment then follows the largest element of
+    each 256, not changes of single elements against it: see ``adamw_step``).
+    ``step()`` uses the parameters' ``.grad``; ``step(grads)``
     the given ones.  A parameter without a gradient is left as it is, and its step
     is not counted: ``tensor_steps`` holds each parameter's own count, which its
     bias corrections go by.  ``steps`` is the largest of them; set, it sets them all.

@@ -15,7 +15,10 @@
 // halves the range that the second moment spans, so that e4m3's 17.8 octaves
 // hold 35 of v; a positive r is never stored as zero (it is raised to the
 // smallest positive code, 2^-9), since the update divides by it.  The update
-// itself uses the unrounded m and v of this step.  A block whose state holds a
+// itself uses the unrounded m and v of this step.  Codes of r lie 6 to 12%
+// apart and one step moves r by less, so over many steps an element follows its
+// block's largest one, held exactly, and not a change of its own gradients (the
+// header says how far that goes).  A block whose state holds a
 // NaN or an infinity gets the scale NaN: all of it reads as NaN.
 //
 // A wave owns whole blocks (four elements per lane), so a block's largest

@@ -563,7 +563,15 @@ another, each tensor's span rounded up to 256 elements
 (``adamw_state_elements``): fp32 without scales, or float8_e4m3fn codes (of m and
 of sqrt(v)) with one fp32 scale for each 256 elements in ``m_scale`` and
 ``v_scale``.  Zeros are the states before the first step.  ``grad_scale``: an fp32
-GPU scalar multiplied onto every gradient.)";
+GPU scalar multiplied onto every gradient.
+
+Limit of the float8 states: codes of sqrt(v) are 6 to 12 percent apart and one
+step moves it by less, so an element follows the largest of its 256, which is held
+exactly.  While the gradients of a block keep their proportions, sqrt(v) stays
+within about 0.7 to 1.7 of its fp32 value; an element whose gradients shrink
+against the rest of its block keeps its old one, and one whose gradients grow falls
+behind by up to about 8 times (beta2 = 0.999; 3 times with 0.99): its steps are too
+small, or too large, by that factor.  Where that matters, use fp32 states.)";
 
 }  // namespace
 
