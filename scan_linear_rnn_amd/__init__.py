@@ -850,7 +850,7 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32 (got {state_bits})")
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
-        self.tensor_steps = [0] * len(self.params)
+        self._steps = 0      # of every parameter, or a list where they differ
         total = sum(adamw_state_elements(p.numel()) for p in self.params)
         device = self.params[0].device if self.params else "cuda"
         self.m_scale = self.v_scale = None
@@ -862,20 +862,36 @@ class AdamW:
             self.m, self.v = torch.zeros((2, total), device=device)
 
     @property
+    def tensor_steps(self) -> list:
+        return [self._steps] * len(self.params) if isinstance(self._steps, int) else list(self._steps)
+
+    @tensor_steps.setter
+    def tensor_steps(self, counts) -> None:
+        counts = [int(n) for n in counts]
+        if len(counts) != len(self.params):
+            raise ValueError(f"{len(self.params)} params but {len(counts)} step counts")
+        self._steps = counts if len(set(counts)) > 1 else max(counts, default=0)
+
+    @property
     def steps(self) -> int:
-        return max(self.tensor_steps, default=0)
+        return self._steps if isinstance(self._steps, int) else max(self._steps)
 
     @steps.setter
     def steps(self, n: int) -> None:
-        self.tensor_steps = [n] * len(self.params)
+        self._steps = int(n)
 
     @torch.no_grad()
     def step(self, grads=None, grad_scale=None) -> None:
         grads = [p.grad for p in self.params] if grads is None else list(grads)
-        adamw_step(self.params, grads, self.m, self.v, m_scale=self.m_scale, v_scale=self.v_scale,
-                   step=[n + 1 for n in self.tensor_steps], lr=self.lr, betas=self.betas, eps=self.eps,
-                   weight_decay=self.weight_decay, grad_scale=grad_scale)
-        self.tensor_steps = [n + (g is not None) for n, g in zip(self.tensor_steps, grads)]
+        now = self._steps
+        alike = isinstance(now, int)
+        moved = adamw_step(self.params, grads, self.m, self.v, m_scale=self.m_scale, v_scale=self.v_scale,
+                           step=now + 1 if alike else [n + 1 for n in now], lr=self.lr, betas=self.betas,
+                           eps=self.eps, weight_decay=self.weight_decay, grad_scale=grad_scale)
+        if alike and moved == len(grads) > 0:
+            self._steps = now + 1
+        elif moved:
+            self.tensor_steps = [n + (g is not None) for n, g in zip(self.tensor_steps, grads)]
 
     def zero_grad(self) -> None:
         for p in self.params:

@@ -447,16 +447,17 @@ std::vector<int64_t> steps_of(const py::object& step, size_t n) {
   return out;
 }
 
-void call_adamw_step(const py::object& params, const py::object& grads, const Tensor& m, const Tensor& v,
-                     const py::object& step, const MaybeTensor& m_scale, const MaybeTensor& v_scale, double lr,
-                     std::pair<double, double> betas, double eps, double weight_decay, const MaybeTensor& grad_scale) {
+int64_t call_adamw_step(const py::object& params, const py::object& grads, const Tensor& m, const Tensor& v,
+                        const py::object& step, const MaybeTensor& m_scale, const MaybeTensor& v_scale, double lr,
+                        std::pair<double, double> betas, double eps, double weight_decay,
+                        const MaybeTensor& grad_scale) {
   const std::vector<Tensor> ps = tensors_of(params, "params", false), gs = tensors_of(grads, "grads", true);
   if (ps.size() != gs.size())
     bad_value(std::to_string(ps.size()) + " params but " + std::to_string(gs.size()) + " grads");
   const bool one = PyIndex_Check(step.ptr());
   const int64_t number = one ? integer(step) : 0;
   const std::vector<int64_t> steps = one ? std::vector<int64_t>() : steps_of(step, ps.size());
-  if (ps.empty()) return;
+  if (ps.empty()) return 0;
   std::vector<sr_adamw_tensor> table(ps.size());
   for (size_t i = 0; i < ps.size(); ++i) {
     const Tensor &p = ps[i], &g = gs[i];
@@ -499,12 +500,17 @@ void call_adamw_step(const py::object& params, const py::object& grads, const Te
     st = one ? call(api.adamw_step, number) : call(api.adamw_step_each, steps.data());
   }
   check("adamw_step", st);
-  for (size_t i = 0; i < ps.size(); ++i)
-    if (gs[i].defined()) written(ps[i]);
+  int64_t moved = 0;
+  for (size_t i = 0; i < ps.size(); ++i) {
+    if (!gs[i].defined()) continue;
+    written(ps[i]);
+    ++moved;
+  }
   written(m);
   written(v);
   written(m_scale);
   written(v_scale);
+  return moved;
 }
 
 constexpr const char* kRowsDoc = R"(quantize_rows(x, q=None, scale=None)
@@ -553,14 +559,15 @@ constexpr const char* kAdamWDoc =
            weight_decay=1e-2, grad_scale=None)
 
 One AdamW step over many tensors, in place on ``params`` and the states.
+Returns how many of them had a gradient.
 
 ``params`` and ``grads``: lists of contiguous GPU tensors of the same shapes,
 fp32 or bf16 each; a gradient may be None (that tensor is left as it is).  A
 parameter is given once: tensors that share memory are refused.
 ``step`` counts from 1: a number for all of them, or a list of one for each.
-``m`` and ``v`` hold the states of all tensors one after
-another, each tensor's span rounded up to 256 elements
-(``adamw_state_elements``): fp32 without scales, or float8_e4m3fn codes (of m and
+``m`` and ``v`` hold the states of all tensors one after another, each tensor's
+span rounded up to 256 elements (``adamw_state_elements``):
+fp32 without scales, or float8_e4m3fn codes (of m and
 of sqrt(v)) with one fp32 scale for each 256 elements in ``m_scale`` and
 ``v_scale``.  Zeros are the states before the first step.  ``grad_scale``: an fp32
 GPU scalar multiplied onto every gradient.

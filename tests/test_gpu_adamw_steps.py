@@ -100,6 +100,21 @@ def test_counters():
     assert opt.tensor_steps == [7, 7]
     opt.step(iter(gs))
     assert opt.tensor_steps == [8, 8]
+    opt.step([None, gs[1]])
+    saved = opt.tensor_steps
+    assert saved == [8, 9] and opt.steps == 9
+    again = sr.AdamW([p.clone() for p in ps])
+    again.m.copy_(opt.m), again.v.copy_(opt.v)
+    again.tensor_steps = saved            # resumed: the same steps from here
+    opt.step(gs), again.step(gs)
+    assert all(torch.equal(a, b) for a, b in zip(ps, again.params)) and again.tensor_steps == [9, 10]
+    with pytest.raises(ValueError):
+        opt.tensor_steps = [1]
+    m, v = torch.zeros(512, device="cuda"), torch.zeros(512, device="cuda")
+    assert sr.adamw_step(ps, [None, gs[1]], m, v, step=[0, 3]) == 1 and not m[:256].any() and m[256:].any()
+    for wrong in ([1], [1, 2, 3], [1, 0], 1.5, [1, 1.5]):
+        with pytest.raises((ValueError, TypeError, sr.ScanRNNError)):
+            sr.adamw_step(ps, gs, m, v, step=wrong)
     empty = sr.AdamW([])
     empty.step([])
     assert empty.steps == 0
