@@ -306,7 +306,8 @@ sr_status mingru_scan_noalloc(int64_t B, int64_t T, int64_t D,
  *   scale [M].
  * quantize_columns: the columns of W [K,N] (rows of ldw >= N elements; an
  *   output channel each) -> q [N, quantized_row_bytes(K)], transposed, scale [N].
- * q must be 16-byte aligned.  K = 0 gives scales 0 and no codes.
+ * q must be 16-byte aligned.  K = 0 gives scales 0 and no codes.  More than
+ * 16777215 rows (quantize_columns: columns) are SR_ERR_UNSUPPORTED.
  */
 int64_t quantized_row_bytes(int64_t K);
 sr_status quantize_rows(int64_t M, int64_t K, const void* x, int64_t ldx, sr_dtype x_dtype,
@@ -354,8 +355,8 @@ sr_status matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t ld
  * mingru_forward_i8 hands [k|p] to the scan in x_dtype: with bf16 activations
  * the gates are rounded to bf16, which halves the staged bytes and is below
  * the rounding of the 8-bit codes.  Everything else as in mingru_step / mingru_forward;
- * codes 16-byte aligned; D_in and D_h at most 131072, W_in below 4 GiB (else
- * SR_ERR_UNSUPPORTED).
+ * codes 16-byte aligned; D_in and D_h at most 131072, W_in below 4 GiB, B (times T)
+ * at most 16777215 (else SR_ERR_UNSUPPORTED).
  * mingru_step_i8: h_next may be the same buffer as h_prev; otherwise it must not
  * overlap h_prev, and it must never overlap x_t or y_t (each is refused with
  * SR_ERR_INVALID_ARGUMENT).  A row's results do not depend on the rows beside it.

@@ -486,7 +486,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void i8_token_kernel(const I8Para
 // next one's first loads.  With MB = NB = 4 a lane holds 256 sums, a CU one
 // workgroup, and an operand byte that a wave reads from LDS is used 128 times.
 // 131072 x 2048 x 4096 with bf16 results takes 1052 to 1077 us, 2.0 to 2.1 POP/s:
-// bound by power (8192^3 runs at 1.47 GHz, the matrix cores 64% busy).
+// the matrix cores are busy half of the cycles, at 1.75 GHz (8192^3: 63% at 1.66
+// GHz; the clock falls as they are busier).
 // v_mfma_i32_32x32x32_i8: lane l supplies 16 consecutive bytes of row l % 32
 // from 16 (l / 32); accumulator r of lane l is D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
 template <int MB_, int NB_>

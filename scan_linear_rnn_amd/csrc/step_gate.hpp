@@ -1,5 +1,7 @@
-// The minGRU update of one (row, channel) in a single-token step, shared by
-// the step kernels' epilogues (gemm.hip, gemm_i8.hip).
+// The minGRU update of one (row, channel) in a single-token step.  The gates
+// and the interpolation are shared by the step kernels' epilogues (gemm.hip,
+// gemm_i8.hip); carried_state is the fp32 step's, the step on codes scales four
+// channels at a time (decayed in gemm_i8.hip).
 #pragma once
 
 #include "internal.hpp"
