@@ -448,6 +448,148 @@ sr_status adamw_step_each(int64_t n_tensors, const sr_adamw_tensor* tensors, voi
                           const int64_t* steps, double lr, double beta1, double beta2, double eps,
                           double weight_decay, const float* grad_scale, void* stream);
 
+/*
+ * Selective state space scan (input-dependent steps and a state of N numbers
+ * per channel), the short causal convolution in front of it and the norm with the
+ * residual's addition around them.  What the five calls of the scan and the
+ * convolution share:
+ *
+ *   lengths     device int32 [B] or NULL: tokens of each sequence of a padded batch
+ *               (values outside [0, T] count as the nearer end).  What stands behind a
+ *               sequence's end is not read into any result, whatever its values;
+ *               outputs and gradients there are zeros, and the last state is the
+ *               one behind the sequence's last token (the first state where it
+ *               has none).
+ *   ld_*        distance of the rows (b, t) of a tensor in elements, row b*T + t at
+ *               (b*T + t) * ld: halves of one projection's output are rows of it.
+ *   outputs     contiguous.  They must not overlap inputs or each other
+ *               (SR_ERR_INVALID_ARGUMENT).
+ * Repeated calls give identical bits.  No call allocates, waits for the GPU or
+ * keeps anything; all can be captured into a graph.
+ *
+ * selective_scan_forward:
+ *
+ *     dt_t = softplus(delta_t + delta_bias)     (delta_softplus 0: delta_t + delta_bias)
+ *     h_n  = exp(dt_t A_n) h_n + dt_t u_t B_tn          n = 1..N, per channel
+ *     y_t  = (sum_n C_tn h_n + skip u_t) silu(z_t)
+ *
+ *   u, delta, z   [B,T,D] rows in x_dtype (SR_F32 or SR_BF16); z NULL: no gate.
+ *   Bm, Cm        [B,T,G,N] rows in x_dtype: G groups of D/G neighbouring channels
+ *                 that share them.  G divides D.
+ *   A             [D,N] fp32, usually negative.
+ *   skip, delta_bias  [D] fp32 or NULL (zeros).
+ *   h0, h_last    [B,D,N] fp32 state in front of and behind the tokens; NULL: zeros,
+ *                 and not wanted.
+ *   y             [B,T,D] in x_dtype.
+ * States, steps and gates are fp32; y is rounded once.  N at most 64 (more:
+ * SR_ERR_UNSUPPORTED).  Few channels and long sequences are cut into chunks of
+ * tokens whose decay is the exponential of their summed steps; a state that left the
+ * fp32 range stays non-finite, but may become NaN where one token after the other would
+ * give an infinity.
+ *
+ * selective_scan_backward: for dL/dy = dy and dL/dh_last = dh_last (or NULL), the
+ * gradients of u, delta, z, Bm and Cm in x_dtype (dB and dC summed over the
+ * channels of a group), of A, skip, delta_bias and h0 in fp32.  dz goes with z;
+ * dskip, ddelta_bias and dh0 may be NULL.  The states are computed again.
+ *
+ * selective_step: one token, rows [B,D] and [B,G,N]; h_next may be the same buffer
+ * as h_prev (NULL: zeros), else they must not overlap.
+ */
+size_t selective_scan_forward_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G);
+sr_status selective_scan_forward(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, const void* u,
+                         int64_t ld_u, const void* delta, int64_t ld_delta, const void* z,
+                         int64_t ld_z, const void* Bm, int64_t ld_b, const void* Cm, int64_t ld_c,
+                         sr_dtype x_dtype, const float* A, const float* skip,
+                         const float* delta_bias, int delta_softplus, const float* h0,
+                         const int32_t* lengths, void* y, float* h_last, void* workspace,
+                         size_t workspace_bytes, void* stream);
+size_t selective_scan_backward_workspace_size(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G);
+sr_status selective_scan_backward(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G,
+                                  const void* u, int64_t ld_u, const void* delta, int64_t ld_delta,
+                                  const void* z, int64_t ld_z, const void* Bm, int64_t ld_b,
+                                  const void* Cm, int64_t ld_c, sr_dtype x_dtype, const float* A,
+                                  const float* skip, const float* delta_bias, int delta_softplus,
+                                  const float* h0, const int32_t* lengths, const void* dy,
+                                  int64_t ld_dy, const float* dh_last, void* du, void* ddelta,
+                                  void* dz, void* dB, void* dC, float* dA, float* dskip,
+                                  float* ddelta_bias, float* dh0, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+sr_status selective_step(int64_t B, int64_t D, int64_t N, int64_t G, const void* u, int64_t ld_u,
+                         const void* delta, int64_t ld_delta, const void* z, int64_t ld_z,
+                         const void* Bm, int64_t ld_b, const void* Cm, int64_t ld_c,
+                         sr_dtype x_dtype, const float* A, const float* skip,
+                         const float* delta_bias, int delta_softplus, const float* h_prev,
+                         float* h_next, void* y, void* stream);
+
+/*
+ * Short causal convolution, a filter of K taps per channel:
+ *
+ *     c_t = bias + sum_{j<K} w_j x_{t-K+1+j},   y_t = silu(c_t)   (silu 0: c_t)
+ *
+ *   x, y        [B,T,D] in x_dtype, x as rows of ld_x.
+ *   w, bias     [D,K] and [D] (or NULL: zeros) in w_dtype.
+ *   state, last [B,K-1,D] in x_dtype: the K - 1 inputs in front of the first
+ *               token, oldest first (NULL: zeros), and behind the sequence (NULL:
+ *               not wanted).
+ * Sums and activation are fp32; y is rounded once.  K from 1 to 8 (more:
+ * SR_ERR_UNSUPPORTED).
+ *
+ * causal_conv_backward: dy and dlast (or NULL) are the gradients on y and last;
+ * dx and dstate in x_dtype, dw and dbias in fp32; dbias and dstate may be NULL.
+ *
+ * causal_conv_step: one token, x and y [B,D]; state_next may be the same buffer as
+ * state (NULL: zeros), else they must not overlap.
+ */
+sr_status causal_conv_forward(int64_t B, int64_t T, int64_t D, int64_t K, const void* x, int64_t ld_x,
+                      sr_dtype x_dtype, const void* w, const void* bias, sr_dtype w_dtype, int silu,
+                      const void* state, const int32_t* lengths, void* y, void* last, void* stream);
+size_t causal_conv_backward_workspace_size(int64_t B, int64_t T, int64_t D, int64_t K,
+                                           sr_dtype x_dtype);
+sr_status causal_conv_backward(int64_t B, int64_t T, int64_t D, int64_t K, const void* x,
+                               int64_t ld_x, sr_dtype x_dtype, const void* w, const void* bias,
+                               sr_dtype w_dtype, int silu, const void* state,
+                               const int32_t* lengths, const void* dy, int64_t ld_dy,
+                               const void* dlast, void* dx, float* dw, float* dbias, void* dstate,
+                               void* workspace, size_t workspace_bytes, void* stream);
+sr_status causal_conv_step(int64_t B, int64_t D, int64_t K, const void* x, int64_t ld_x,
+                           sr_dtype x_dtype, const void* w, const void* bias, sr_dtype w_dtype,
+                           int silu, const void* state, void* state_next, void* y, void* stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition in front:
+ *
+ *     t = x + r   (rounded to r_dtype, stored as total),   y = t / sqrt(mean(t^2) + eps) w
+ *
+ *   x, y       [M,D] in x_dtype, x as rows of ld_x.
+ *   r, total   [M,D] in r_dtype, or both NULL: t = x.  total may be the same
+ *              buffer as r (rows of D then).
+ *   w          [D] in w_dtype.
+ * Sums are fp32; y is made of the sum as it is stored and rounded once.  D from 1 to
+ * 16384 (more: SR_ERR_UNSUPPORTED).
+ *
+ * rms_norm_quantize: y as 8-bit codes with a scale per row, as quantize_rows makes
+ * them, but of the fp32 values: q [M, quantized_row_bytes(D)] 16-byte aligned,
+ * scale [M].
+ *
+ * rms_norm_backward: dy on y and dtotal (or NULL) on total give
+ *     dx = (g - n mean(g n)) / rms + dtotal,   n = t / rms, g = dy w
+ * in total_dtype, the gradient of x and of r, and dw = sum over rows of dy n in fp32.
+ * total is the stored sum (x where there was no residual).
+ */
+sr_status rms_norm_forward(int64_t M, int64_t D, const void* x, int64_t ld_x, sr_dtype x_dtype,
+                   const void* r, int64_t ld_r, sr_dtype r_dtype, const void* w, sr_dtype w_dtype,
+                   float eps, void* total, void* y, void* stream);
+sr_status rms_norm_quantize(int64_t M, int64_t D, const void* x, int64_t ld_x, sr_dtype x_dtype,
+                            const void* r, int64_t ld_r, sr_dtype r_dtype, const void* w,
+                            sr_dtype w_dtype, float eps, void* total, int8_t* q, float* scale,
+                            void* stream);
+size_t rms_norm_backward_workspace_size(int64_t M, int64_t D);
+sr_status rms_norm_backward(int64_t M, int64_t D, const void* total, int64_t ld_total,
+                            sr_dtype total_dtype, const void* w, sr_dtype w_dtype, float eps,
+                            const void* dy, int64_t ld_dy, sr_dtype dy_dtype, const void* dtotal,
+                            int64_t ld_dtotal, void* dx, float* dw, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* Text of the last non-OK status returned on this thread ("" if none). */
 const char* scanrnn_last_error(void);
 

@@ -23,7 +23,10 @@ The calls on 8-bit codes and AdamW (quantize_rows, quantize_columns,
 matmul_i8, mingru_step_i8, mingru_forward_i8, adamw_step) marshal their
 arguments in a compiled module, _binding, since a single-token call would
 spend more time in Python than on the GPU; MinGRU.quantized() and AdamW are
-the objects that hold their codes and states.
+the objects that hold their codes and states.  So do the calls of the
+selective state space scan, the short causal convolution and the
+root-mean-square norm; selective_scan, causal_conv and rms_norm are their
+differentiable forms.
 """
 
 from __future__ import annotations
@@ -32,6 +35,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 __all__ = [
     "MinGRU",
@@ -54,6 +58,18 @@ __all__ = [
     "adamw_step",
     "AdamW",
     "MinGRUInt8",
+    "selective_scan",
+    "selective_scan_forward",
+    "selective_scan_backward",
+    "selective_step",
+    "causal_conv",
+    "causal_conv_forward",
+    "causal_conv_backward",
+    "causal_conv_step",
+    "rms_norm",
+    "rms_norm_forward",
+    "rms_norm_quantize",
+    "rms_norm_backward",
     "library_path",
     "ScanRNNError",
 ]
@@ -102,6 +118,19 @@ EXPORTED = (
     "adamw_state_elements",
     "adamw_step",
     "adamw_step_each",
+    "selective_scan_forward_workspace_size",
+    "selective_scan_forward",
+    "selective_scan_backward_workspace_size",
+    "selective_scan_backward",
+    "selective_step",
+    "causal_conv_forward",
+    "causal_conv_backward_workspace_size",
+    "causal_conv_backward",
+    "causal_conv_step",
+    "rms_norm_forward",
+    "rms_norm_quantize",
+    "rms_norm_backward_workspace_size",
+    "rms_norm_backward",
     "scanrnn_last_error",
     "scanrnn_set_lookback_spin_limit",
     "scanrnn_workspace_status",
@@ -191,6 +220,25 @@ def _load() -> ctypes.CDLL:
     lib.adamw_step_each.restype = i32
     lib.adamw_step_each.argtypes = [i64, vp, vp, vp, vp, vp, i32, i64, vp, f64, f64, f64, f64, f64, vp,
                                     vp]
+    for name, args in (
+            ("selective_scan_forward", [*[i64] * 5, *[vp, i64] * 5, i32, vp, vp, vp, i32, *[vp] * 5, sz, vp]),
+            ("selective_scan_backward", [*[i64] * 5, *[vp, i64] * 5, i32, vp, vp, vp, i32, vp, vp, vp, i64,
+                                         *[vp] * 11, sz, vp]),
+            ("selective_step", [*[i64] * 4, *[vp, i64] * 5, i32, vp, vp, vp, i32, *[vp] * 4]),
+            ("causal_conv_forward", [*[i64] * 4, vp, i64, i32, vp, vp, i32, i32, *[vp] * 5]),
+            ("causal_conv_backward", [*[i64] * 4, vp, i64, i32, vp, vp, i32, i32, vp, vp, vp, i64, *[vp] * 6, sz, vp]),
+            ("causal_conv_step", [*[i64] * 3, vp, i64, i32, vp, vp, i32, i32, *[vp] * 4]),
+            ("rms_norm_forward", [i64, i64, *[vp, i64, i32] * 2, vp, i32, ctypes.c_float, *[vp] * 3]),
+            ("rms_norm_quantize", [i64, i64, *[vp, i64, i32] * 2, vp, i32, ctypes.c_float, *[vp] * 4]),
+            ("rms_norm_backward", [i64, i64, vp, i64, i32, vp, i32, ctypes.c_float, vp, i64, i32, vp, i64, *[vp] * 3,
+                                   sz, vp])):
+        getattr(lib, name).restype = i32
+        getattr(lib, name).argtypes = args
+    for name, args in (("selective_scan_forward_workspace_size", [i64] * 5), ("selective_scan_backward_workspace_size", [i64] * 5),
+                       ("causal_conv_backward_workspace_size", [*[i64] * 4, i32]),
+                       ("rms_norm_backward_workspace_size", [i64] * 2)):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = args
     lib.scanrnn_last_error.restype = ctypes.c_char_p
     lib.scanrnn_last_error.argtypes = []
     lib.scanrnn_set_lookback_spin_limit.restype = i32
@@ -588,7 +636,7 @@ def minmax_scan_backward(r, s, x0, x_out, dx, dx_last=None, workspace=None):
     return dr, ds, dx0
 
 
-# The 8-bit and AdamW calls are marshalled in C++ (csrc/binding.cpp): their small
+# The 8-bit, AdamW and later calls are marshalled in C++ (csrc/binding*.cpp): their small
 # calls take 3 us on the GPU, which Python's checks would double.  The other calls
 # do without: where the module is missing (or was built against another PyTorch),
 # only these fail, each with the reason.
@@ -619,6 +667,15 @@ matmul_i8 = _bound("matmul_i8")
 mingru_step_i8 = _bound("mingru_step_i8")
 mingru_forward_i8 = _bound("mingru_forward_i8")
 adamw_step = _bound("adamw_step")
+selective_scan_forward = _bound("selective_scan_forward")
+selective_scan_backward = _bound("selective_scan_backward")
+selective_step = _bound("selective_step")
+causal_conv_forward = _bound("causal_conv_forward")
+causal_conv_backward = _bound("causal_conv_backward")
+causal_conv_step = _bound("causal_conv_step")
+rms_norm_forward = _bound("rms_norm_forward")
+rms_norm_quantize = _bound("rms_norm_quantize")
+rms_norm_backward = _bound("rms_norm_backward")
 
 
 def quantized_row_bytes(K: int) -> int:
@@ -683,6 +740,89 @@ def mingru_scan(k, p, h0=None, *, decay_rate=None, delta_t=None, log1p_delta=Fal
     if (decay_rate is None) != (delta_t is None):
         raise ValueError("decay_rate and delta_t go together")
     return _Scan.apply(k, p, h0, decay_rate, delta_t, bool(log1p_delta))
+
+
+class _SelectiveScan(torch.autograd.Function):
+    """The selective scan, differentiable in every tensor but ``lengths``."""
+
+    @staticmethod
+    def forward(ctx, u, delta, A, B, C, skip, z, delta_bias, h0, delta_softplus, lengths):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(u, delta, A, B, C, skip, z, delta_bias, h0, lengths)
+        ctx.delta_softplus = delta_softplus
+        return selective_scan_forward(u, delta, A, B, C, skip=skip, z=z, delta_bias=delta_bias,
+                                      delta_softplus=delta_softplus, h0=h0, lengths=lengths, return_last=True)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh_last):
+        u, delta, A, B, C, skip, z, delta_bias, h0, lengths = ctx.saved_tensors
+        dy = torch.zeros_like(u) if dy is None else dy
+        du, ddelta, dA, dB, dC, dskip, dz, dbias, dh0 = selective_scan_backward(
+            u, delta, A, B, C, dy, skip=skip, z=z, delta_bias=delta_bias, delta_softplus=ctx.delta_softplus, h0=h0,
+            lengths=lengths, dh_last=dh_last)
+        return du, ddelta, dA, dB, dC, dskip, dz, dbias, dh0, None, None
+
+
+def selective_scan(u, delta, A, B, C, *, skip=None, z=None, delta_bias=None, delta_softplus=False, h0=None,
+                   lengths=None, return_last=False):
+    """``selective_scan_forward``, differentiable through ``selective_scan_backward``: y
+    [B,T,D], and the last state [B,D,N] when ``return_last``."""
+    y, h_last = _SelectiveScan.apply(u, delta, A, B, C, skip, z, delta_bias, h0, bool(delta_softplus), lengths)
+    return (y, h_last) if return_last else y
+
+
+class _CausalConv(torch.autograd.Function):
+    """The short causal convolution, differentiable in x, weight, bias and state."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, state, silu, lengths):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, weight, bias, state, lengths)
+        ctx.silu = silu
+        return causal_conv_forward(x, weight, bias, silu=silu, state=state, lengths=lengths, return_last=True)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dlast):
+        x, weight, bias, state, lengths = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else dy
+        dx, dw, dbias, dstate = causal_conv_backward(x, weight, dy, bias, silu=ctx.silu, state=state, lengths=lengths,
+                                                     dlast=dlast)
+        return dx, dw.to(weight.dtype), None if bias is None else dbias.to(bias.dtype), dstate, None, None
+
+
+def causal_conv(x, weight, bias=None, *, silu=False, state=None, lengths=None, return_last=False):
+    """``causal_conv_forward``, differentiable through ``causal_conv_backward``: y
+    [B,T,D], and the state behind the sequence [B,K-1,D] when ``return_last``."""
+    y, last = _CausalConv.apply(x, weight, bias, state, bool(silu), lengths)
+    return (y, last) if return_last else y
+
+
+class _RMSNorm(torch.autograd.Function):
+    """The norm with the residual's addition, differentiable in x, weight and residual."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        ctx.set_materialize_grads(False)
+        ctx.eps, ctx.x_dtype, ctx.added = eps, x.dtype, residual is not None
+        out = rms_norm_forward(x, weight, residual, eps=eps)
+        ctx.save_for_backward(out[1] if ctx.added else x, weight)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dtotal=None):
+        total, weight = ctx.saved_tensors
+        dy = torch.zeros_like(total, dtype=ctx.x_dtype) if dy is None else dy
+        dx, dw = rms_norm_backward(total, weight, dy, dtotal=dtotal, eps=ctx.eps)
+        return dx.to(ctx.x_dtype), dw.to(weight.dtype), dx if ctx.added else None, None
+
+
+def rms_norm(x, weight, residual=None, *, eps=1e-6):
+    """``rms_norm_forward``, differentiable through ``rms_norm_backward``: y, or (y, t)
+    with ``residual``."""
+    return _RMSNorm.apply(x, weight, residual, float(eps))
 
 
 class MinGRU:

@@ -8,7 +8,7 @@ package directory.
 Every HIP source is compiled for gfx950 only, with packed-FP32 instruction
 generation switched off (-packed-fp32-ops), and linked into one shared
 library exporting the C ABI declared in include/scanrnn.h.  The binding
-(csrc/binding.cpp, host code against PyTorch's headers) is a Python extension
+(csrc/binding*.cpp, host code against PyTorch's headers) is a Python extension
 module that is given the library's entry points when the package loads.
 
 build_host_sanitized(out_dir) makes a second copy whose HOST code (argument
@@ -36,7 +36,8 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = "gfx950"
 SOURCES = ["scan.hip", "scan_bwd.hip", "gemm.hip", "fused.hip", "noalloc.hip", "quant.hip",
-           "gemm_i8.hip", "adamw.hip", "api.cpp"]
+           "gemm_i8.hip", "adamw.hip", "selective.hip", "selective_bwd.hip",
+           "conv.hip", "norm.hip", "api.cpp", "api_layers.cpp"]
 COMMON = [
     f"--offload-arch={ARCH}",
     "-O3",
@@ -69,6 +70,9 @@ def _compile(src: str, obj_dir: str = OBJ, extra=()) -> str:
     return obj
 
 
+BINDING_SOURCES = ["binding.cpp", "binding_layers.cpp"]
+
+
 def _build_binding() -> None:
     import sysconfig
 
@@ -77,15 +81,23 @@ def _build_binding() -> None:
     rocm = os.path.dirname(os.path.dirname(_hipcc()))
     includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
                 os.path.join(rocm, "include"), INCLUDE]
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           "-DTORCH_EXTENSION_NAME=_binding", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *(f"-I{i}" for i in includes), os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
-           *(f"-L{p}" for p in cpp_extension.library_paths()),
-           "-lc10", "-lc10_hip", "-ltorch_hip", "-ltorch_cpu", "-ltorch_python", "-ltorch"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+             "-DTORCH_EXTENSION_NAME=_binding", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             *(f"-I{i}" for i in includes)]
+
+    def run(cmd):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+
+    objs = [os.path.join(OBJ, os.path.splitext(src)[0] + ".o") for src in BINDING_SOURCES]
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(objs)) as ex:
+        list(ex.map(lambda so: run(["g++", *flags, "-c", os.path.join(CSRC, so[0]), "-o", so[1]]),
+                    zip(BINDING_SOURCES, objs)))
+    run(["g++", "-shared", *objs, "-o", BINDING + ".tmp",
+         *(f"-L{p}" for p in cpp_extension.library_paths()),
+         "-lc10", "-lc10_hip", "-ltorch_hip", "-ltorch_cpu", "-ltorch_python", "-ltorch"])
     os.replace(BINDING + ".tmp", BINDING)
 
 

@@ -10,25 +10,13 @@
 #include <cstdio>
 #include <cstring>
 
-#include "internal.hpp"
+#include "api_util.hpp"
 
 namespace sr {
 
 namespace {
 thread_local char g_last_error[512] = "";
 std::atomic<uint32_t> g_spin_limit{SCANRNN_LOOKBACK_SPIN_LIMIT};
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
-
-// n = a * b * c without overflow, all non-negative.
-bool prod3(int64_t a, int64_t b, int64_t c, int64_t* n) {
-  int64_t ab;
-  return mul_ok(a, b, &ab) && mul_ok(ab, c, n);
-}
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 struct FwdLayout {
   size_t scan_bytes, kp_off, kp_bytes, h_off, h_bytes, g_off, g_bytes, total;
@@ -60,20 +48,6 @@ size_t step_workspace(int64_t B, int64_t D_in, int64_t D_h, int64_t D_out) {
   const size_t b = gemm_workspace_bytes(B, D_out, D_h, false);
   return a > b ? a : b;
 }
-
-sr_status check_workspace(void* ws, size_t have, size_t need) {
-  if (need == 0) return SR_OK;
-  if (ws == nullptr) return fail(SR_ERR_INVALID_ARGUMENT, "workspace is NULL (%zu bytes needed)", need);
-  if (!aligned(ws, kAlign)) return fail(SR_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
-  if (have < need)
-    return fail(SR_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, %zu needed", have, need);
-  return SR_OK;
-}
-
-#define SR_REQUIRE(cond, ...)                                   \
-  do {                                                          \
-    if (!(cond)) return fail(SR_ERR_INVALID_ARGUMENT, __VA_ARGS__); \
-  } while (0)
 
 // Time decay of the carried state: the rate per channel, the gap per token.
 struct Decay {
@@ -312,10 +286,6 @@ sr_status mingru_backward_impl(int64_t B, int64_t T, int64_t D, const void* k, c
 
 // ------------------------------------------------------------- 8-bit path
 
-size_t elem_size(sr_dtype t) { return t == SR_BF16 ? 2 : 4; }
-
-bool is_dtype(sr_dtype t) { return t == SR_F32 || t == SR_BF16; }
-
 // Bytes of the codes and of the scales of [M, K], each a multiple of kAlign.
 size_t code_bytes(int64_t M, int64_t K) {
   return align_up(size_t(M) * size_t(sr::quantized_row_bytes(K)), kAlign);
@@ -369,13 +339,6 @@ sr_status check_i8_weights(int64_t D_in, int64_t D_h, int64_t D_out, const int8_
     return fail(SR_ERR_UNSUPPORTED, "8-bit products are at most %lld deep (D_in=%lld, D_h=%lld)",
                 (long long)kMaxI8Depth, (long long)D_in, (long long)D_h);
   return SR_OK;
-}
-
-// Whether two ranges of bytes (of any length, none of them NULL) share memory.
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && a_bytes > 0 && b_bytes > 0 && x < y + uintptr_t(b_bytes) &&
-         y < x + uintptr_t(a_bytes);
 }
 
 // `dec.rate` null: no decay, and then nothing else of it may be given.

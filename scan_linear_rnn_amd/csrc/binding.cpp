@@ -7,26 +7,13 @@
 // The library's entry points come from the package (init), which has loaded
 // the library; nothing is linked against it.
 
-#include <ATen/ATen.h>
-#include <ATen/hip/EmptyTensor.h>
-#include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/csrc/utils/pybind.h>
 
-#include <optional>
-#include <string>
-#include <vector>
-
-#include "scanrnn.h"
-
-namespace py = pybind11;
-using at::Tensor;
-using MaybeTensor = std::optional<Tensor>;
+#include "binding_util.hpp"
 
 namespace {
 
 struct Api {
-  decltype(&::scanrnn_last_error) last_error;
   decltype(&::quantize_rows) quantize_rows;
   decltype(&::quantize_columns) quantize_columns;
   decltype(&::matmul_i8) matmul_i8;
@@ -37,15 +24,9 @@ struct Api {
   decltype(&::adamw_step) adamw_step;
   decltype(&::adamw_step_each) adamw_step_each;
 } api;
-PyObject* error_class = nullptr;  // ScanRNNError(function, status, message)
-
-template <class F>
-void entry(const py::dict& entries, const char* name, F& fn) {
-  fn = reinterpret_cast<F>(entries[name].cast<uintptr_t>());
-}
 
 void init(const py::dict& entries, py::object error) {
-  entry(entries, "scanrnn_last_error", api.last_error);
+  entry(entries, "scanrnn_last_error", last_error);
   entry(entries, "quantize_rows", api.quantize_rows);
   entry(entries, "quantize_columns", api.quantize_columns);
   entry(entries, "matmul_i8", api.matmul_i8);
@@ -56,144 +37,7 @@ void init(const py::dict& entries, py::object error) {
   entry(entries, "adamw_step", api.adamw_step);
   entry(entries, "adamw_step_each", api.adamw_step_each);
   error_class = error.release().ptr();
-}
-
-// ------------------------------------------------------------------ checks
-
-[[noreturn]] void bad_value(const std::string& what) { throw py::value_error(what); }
-[[noreturn]] void bad_type(const std::string& what) { throw py::type_error(what); }
-
-std::string text(at::IntArrayRef shape) {
-  std::string s = "(";
-  for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
-  return s + (shape.size() == 1 ? ",)" : ")");
-}
-
-void check(const char* fn, sr_status st) {
-  if (st == SR_OK) return;
-  py::object error = py::reinterpret_borrow<py::object>(error_class)(fn, int(st), std::string(api.last_error()));
-  PyErr_SetObject(error_class, error.ptr());
-  throw py::error_already_set();
-}
-
-void on_gpu(const Tensor& t, const std::string& name) {
-  if (!t.defined() || !t.is_cuda())
-    bad_value(name + " must be a GPU tensor (got " + (t.defined() ? t.device().str() : "none") + ")");
-}
-void has_type(const Tensor& t, const std::string& name, at::ScalarType want) {
-  on_gpu(t, name);
-  if (t.scalar_type() != want)
-    bad_type(name + " must be " + at::toString(want) + " (got " + at::toString(t.scalar_type()) + ")");
-}
-sr_dtype float_type(const Tensor& t, const std::string& name) {
-  on_gpu(t, name);
-  if (t.scalar_type() == at::kFloat) return SR_F32;
-  if (t.scalar_type() == at::kBFloat16) return SR_BF16;
-  bad_type(name + " must be float32 or bfloat16 (got " + at::toString(t.scalar_type()) + ")");
-}
-void same_device(const Tensor& t, const std::string& name, const Tensor& like) {
-  if (t.device() != like.device())
-    bad_value(name + " must be on " + like.device().str() + " (got " + t.device().str() + ")");
-}
-void has_shape(const Tensor& t, const std::string& name, at::IntArrayRef shape) {
-  if (t.sizes() != shape) bad_value(name + " must have shape " + text(shape) + " (got " + text(t.sizes()) + ")");
-}
-// A tensor that is written or carried: contiguous as it is.
-void in_place(const Tensor& t, const std::string& name, at::ScalarType type, at::IntArrayRef shape, const Tensor& like) {
-  has_type(t, name, type);
-  has_shape(t, name, shape);
-  if (!t.is_contiguous()) bad_value(name + " must be contiguous");
-  same_device(t, name, like);
-}
-
-template <class T = void>
-T* data(const Tensor& t) { return t.numel() ? static_cast<T*>(t.data_ptr()) : nullptr; }
-template <class T = void>
-T* data(const MaybeTensor& t) { return t ? data<T>(*t) : nullptr; }
-// An optional weight that is present but has no elements (no input features,
-// no state) still has to read as present: an address that is never followed.
-template <class T>
-const T* operand(const MaybeTensor& t) {
-  if (!t) return nullptr;
-  return t->numel() ? static_cast<const T*>(t->data_ptr()) : reinterpret_cast<const T*>(uintptr_t(4096));
-}
-
-// After a call has written them, tensors of the caller's count a version up, as
-// PyTorch's own in-place operations do: a backward pass that saved one of them
-// before is then refused.  (Tensors made in inference mode have no version.)
-void written(const Tensor& t) {
-  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-}
-void written(const MaybeTensor& t) {
-  if (t) written(*t);
-}
-
-void* stream_of(const Tensor& t) {
-  return c10::hip::getCurrentHIPStream(t.device().index()).stream();
-}
-
-Tensor make(const Tensor& like, at::IntArrayRef shape, at::ScalarType type) {
-  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
-}
-
-int64_t stored_width(int64_t K) { return (K + 127) / 128 * 128; }
-
-// fp32 or bf16 as rows of its last dimension: a view when it can be one.
-struct Rows {
-  Tensor t;
-  int64_t n, width, stride;
-  sr_dtype type;
-};
-Rows rows_of(const Tensor& t, const char* name, int64_t dims) {
-  Rows r;
-  r.type = float_type(t, name);
-  if (dims ? t.dim() != dims : t.dim() < 1)
-    bad_value(std::string(name) + " must have " + (dims ? std::to_string(dims) : "at least one") +
-              " dims (got shape " + text(t.sizes()) + ")");
-  r.width = t.size(-1);
-  r.n = 1;
-  for (int64_t i = 0; i + 1 < t.dim(); ++i) r.n *= t.size(i);
-  if (t.dim() == 2 && r.n > 1 && t.stride(1) == 1 && t.stride(0) >= r.width) {
-    r.t = t;
-    r.stride = t.stride(0);
-  } else {
-    r.t = t.contiguous();
-    r.stride = r.width;
-  }
-  return r;
-}
-
-// Codes [.., K] as rows.
-Rows codes_of(const Tensor& t, const char* name, int64_t dims) {
-  has_type(t, name, at::kChar);
-  if (dims ? t.dim() != dims : t.dim() < 2)
-    bad_value(std::string(name) + " must have " + (dims ? std::to_string(dims) : "at least 2") +
-              " dims (got shape " + text(t.sizes()) + ")");
-  Rows r;
-  r.width = t.size(-1);
-  if (r.width % 128)
-    bad_value(std::string(name) + " must have rows of a multiple of 128 codes, zeros behind the data (got " +
-              std::to_string(r.width) + ")");
-  r.n = 1;
-  for (int64_t i = 0; i + 1 < t.dim(); ++i) r.n *= t.size(i);
-  const auto aligned = [](const Tensor& x) { return reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0; };
-  if (t.dim() == 2 && r.n > 1 && t.stride(1) == 1 && t.stride(0) >= r.width && t.stride(0) % 16 == 0 && aligned(t)) {
-    r.t = t;
-    r.stride = t.stride(0);
-  } else {
-    r.t = t.contiguous();
-    if (!aligned(r.t)) r.t = r.t.clone();
-    r.stride = r.width;
-  }
-  return r;
-}
-
-Tensor scales_of(const Tensor& t, const std::string& name, int64_t n, const Tensor& like) {
-  has_type(t, name, at::kFloat);
-  if (t.numel() != n)
-    bad_value(name + " must have " + std::to_string(n) + " elements (got shape " + text(t.sizes()) + ")");
-  same_device(t, name, like);
-  return t.contiguous();
+  init_layers(entries);
 }
 
 // ------------------------------------------------------------------- codes
@@ -333,16 +177,6 @@ DecayArgs decay_of(const MaybeTensor& rate, const MaybeTensor& gap, const MaybeT
     d.saturated = saturated;
   }
   return d;
-}
-
-Tensor workspace_of(const MaybeTensor& workspace, size_t bytes, const Tensor& like) {
-  if (!workspace) return make(like, {int64_t(bytes ? bytes : 1)}, at::kByte);
-  if (workspace->scalar_type() != at::kByte) bad_type("workspace must be a torch.uint8 tensor");
-  if (workspace->device() != like.device() || !workspace->is_contiguous())
-    bad_value("workspace must be a contiguous tensor on " + like.device().str());
-  if (size_t(workspace->numel()) < bytes)
-    bad_value("workspace has " + std::to_string(workspace->numel()) + " bytes, " + std::to_string(bytes) + " needed");
-  return *workspace;
 }
 
 std::pair<Tensor, Tensor> call_mingru_step_i8(const Tensor& x_t, const Tensor& W_in, const Tensor& W_in_scale,
@@ -589,6 +423,7 @@ PYBIND11_MODULE(_binding, mod) {
   py::options options;
   options.disable_function_signatures();
   mod.def("init", &init);
+  bind_layers(mod);
   mod.def("quantize_rows", &call_quantize_rows, kRowsDoc, arg("x"), arg("q") = none, arg("scale") = none);
   mod.def("quantize_columns", &call_quantize_columns, kColumnsDoc, arg("W"), arg("q") = none, arg("scale") = none);
   mod.def("matmul_i8", &call_matmul_i8, kMatmulDoc, arg("a"), arg("a_scale"), arg("b"), arg("b_scale"),

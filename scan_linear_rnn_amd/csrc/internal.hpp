@@ -219,6 +219,125 @@ struct AdamWRequest {
 
 sr_status launch_adamw(const AdamWRequest& rq);
 
+// ------------------------------------------------- selective state space scan
+
+constexpr int kSelectiveTile = 16;        // tokens a workgroup handles between barriers
+constexpr int kSelectiveStates = 64;      // most states per channel
+constexpr int64_t kSelectiveMinChunk = 64;  // tokens of the shortest chunk
+
+// How a call is cut: 64 channels of a group per workgroup, the tokens in chunks.
+struct SelectivePlan {
+  int64_t tiles_per_group;
+  int64_t chunks, chunk_len;  // chunk_len a multiple of kSelectiveTile where there are several
+};
+SelectivePlan selective_plan(int64_t B, int64_t T, int64_t D, int64_t G);
+SelectivePlan selective_backward_plan(int64_t B, int64_t T, int64_t D, int64_t G);
+
+// The operands of the calls (scanrnn.h) and the areas of their workspaces.
+struct SelectiveRequest {
+  sr_dtype dtype;
+  int64_t B, T, D;
+  int N, G;
+  const void *u, *delta, *z;  // z may be null
+  int64_t ld_u, ld_delta, ld_z;
+  const float* A;
+  const void *Bm, *Cm;
+  int64_t ld_b, ld_c;
+  const float *skip, *bias;  // may be null
+  int softplus;
+  const float* h0;  // may be null; the step's h_prev
+  const int32_t* lengths;
+  void* y;
+  float* h_last;  // may be null; the step's h_next
+  int tiles_per_group;
+  int chunks;
+  int64_t chunk_len;
+  float* ends;   // [chunks][B][N][D]
+  float* steps;  // [chunks][B][D]
+  float* marks;  // [T / 16][B][N + 1][D], or null
+  hipStream_t stream;
+  // The backward pass.
+  const void* dy;
+  int64_t ld_dy;
+  const float* dh_last;  // may be null
+  void *du, *ddelta, *dz, *dB, *dC;
+  float *dA, *dskip, *dbias, *dh0;  // dskip, dbias, dh0 may be null
+  float* gends;   // [chunks][B][N][D]
+  float* parts;   // dB and dC of each 64 channels: [tile][B][T][2][states rounded up]
+  float* aparts;  // dA, dskip and dbias of each sequence and chunk: [B][chunks][N + 2][D]
+};
+
+sr_status launch_selective_scan(const SelectiveRequest& rq);
+sr_status launch_selective_states(const SelectiveRequest& rq);
+sr_status launch_selective_carry(const SelectiveRequest& rq, const float* init, float* last, bool reverse);
+sr_status launch_selective_backward(const SelectiveRequest& rq);
+sr_status launch_selective_step(const SelectiveRequest& rq);
+// States of one row of `parts`: N rounded up to what the workgroup's waves hold.
+inline int64_t selective_padded(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+
+// ------------------------------------------------- short causal convolution
+
+constexpr int kConvTaps = 8;  // most taps per channel
+
+struct ConvPlan {
+  int64_t run_len, runs;  // tokens of a thread, and runs per sequence
+};
+ConvPlan conv_plan(int64_t B, int64_t T, int64_t D, sr_dtype dtype);
+
+struct ConvRequest {
+  sr_dtype dtype, w_dtype;
+  int64_t B, T, D;
+  int K;
+  const void* x;
+  int64_t ld_x;
+  const void *w, *bias;  // bias may be null
+  int silu;
+  const void* state;  // [B][K - 1][D] or null
+  const int32_t* lengths;
+  void *y, *last;  // last may be null
+  int64_t run_len, runs;
+  hipStream_t stream;
+  // The backward pass.
+  const void* dy;
+  int64_t ld_dy;
+  const void* dlast;  // may be null
+  void *dx, *dstate;  // dstate may be null
+  float *dw, *dbias;  // dbias may be null
+  float* parts;       // [B][runs][K + 1][D]
+};
+
+sr_status launch_conv(const ConvRequest& rq);
+sr_status launch_conv_backward(const ConvRequest& rq);
+sr_status launch_conv_step(const ConvRequest& rq);
+
+// ------------------------------------------------- root-mean-square norm
+
+constexpr int64_t kNormWidth = 16384;  // longest row
+
+struct NormRequest {
+  sr_dtype dtype, r_dtype, w_dtype;
+  int64_t M, D;
+  const void *x, *r;  // r may be null
+  int64_t ld_x, ld_r;
+  const void* w;
+  float eps;
+  void *total, *y;
+  int8_t* q;  // null: y
+  float* scale;
+  int64_t ld_q;
+  hipStream_t stream;
+  // The backward pass.
+  const void *t, *dy, *dt;  // dt may be null
+  int64_t ld_t, ld_dy, ld_dt;
+  void* dx;
+  float* dw;
+  float* parts;  // [norm_backward_blocks][D]
+};
+
+int64_t norm_backward_blocks(int64_t M, int64_t D);
+sr_status launch_norm(const NormRequest& rq);
+sr_status launch_norm_backward(const NormRequest& rq);
+
 // One MinMax step over n channels (x_next may alias x_prev).
 sr_status launch_minmax_step(const float* r, const float* s, const float* x_prev, float* x_next,
                              int64_t n, hipStream_t stream);
