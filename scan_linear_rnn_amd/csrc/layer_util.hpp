@@ -19,6 +19,14 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ uint16_t from_f32<uint16_t>(float x) { return uint16_t(bf16_bits(x)); }
 
+// The element at a byte offset from an address that all lanes share: loads take the
+// two as they are.
+template <typename T>
+__device__ __forceinline__ T* at_byte(T* base, uint32_t offset) {
+  using Byte = std::conditional_t<std::is_const_v<T>, const char, char>;
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(base) + offset);
+}
+
 // N neighbouring elements at any element: global loads and stores take any
 // address that is a multiple of the element's size.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -27,7 +35,11 @@ __device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
   if constexpr (sizeof(T) == 4) {
     __builtin_memcpy(v, __builtin_assume_aligned(p, 4), N * 4);
   } else {
-    uint32_t w[N / 2];
+    if constexpr (N == 1) {
+      v[0] = to_f32(*p);
+      return;
+    }
+    uint32_t w[(N + 1) / 2];
     __builtin_memcpy(w, __builtin_assume_aligned(p, 2), N * 2);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
@@ -41,7 +53,11 @@ __device__ __forceinline__ void store_n(T* p, const float (&v)[N]) {
   if constexpr (sizeof(T) == 4) {
     __builtin_memcpy(__builtin_assume_aligned(p, 4), v, N * 4);
   } else {
-    uint32_t w[N / 2];
+    if constexpr (N == 1) {
+      *p = from_f32<T>(v[0]);
+      return;
+    }
+    uint32_t w[(N + 1) / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
     __builtin_memcpy(__builtin_assume_aligned(p, 2), w, N * 2);
@@ -80,6 +96,38 @@ __device__ __forceinline__ void store4(T* p, f32x4 v, int n) {
   store_some(p, n, w);
 }
 
+// Q neighbouring elements as they stand in memory, for loads that are on the way
+// while something else is computed: their conversion waits for them.
+template <typename T, int Q>
+struct Raw {
+  static constexpr int kWords = (Q * int(sizeof(T)) + 3) / 4;
+  uint32_t w[kWords];
+};
+// kWhole: all Q exist; else the last of the n >= 1 is repeated (and waited for).
+template <bool kWhole, typename T, int Q>
+__device__ __forceinline__ void load_raw(const T* p, int n, Raw<T, Q>& r) {
+  if constexpr (Q * sizeof(T) == 2) {
+    r.w[0] = *p;
+  } else if constexpr (kWhole) {
+    __builtin_memcpy(r.w, __builtin_assume_aligned(p, sizeof(T)), sizeof(r.w));
+  } else {
+    T v[Q];
+#pragma unroll
+    for (int i = 0; i < Q; ++i) v[i] = p[i < n ? i : n - 1];
+    __builtin_memcpy(r.w, v, sizeof(r.w));
+  }
+}
+template <int Q>
+__device__ __forceinline__ void values(const Raw<float, Q>& r, float (&v)[Q]) {
+#pragma unroll
+  for (int i = 0; i < Q; ++i) v[i] = __uint_as_float(r.w[i]);
+}
+template <int Q>
+__device__ __forceinline__ void values(const Raw<uint16_t, Q>& r, float (&v)[Q]) {
+#pragma unroll
+  for (int i = 0; i < Q; ++i) v[i] = __uint_as_float(i % 2 ? r.w[i / 2] & 0xFFFF0000u : r.w[i / 2] << 16);
+}
+
 // A weight of either type.
 __device__ __forceinline__ float weight_at(const void* w, sr_dtype dtype, int64_t i) {
   return dtype == SR_BF16 ? to_f32(static_cast<const uint16_t*>(w)[i]) : static_cast<const float*>(w)[i];
@@ -98,6 +146,52 @@ __device__ __forceinline__ float softplus_f(float x) {
 // 1 / (1 + e^-x), to a few ulps.
 __device__ __forceinline__ float logistic_f(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * kLog2e));
+}
+
+// Lane n of each row of 16 lanes, in all lanes of the row: multiplications take
+// it as an operand of their own.
+template <int n>
+__device__ __forceinline__ float of_row(float x) {
+  return __uint_as_float(
+      uint32_t(__builtin_amdgcn_mov_dpp(int(__float_as_uint(x)), 0x150 + n, 0xF, 0xF, true)));
+}
+// sum_i m[i][n] x[i] with m[i][n] in lane n of each row of 16.  (The compiler does not
+// put such an operand into fused multiply-adds by itself.  The two wait states are
+// those between a vector instruction's result and its use across lanes.)
+template <int n>
+__device__ __forceinline__ float row_dot(const float (&m)[1], const float (&x)[1]) {
+  return of_row<n>(m[0]) * x[0];
+}
+template <int n>
+__device__ __forceinline__ float row_dot(const float (&m)[2], const float (&x)[2]) {
+  float sum;
+  asm("s_nop 1\n\t"
+      "v_mul_f32_dpp %0, %1, %3 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %2, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf"
+      : "=&v"(sum)
+      : "v"(m[0]), "v"(m[1]), "v"(x[0]), "v"(x[1]), "i"(n));
+  return sum;
+}
+template <int n>
+__device__ __forceinline__ float row_dot(const float (&m)[4], const float (&x)[4]) {
+  float sum;
+  asm("s_nop 1\n\t"
+      "v_mul_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %2, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %3, %7 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+      : "=&v"(sum)
+      : "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "i"(n));
+  return sum;
+}
+
+// Calls f with 0 .. n - 1 as constants.
+template <int n, typename F, int i = 0>
+__device__ __forceinline__ void unrolled(F f) {
+  if constexpr (i < n) {
+    f(std::integral_constant<int, i>{});
+    unrolled<n, F, i + 1>(f);
+  }
 }
 
 // Sums of the columns of parts [rows][cols] in fp32, always in the same order: 16

@@ -29,15 +29,16 @@ namespace {
 // kStates: the state that the chunk's tokens make of zero (P.ends) and the sum
 // of their steps (P.steps), and with P.marks what the chunk has made of zero in
 // front of each tile, with the sum of the steps so far.  Else: y from the chunk's own
-// start state, and the last state.
-template <typename T, int W, bool kStates>
+// start state, and the last state.  W waves of NS states per lane.
+//
+// While the waves go through tile k, each thread also prepares its part of tile
+// k + 1's steps, sums its part of tile k - 1's outputs and has tile k + 2's inputs on
+// their way: everything between two barriers is independent, one barrier per tile.
+template <typename T, int W, int NS, bool kStates, bool kWhole>
 __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) {
-  constexpr int kSlots = kTile * kLanes / 4;                    // four channels of one token each
-  constexpr int kPer = kSlots > W * 64 ? kSlots / (W * 64) : 1;  // a thread's
-  constexpr int kN = W * kNS;
-  __shared__ __align__(16) float2 s_step[kTile][kLanes];  // dt, dt u
-  __shared__ float s_b[kTile][kN], s_c[kStates ? 1 : kTile][kN];
-  __shared__ __align__(16) float s_y[kStates ? 1 : W][kTile][kLanes];
+  constexpr int Q = kTile / W;  // neighbouring channels of a token that a thread prepares
+  __shared__ __align__(16) float2 s_step[2][kTile][kLanes];  // dt, dt u
+  __shared__ __align__(16) float s_y[2][kStates ? 1 : W][kTile][kLanes];
   const Place p = place_of(P);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -46,19 +47,12 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
   const int64_t stop = first + P.chunk_len < P.T ? first + P.chunk_len : P.T;
   const int64_t end = length < stop ? length : stop;
 
-  const T* u = static_cast<const T*>(P.u);
-  const T* delta = static_cast<const T*>(P.delta);
-  const T* z = static_cast<const T*>(P.z);
-  const T* Bm = static_cast<const T*>(P.Bm);
-  const T* Cm = static_cast<const T*>(P.Cm);
-  T* y = static_cast<T*>(P.y);
-
   const int64_t d = p.c0 + lane;
-  const int n0 = wave * kNS;
+  const int n0 = wave * NS;
   const bool mine = lane < p.width;
-  float a2[kNS], h[kNS];
+  float a2[NS], h[NS];
 #pragma unroll
-  for (int i = 0; i < kNS; ++i) {
+  for (int i = 0; i < NS; ++i) {
     const bool is = mine && n0 + i < P.N;
     a2[i] = is ? P.A[d * P.N + n0 + i] * kLog2e : 0.0f;
     h[i] = 0.0f;
@@ -71,123 +65,182 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
     }
   }
 
-  int at[kPer], c4[kPer];  // a slot's token in the tile and first channel
-  f32x4 bias[kPer], skip[kPer], ru[kPer], rd[kPer], rz[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int slot = tid + j * W * 64;
-    at[j] = slot / (kLanes / 4);
-    c4[j] = slot % (kLanes / 4) * 4;
-    if (slot >= kSlots || c4[j] >= p.width) at[j] = kTile;  // nothing to do
-    bias[j] = skip[j] = rz[j] = f32x4{};
-    if (at[j] < kTile) {
-      const int n = p.width - c4[j];
-      if (P.bias) bias[j] = load4(P.bias + p.c0 + c4[j], n);
-      if (!kStates && P.skip) skip[j] = load4(P.skip + p.c0 + c4[j], n);
+  const int at = tid / (kLanes / Q), lc = tid % (kLanes / Q) * Q;  // a thread's token in the tile and first lane
+  const int c = lc < p.width ? lc : 0;                             // its channel; lanes without one repeat the first
+  const int nc = p.width - c;
+  float bias[Q], skip[Q];
+  load_some(P.bias + p.c0 + c, P.bias ? nc : 0, bias);
+  load_some(P.skip + p.c0 + c, !kStates && P.skip ? nc : 0, skip);
+  // B and C go from memory to where the recurrence takes them from: lane t of each
+  // row of 16 has the wave's states of a tile's token t.
+  const int bc_at = lane % 16;
+  const int64_t group0 = int64_t(p.group) * P.N + (n0 < P.N ? n0 : 0);
+  const int nn = n0 < P.N ? P.N - n0 : 1;
+  struct Inputs {
+    Raw<T, Q> u, delta, z;
+    Raw<T, NS> Bm, Cm;
+  };
+  const auto bytes = [](int t, int64_t ld, int i) { return uint32_t(t * int(ld) + i) * uint32_t(sizeof(T)); };
+  const uint32_t o_u = bytes(at, P.ld_u, c), o_d = bytes(at, P.ld_delta, c), o_z = bytes(at, P.ld_z, c),
+                 o_b = bytes(bc_at, P.ld_b, 0), o_c = bytes(bc_at, P.ld_c, 0);
+  // The inputs of the tile at t0, as they stand in memory; behind the sequence's
+  // last token that one again.
+  auto fetch = [&](int64_t t0, Inputs& in) {
+    t0 = t0 < P.T ? t0 : P.T - 1;
+    const int64_t row0 = p.b * P.T + t0;
+    uint32_t b_u = o_u, b_d = o_d, b_z = o_z, b_b = o_b, b_c = o_c;
+    if (t0 + kTile > P.T) {
+      const int last = int(P.T - 1 - t0), t = at < last ? at : last, tb = bc_at < last ? bc_at : last;
+      b_u = bytes(t, P.ld_u, c);
+      b_d = bytes(t, P.ld_delta, c);
+      b_z = bytes(t, P.ld_z, c);
+      b_b = bytes(tb, P.ld_b, 0);
+      b_c = bytes(tb, P.ld_c, 0);
     }
-  }
-  // The inputs of the slots of the tile at t0; zeros behind the end.
-  auto fetch = [&](int64_t t0) {
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.u) + row0 * P.ld_u + p.c0, b_u), nc, in.u);
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.delta) + row0 * P.ld_delta + p.c0, b_d), nc, in.delta);
+    if (!kStates && P.z) load_raw<kWhole>(at_byte(static_cast<const T*>(P.z) + row0 * P.ld_z + p.c0, b_z), nc, in.z);
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.Bm) + row0 * P.ld_b + group0, b_b), nn, in.Bm);
+    if constexpr (!kStates) load_raw<kWhole>(at_byte(static_cast<const T*>(P.Cm) + row0 * P.ld_c + group0, b_c), nn, in.Cm);
+  };
+  // Converts what was fetched for the tile at t0 and writes its steps.
+  auto prepare = [&](int64_t t0, int buffer, const Inputs& in, float (&bm)[NS], float (&cm)[NS]) {
+    float u[Q], dt[Q], du[Q];
+    values(in.u, u);
+    values(in.delta, dt);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      ru[j] = rd[j] = f32x4{};
-      if (at[j] < kTile && t0 + at[j] < end) {
-        const int64_t row = p.b * P.T + t0 + at[j], c = p.c0 + c4[j];
-        const int n = p.width - c4[j];
-        ru[j] = load4(u + row * P.ld_u + c, n);
-        rd[j] = load4(delta + row * P.ld_delta + c, n);
-        if (!kStates && z) rz[j] = load4(z + row * P.ld_z + c, n);
-      }
+    for (int e = 0; e < Q; ++e) dt[e] += bias[e];
+    if (P.softplus) {
+#pragma unroll
+      for (int e = 0; e < Q; ++e) dt[e] = softplus_f(dt[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < Q; ++e) du[e] = dt[e] * u[e];
+    values(in.Bm, bm);
+    if constexpr (!kStates) values(in.Cm, cm);
+    if (t0 + kTile > end) {  // behind the end the state stays, whatever stands there
+#pragma unroll
+      for (int e = 0; e < Q; ++e)
+        if (t0 + at >= end) dt[e] = du[e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (t0 + bc_at >= end) bm[i] = cm[i] = 0.0f;
+    }
+    if (!kWhole || n0 >= P.N) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (n0 + i >= P.N) bm[i] = cm[i] = 0.0f;
+    }
+    float pair[2 * Q];
+#pragma unroll
+    for (int e = 0; e < Q; ++e) {
+      pair[2 * e] = dt[e];
+      pair[2 * e + 1] = du[e];
+    }
+    __builtin_memcpy(__builtin_assume_aligned(&s_step[buffer][at][lc], Q > 1 ? 16 : 8), pair, 8 * Q);
+  };
+  // y of the tile at t0, whose shares are in `buffer`.
+  auto finish = [&](int64_t t0, int buffer, const Raw<T, Q>& ru, const Raw<T, Q>& rz) {
+    float u[Q], z[Q], sum[Q];
+    values(ru, u);
+#pragma unroll
+    for (int e = 0; e < Q; ++e) sum[e] = skip[e] * u[e];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      float part[Q];
+      __builtin_memcpy(part, __builtin_assume_aligned(&s_y[buffer][kStates ? 0 : w][at][lc], 4 * Q), 4 * Q);
+#pragma unroll
+      for (int e = 0; e < Q; ++e) sum[e] += part[e];
+    }
+    if (P.z) {
+      values(rz, z);
+#pragma unroll
+      for (int e = 0; e < Q; ++e) sum[e] *= z[e] * logistic_f(z[e]);
+    }
+    if (t0 >= first && t0 + at < end && lc < p.width) {
+      T* y = at_byte(static_cast<T*>(P.y) + (p.b * P.T + t0) * P.D + p.c0, bytes(at, P.D, c));
+      if constexpr (kWhole)
+        store_n(y, sum);
+      else
+        store_some(y, nc, sum);
     }
   };
   float total = 0.0f;  // of the steps (the first wave's)
-  fetch(first);
-  for (int64_t t0 = first; t0 < end; t0 += kTile) {
-    f32x4 cu[kPer], cz[kPer];
+  Inputs in[2];        // of the next tile and the one after it
+  Raw<T, Q> u0{}, z0{}, u1{}, z1{};  // of the present tile and the one before it
+  float b0[NS], c0[NS];
+  // One tile, at t0: the waves go through it, in[s] is the next one's input.
+  auto tile = [&](auto parity, int64_t t0) {
+    constexpr int s = decltype(parity)::value;
+    float2 step[kTile];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      cu[j] = ru[j];
-      cz[j] = rz[j];
-      if (at[j] >= kTile) continue;
-      f32x4 dt = rd[j] + bias[j];
-      if (P.softplus) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dt[e] = softplus_f(dt[e]);
-      }
-      const f32x4 du = dt * cu[j];
-      f32x4* to = reinterpret_cast<f32x4*>(&s_step[at[j]][c4[j]]);
-      to[0] = f32x4{dt[0], du[0], dt[1], du[1]};
-      to[1] = f32x4{dt[2], du[2], dt[3], du[3]};
-    }
-    for (int i = tid; i < kTile * kN; i += W * 64) {
-      const int t = i / kN, n = i % kN;
-      const bool is = t0 + t < end && n < P.N;
-      const int64_t row = p.b * P.T + t0 + t, off = int64_t(p.group) * P.N + n;
-      s_b[t][n] = is ? to_f32(Bm[row * P.ld_b + off]) : 0.0f;
-      if constexpr (!kStates) s_c[t][n] = is ? to_f32(Cm[row * P.ld_c + off]) : 0.0f;
-    }
-    fetch(t0 + kTile);
-    __syncthreads();
+    for (int t = 0; t < kTile; ++t) step[t] = s_step[s][t][lane];
+    float bm[NS], cm[NS];
+    prepare(t0 + kTile, s ^ 1, in[s], bm, cm);
+    const Raw<T, Q> un = in[s].u, zn = in[s].z;
+    fetch(t0 + 3 * kTile, in[s]);
     if constexpr (kStates) {
       if (P.marks != nullptr) {  // [tile][b][n][D], the steps as one more state
         const int64_t m = (t0 / kTile * P.B + p.b) * (P.N + 1);
 #pragma unroll
-        for (int i = 0; i < kNS; ++i)
+        for (int i = 0; i < NS; ++i)
           if (mine && n0 + i < P.N) P.marks[(m + n0 + i) * P.D + d] = h[i];
         if (mine && wave == 0) P.marks[(m + P.N) * P.D + d] = total;
       }
     }
-    const int count = int(end - t0 < kTile ? end - t0 : kTile);
-    auto step = [&](int t) {
-      const float2 s = s_step[t][lane];
-      total += s.x;
-      float sum = 0.0f;
+    unrolled<kTile>([&](auto token) {
+      constexpr int t = decltype(token)::value;
+      if constexpr (kStates) total += step[t].x;
 #pragma unroll
-      for (int i = 0; i < kNS; ++i) {
-        h[i] = fmaf(__builtin_amdgcn_exp2f(s.x * a2[i]), h[i], s.y * s_b[t][n0 + i]);
-        if constexpr (!kStates) sum = fmaf(h[i], s_c[t][n0 + i], sum);
-      }
-      if constexpr (!kStates) s_y[wave][t][lane] = sum;
-    };
-    if (count == kTile) {
+      for (int i = 0; i < NS; ++i)
+        h[i] = fmaf(__builtin_amdgcn_exp2f(step[t].x * a2[i]), h[i], of_row<t>(b0[i]) * step[t].y);
+      if constexpr (!kStates) s_y[s][wave][t][lane] = row_dot<t>(c0, h);
+    });
+    if constexpr (!kStates) {
+      finish(t0 - kTile, s ^ 1, u1, z1);
+      u1 = u0, z1 = z0;
+      u0 = un, z0 = zn;
+    }
 #pragma unroll
-      for (int t = 0; t < kTile; ++t) step(t);
-    } else {
-      for (int t = 0; t < count; ++t) step(t);
+    for (int i = 0; i < NS; ++i) {
+      b0[i] = bm[i];
+      c0[i] = cm[i];
     }
     __syncthreads();
-    if constexpr (!kStates) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (at[j] >= count) continue;
-        f32x4 sum = skip[j] * cu[j];
-#pragma unroll
-        for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const f32x4*>(&s_y[w][at[j]][c4[j]]);
-        if (z) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] *= cz[j][e] * logistic_f(cz[j][e]);
-        }
-        store4(y + (p.b * P.T + t0 + at[j]) * P.D + p.c0 + c4[j], sum, p.width - c4[j]);
-      }
+  };
+  if (first < end) {
+    fetch(first, in[1]);
+    fetch(first + kTile, in[0]);
+    prepare(first, 0, in[1], b0, c0);
+    u0 = in[1].u, z0 = in[1].z;
+    fetch(first + 2 * kTile, in[1]);
+    __syncthreads();
+    int64_t t0 = first;
+    for (; t0 + kTile < end; t0 += 2 * kTile) {
+      tile(std::integral_constant<int, 0>{}, t0);
+      tile(std::integral_constant<int, 1>{}, t0 + kTile);
+    }
+    if (t0 < end) {
+      tile(std::integral_constant<int, 0>{}, t0);
+      if constexpr (!kStates) finish(t0, 0, u1, z1);
+    } else {
+      if constexpr (!kStates) finish(t0 - kTile, 1, u1, z1);
     }
   }
   if constexpr (kStates) {
     const int64_t m = (int64_t(p.chunk) * P.B + p.b) * P.N;
 #pragma unroll
-    for (int i = 0; i < kNS; ++i)
+    for (int i = 0; i < NS; ++i)
       if (mine && n0 + i < P.N) P.ends[(m + n0 + i) * P.D + d] = h[i];
     if (mine && wave == 0) P.steps[(int64_t(p.chunk) * P.B + p.b) * P.D + d] = total;
   } else {
     // Rows behind the sequence's end are zero.
-    for (int64_t t0 = first > end ? first : end; t0 < stop; t0 += kTile) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (at[j] < kTile && t0 + at[j] < stop)
-          store4(y + (p.b * P.T + t0 + at[j]) * P.D + p.c0 + c4[j], f32x4{}, p.width - c4[j]);
-    }
+    const float none[Q] = {};
+    for (int64_t t = (first > end ? first : end) + at; t < stop; t += kTile)
+      if (lc < p.width) store_some(static_cast<T*>(P.y) + (p.b * P.T + t) * P.D + p.c0 + c, nc, none);
     if (P.h_last != nullptr && stop == P.T) {
 #pragma unroll
-      for (int i = 0; i < kNS; ++i)
+      for (int i = 0; i < NS; ++i)
         if (mine && n0 + i < P.N) P.h_last[(p.b * P.D + d) * P.N + n0 + i] = h[i];
     }
   }
@@ -285,25 +338,26 @@ __global__ __launch_bounds__(256) void step_kernel(const SelectiveRequest P) {
   }
 }
 
-template <typename T, int W>
+template <typename T, int W, int NS>
 void launch_scan(const SelectiveRequest& P, bool states, uint32_t blocks) {
-  if (states)
-    hipLaunchKernelGGL((scan_kernel<T, W, true>), dim3(blocks), dim3(W * 64), 0, P.stream, P);
+  auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(W * 64), 0, P.stream, P); };
+  if (P.D / P.G % (kTile / W) == 0 && P.N % NS == 0)
+    states ? run(scan_kernel<T, W, NS, true, true>) : run(scan_kernel<T, W, NS, false, true>);
   else
-    hipLaunchKernelGGL((scan_kernel<T, W, false>), dim3(blocks), dim3(W * 64), 0, P.stream, P);
+    states ? run(scan_kernel<T, W, NS, true, false>) : run(scan_kernel<T, W, NS, false, false>);
 }
 template <typename T>
 void launch_scan(const SelectiveRequest& P, bool states, uint32_t blocks) {
   if (P.N <= 4)
-    launch_scan<T, 1>(P, states, blocks);
+    launch_scan<T, 4, 1>(P, states, blocks);
   else if (P.N <= 8)
-    launch_scan<T, 2>(P, states, blocks);
+    launch_scan<T, 4, 2>(P, states, blocks);
   else if (P.N <= 16)
-    launch_scan<T, 4>(P, states, blocks);
+    launch_scan<T, 4, 4>(P, states, blocks);
   else if (P.N <= 32)
-    launch_scan<T, 8>(P, states, blocks);
+    launch_scan<T, 8, 4>(P, states, blocks);
   else
-    launch_scan<T, 16>(P, states, blocks);
+    launch_scan<T, 16, 4>(P, states, blocks);
 }
 
 template <typename T, int V>

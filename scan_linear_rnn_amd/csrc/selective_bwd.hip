@@ -29,8 +29,8 @@ namespace {
 
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float x) {
-  return __uint_as_float(uint32_t(
-      __builtin_amdgcn_update_dpp(0, int(__float_as_uint(x)), kCtrl, 0xF, 0xF, false)));
+  return __uint_as_float(
+      uint32_t(__builtin_amdgcn_mov_dpp(int(__float_as_uint(x)), kCtrl, 0xF, 0xF, true)));
 }
 
 // Sums of 64 values over the 64 lanes: lane l returns the sum of v[l].
