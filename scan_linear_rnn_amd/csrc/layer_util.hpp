@@ -140,7 +140,7 @@ __device__ __forceinline__ float softplus_f(float x) {
   const float e = __builtin_amdgcn_exp2f(-fabsf(x) * kLog2e);
   const float u = 1.0f + e, d = u - 1.0f;
   const float l = d > 0.0f ? __builtin_amdgcn_logf(u) * (kLn2 * e) * __builtin_amdgcn_rcpf(d) : e;
-  return x != x ? x : fmaxf(x, 0.0f) + l;
+  return fmaxf(x, 0.0f) + l;  // (a NaN is in l)
 }
 
 // 1 / (1 + e^-x), to a few ulps.
@@ -183,6 +183,30 @@ __device__ __forceinline__ float row_dot(const float (&m)[4], const float (&x)[4
       : "=&v"(sum)
       : "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "i"(n));
   return sum;
+}
+
+// y[i] += m[i][n] x with m[i][n] in lane n of each row of 16.
+template <int n>
+__device__ __forceinline__ void row_add(const float (&m)[1], float x, float (&y)[1]) {
+  y[0] += of_row<n>(m[0]) * x;
+}
+template <int n>
+__device__ __forceinline__ void row_add(const float (&m)[2], float x, float (&y)[2]) {
+  asm("s_nop 1\n\t"
+      "v_fmac_f32_dpp %0, %2, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %3, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf"
+      : "+&v"(y[0]), "+&v"(y[1])
+      : "v"(m[0]), "v"(m[1]), "v"(x), "i"(n));
+}
+template <int n>
+__device__ __forceinline__ void row_add(const float (&m)[4], float x, float (&y)[4]) {
+  asm("s_nop 1\n\t"
+      "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %5, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %2, %6, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %3, %7, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+      : "+&v"(y[0]), "+&v"(y[1]), "+&v"(y[2]), "+&v"(y[3])
+      : "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "v"(x), "i"(n));
 }
 
 // Calls f with 0 .. n - 1 as constants.

@@ -139,19 +139,22 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
     }
     __builtin_memcpy(__builtin_assume_aligned(&s_step[buffer][at][lc], Q > 1 ? 16 : 8), pair, 8 * Q);
   };
-  // y of the tile at t0, whose shares are in `buffer`.
-  auto finish = [&](int64_t t0, int buffer, const Raw<T, Q>& ru, const Raw<T, Q>& rz) {
+  // The waves' shares of y for a thread's token.
+  auto collect = [&](int buffer, float (&part)[W][Q]) {
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      __builtin_memcpy(part[w], __builtin_assume_aligned(&s_y[buffer][kStates ? 0 : w][at][lc], 4 * Q), 4 * Q);
+  };
+  // y of the tile at t0.
+  auto finish = [&](int64_t t0, const float (&part)[W][Q], const Raw<T, Q>& ru, const Raw<T, Q>& rz) {
     float u[Q], z[Q], sum[Q];
     values(ru, u);
 #pragma unroll
     for (int e = 0; e < Q; ++e) sum[e] = skip[e] * u[e];
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      float part[Q];
-      __builtin_memcpy(part, __builtin_assume_aligned(&s_y[buffer][kStates ? 0 : w][at][lc], 4 * Q), 4 * Q);
+    for (int w = 0; w < W; ++w)
 #pragma unroll
-      for (int e = 0; e < Q; ++e) sum[e] += part[e];
-    }
+      for (int e = 0; e < Q; ++e) sum[e] += part[w][e];
     if (P.z) {
       values(rz, z);
 #pragma unroll
@@ -175,6 +178,9 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
     float2 step[kTile];
 #pragma unroll
     for (int t = 0; t < kTile; ++t) step[t] = s_step[s][t][lane];
+    float part[W][Q];
+    if constexpr (!kStates) collect(s ^ 1, part);
+    __builtin_amdgcn_sched_barrier(0);  // all reads first: a wait for each would follow else
     float bm[NS], cm[NS];
     prepare(t0 + kTile, s ^ 1, in[s], bm, cm);
     const Raw<T, Q> un = in[s].u, zn = in[s].z;
@@ -197,7 +203,7 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
       if constexpr (!kStates) s_y[s][wave][t][lane] = row_dot<t>(c0, h);
     });
     if constexpr (!kStates) {
-      finish(t0 - kTile, s ^ 1, u1, z1);
+      finish(t0 - kTile, part, u1, z1);
       u1 = u0, z1 = z0;
       u0 = un, z0 = zn;
     }
@@ -220,11 +226,12 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
       tile(std::integral_constant<int, 0>{}, t0);
       tile(std::integral_constant<int, 1>{}, t0 + kTile);
     }
-    if (t0 < end) {
-      tile(std::integral_constant<int, 0>{}, t0);
-      if constexpr (!kStates) finish(t0, 0, u1, z1);
-    } else {
-      if constexpr (!kStates) finish(t0 - kTile, 1, u1, z1);
+    const bool odd = t0 < end;
+    if (odd) tile(std::integral_constant<int, 0>{}, t0);
+    if constexpr (!kStates) {
+      float part[W][Q];
+      collect(odd ? 0 : 1, part);
+      finish(odd ? t0 : t0 - kTile, part, u1, z1);
     }
   }
   if constexpr (kStates) {

@@ -16,7 +16,7 @@
 // exponential and one product away from the chunk's start.  A workgroup then owns
 // 64 channels of one chunk, a lane each, goes back over its tiles of 16
 // tokens, runs each forward into registers and back again.  The sums over
-// channels, dB and dC, are 64 values per wave and tile (16 tokens, 4 states) to be
+// channels, dB and dC, are 64 values each per wave and tile (16 tokens, 4 states) to be
 // summed over 64 lanes: a halving exchange (swaps of half waves, then of rows,
 // then DPP) leaves one sum in every lane at about two instructions per value,
 // where separate sums would take six.  They go out per 64 channels and
@@ -33,43 +33,61 @@ __device__ __forceinline__ float dpp(float x) {
       uint32_t(__builtin_amdgcn_mov_dpp(int(__float_as_uint(x)), kCtrl, 0xF, 0xF, true)));
 }
 
-// Sums of 64 values over the 64 lanes: lane l returns the sum of v[l].
-__device__ __forceinline__ float sum64(float (&v)[64], int lane) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {  // lanes below 32 take v[k], the others v[k + 32]
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 32]), false, false);
-    v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {  // rows of 16 lanes
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 16]), false, false);
-    v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  auto halve = [&](auto half, auto ctrl) {
-    constexpr int kHalf = decltype(half)::value;
-    const bool up = lane & kHalf;
+// One stage of sum_lanes: every lane adds the partner's number at lane ^ kBit (or, for 4,
+// at the mirrored place of its eight lanes), and of two numbers keeps one half of the sums.
+template <int kBit, int n>
+__device__ __forceinline__ void sum_stage(float (&v)[n], int lane) {
+  constexpr int kLeft = n > 64 ? 0 : n;
+  constexpr int kHalf = kLeft * kBit / 64;  // numbers left after this stage, none: one in several lanes
+  auto partner = [](float x) {
+    if constexpr (kBit == 8) return dpp<0x128>(x);  // row_ror:8
+    if constexpr (kBit == 4) return dpp<0x141>(x);  // row_half_mirror
+    if constexpr (kBit == 2) return dpp<0x4E>(x);   // quad_perm 2,3,0,1
+    return dpp<0xB1>(x);                            // quad_perm 1,0,3,2
+  };
+  if constexpr (kHalf == 0) {
+    v[0] += partner(v[0]);
+  } else {
 #pragma unroll
     for (int k = 0; k < kHalf; ++k) {
-      const float keep = up ? v[k + kHalf] : v[k], give = up ? v[k] : v[k + kHalf];
-      v[k] = keep + dpp<decltype(ctrl)::value>(give);
+      if constexpr (kBit == 32) {  // lanes below 32 keep v[k], the others v[k + kHalf]
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + kHalf]), false, false);
+        v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+      } else if constexpr (kBit == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + kHalf]), false, false);
+        v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+      } else {
+        const bool up = lane & kBit;
+        const float keep = up ? v[k + kHalf] : v[k], give = up ? v[k] : v[k + kHalf];
+        v[k] = keep + partner(give);
+      }
     }
-  };
-  halve(std::integral_constant<int, 8>{}, std::integral_constant<int, 0x128>{});  // row_ror:8
-  halve(std::integral_constant<int, 4>{}, std::integral_constant<int, 0x141>{});  // row_half_mirror
-  halve(std::integral_constant<int, 2>{}, std::integral_constant<int, 0x4E>{});   // quad_perm 2,3,0,1
-  halve(std::integral_constant<int, 1>{}, std::integral_constant<int, 0xB1>{});   // quad_perm 1,0,3,2
+  }
+}
+// Sums of n values (8, 16 or 32) over the 64 lanes: lane l returns the sum of v[l n / 64].
+template <int n>
+__device__ __forceinline__ float sum_lanes(float (&v)[n], int lane) {
+  sum_stage<32>(v, lane);
+  sum_stage<16>(v, lane);
+  sum_stage<8>(v, lane);
+  sum_stage<4>(v, lane);
+  sum_stage<2>(v, lane);
+  sum_stage<1>(v, lane);
   return v[0];
 }
 
+// The offsets of a thread's elements in a tile's rows, in bytes.
+template <typename T>
+__device__ __forceinline__ uint32_t bytes_of(int t, int64_t ld, int i) {
+  return uint32_t(t * int(ld) + i) * uint32_t(sizeof(T));
+}
+
 // The gradient that each chunk's own outputs send in front of it (P.gends):
-// g <- (g + ds C) a from its last token to its first.
-template <typename T, int W>
+// g <- (g + ds C) a from its last token to its first.  Tiles as in scan_kernel, last one first.
+template <typename T, int W, int NS, bool kWhole>
 __global__ __launch_bounds__(W * 64) void grad_ends_kernel(const SelectiveRequest P) {
-  constexpr int kSlots = kTile * kLanes / 4;
-  constexpr int kPer = kSlots > W * 64 ? kSlots / (W * 64) : 1;
-  constexpr int kN = W * kNS;
-  __shared__ __align__(16) float2 s_step[kTile][kLanes];  // dt, ds
-  __shared__ float s_c[kTile][kN];
+  constexpr int Q = kTile / W;
+  __shared__ __align__(16) float2 s_step[2][kTile][kLanes];  // dt, ds
   const Place p = place_of(P);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -77,77 +95,124 @@ __global__ __launch_bounds__(W * 64) void grad_ends_kernel(const SelectiveReques
   const int64_t first = int64_t(p.chunk) * P.chunk_len;
   const int64_t stop = first + P.chunk_len < P.T ? first + P.chunk_len : P.T;
   const int64_t end = length < stop ? length : stop;
-  const T* delta = static_cast<const T*>(P.delta);
-  const T* z = static_cast<const T*>(P.z);
-  const T* dy = static_cast<const T*>(P.dy);
-  const T* Cm = static_cast<const T*>(P.Cm);
   const int64_t d = p.c0 + lane;
-  const int n0 = wave * kNS;
+  const int n0 = wave * NS;
   const bool mine = lane < p.width;
-  float a2[kNS], g[kNS];
+  float a2[NS], g[NS];
 #pragma unroll
-  for (int i = 0; i < kNS; ++i) {
+  for (int i = 0; i < NS; ++i) {
     a2[i] = mine && n0 + i < P.N ? P.A[d * P.N + n0 + i] * kLog2e : 0.0f;
     g[i] = 0.0f;
   }
-  const int64_t tiles = end > first ? (end - first + kTile - 1) / kTile : 0;
-  for (int64_t k = tiles - 1; k >= 0; --k) {
-    const int64_t t0 = first + k * kTile;
+  const int at = tid / (kLanes / Q), lc = tid % (kLanes / Q) * Q;
+  const int c = lc < p.width ? lc : 0, nc = p.width - c, bc_at = lane % 16;
+  const int64_t group0 = int64_t(p.group) * P.N + (n0 < P.N ? n0 : 0);
+  const int nn = n0 < P.N ? P.N - n0 : 1;
+  float bias[Q];
+  load_some(P.bias + p.c0 + c, P.bias ? nc : 0, bias);
+  struct Inputs {
+    Raw<T, Q> delta, dy, z;
+    Raw<T, NS> Cm;
+  };
+  auto fetch = [&](int64_t t0, Inputs& in) {
+    t0 = t0 < first ? first : t0;
+    const int64_t row0 = p.b * P.T + t0;
+    const int last = int(P.T - 1 - t0), t = at < last ? at : last, tb = bc_at < last ? bc_at : last;
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.delta) + row0 * P.ld_delta + p.c0, bytes_of<T>(t, P.ld_delta, c)), nc, in.delta);
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.dy) + row0 * P.ld_dy + p.c0, bytes_of<T>(t, P.ld_dy, c)), nc, in.dy);
+    if (P.z) load_raw<kWhole>(at_byte(static_cast<const T*>(P.z) + row0 * P.ld_z + p.c0, bytes_of<T>(t, P.ld_z, c)), nc, in.z);
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.Cm) + row0 * P.ld_c + group0, bytes_of<T>(tb, P.ld_c, 0)), nn, in.Cm);
+  };
+  auto prepare = [&](int64_t t0, int buffer, const Inputs& in, float (&cm)[NS]) {
+    float dt[Q], ds[Q], z[Q];
+    values(in.delta, dt);
+    values(in.dy, ds);
+#pragma unroll
+    for (int e = 0; e < Q; ++e) dt[e] += bias[e];
+    if (P.softplus) {
+#pragma unroll
+      for (int e = 0; e < Q; ++e) dt[e] = softplus_f(dt[e]);
+    }
+    if (P.z) {
+      values(in.z, z);
+#pragma unroll
+      for (int e = 0; e < Q; ++e) ds[e] *= z[e] * logistic_f(z[e]);
+    }
+    values(in.Cm, cm);
+    if (t0 + kTile > end) {  // tokens behind the end have step 0 and gradient 0
+#pragma unroll
+      for (int e = 0; e < Q; ++e)
+        if (t0 + at >= end) dt[e] = ds[e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (t0 + bc_at >= end) cm[i] = 0.0f;
+    }
+    if (!kWhole || n0 >= P.N) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (n0 + i >= P.N) cm[i] = 0.0f;
+    }
+    float pair[2 * Q];
+#pragma unroll
+    for (int e = 0; e < Q; ++e) {
+      pair[2 * e] = dt[e];
+      pair[2 * e + 1] = ds[e];
+    }
+    __builtin_memcpy(__builtin_assume_aligned(&s_step[buffer][at][lc], Q > 1 ? 16 : 8), pair, 8 * Q);
+  };
+  Inputs in[2];
+  float c0[NS];
+  auto tile = [&](auto parity, int64_t t0) {
+    constexpr int s = decltype(parity)::value;
+    float2 step[kTile];
+#pragma unroll
+    for (int t = 0; t < kTile; ++t) step[t] = s_step[s][t][lane];
+    float cm[NS];
+    prepare(t0 - kTile, s ^ 1, in[s], cm);
+    fetch(t0 - 3 * kTile, in[s]);
+    unrolled<kTile>([&](auto token) {
+      constexpr int t = kTile - 1 - decltype(token)::value;
+      row_add<t>(c0, step[t].y, g);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) g[i] *= __builtin_amdgcn_exp2f(step[t].x * a2[i]);
+    });
+#pragma unroll
+    for (int i = 0; i < NS; ++i) c0[i] = cm[i];
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int slot = tid + j * W * 64, at = slot / (kLanes / 4), c4 = slot % (kLanes / 4) * 4;
-      const int n = p.width - c4;
-      if (slot >= kSlots || n <= 0) continue;
-      f32x4 dt{}, ds{};
-      if (t0 + at < end) {
-        const int64_t row = p.b * P.T + t0 + at, c = p.c0 + c4;
-        dt = load4(delta + row * P.ld_delta + c, n);
-        if (P.bias) dt += load4(P.bias + c, n);
-        ds = load4(dy + row * P.ld_dy + c, n);
-        f32x4 zz{};
-        if (z) zz = load4(z + row * P.ld_z + c, n);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (P.softplus) dt[e] = softplus_f(dt[e]);
-          if (z) ds[e] *= zz[e] * logistic_f(zz[e]);
-        }
-      }
-      f32x4* to = reinterpret_cast<f32x4*>(&s_step[at][c4]);
-      to[0] = f32x4{dt[0], ds[0], dt[1], ds[1]};
-      to[1] = f32x4{dt[2], ds[2], dt[3], ds[3]};
-    }
-    for (int i = tid; i < kTile * kN; i += W * 64) {
-      const int t = i / kN, n = i % kN;
-      s_c[t][n] = t0 + t < end && n < P.N ? to_f32(Cm[(p.b * P.T + t0 + t) * P.ld_c + int64_t(p.group) * P.N + n]) : 0.0f;
-    }
+  };
+  if (first < end) {
+    int64_t t0 = first + (end - 1 - first) / kTile * kTile;
+    fetch(t0, in[1]);
+    fetch(t0 - kTile, in[0]);
+    prepare(t0, 0, in[1], c0);
+    fetch(t0 - 2 * kTile, in[1]);
     __syncthreads();
-    // tokens behind the end have step 0 and gradient 0
-#pragma unroll
-    for (int t = kTile - 1; t >= 0; --t) {
-      const float2 s = s_step[t][lane];
-#pragma unroll
-      for (int i = 0; i < kNS; ++i) g[i] = fmaf(s.y, s_c[t][n0 + i], g[i]) * __builtin_amdgcn_exp2f(s.x * a2[i]);
+    for (; t0 - kTile >= first; t0 -= 2 * kTile) {
+      tile(std::integral_constant<int, 0>{}, t0);
+      tile(std::integral_constant<int, 1>{}, t0 - kTile);
     }
+    if (t0 >= first) tile(std::integral_constant<int, 0>{}, t0);
   }
   const int64_t m = (int64_t(p.chunk) * P.B + p.b) * P.N;
 #pragma unroll
-  for (int i = 0; i < kNS; ++i)
+  for (int i = 0; i < NS; ++i)
     if (mine && n0 + i < P.N) P.gends[(m + n0 + i) * P.D + d] = g[i];
 }
 
-// SG: groups of four states that each wave goes through one after another (two
-// where N is above 32).
-template <typename T, int W, int SG>
-__global__ __launch_bounds__(W * 64) void backward_kernel(const SelectiveRequest P) {
-  constexpr int kSlots = kTile * kLanes / 4;
-  constexpr int kPer = kSlots > W * 64 ? kSlots / (W * 64) : 1;
-  constexpr int kN = W * kNS * SG;
-  __shared__ __align__(16) f32x4 s_step[kTile][kLanes];  // dt, dt u, ds
-  __shared__ float s_b[kTile][kN], s_c[kTile][kN];
-  __shared__ __align__(16) float s_write[W][kTile][kLanes];  // the waves' shares of sum G B
-  __shared__ __align__(16) float s_decay[W][kTile][kLanes];  // of sum A q
-  __shared__ __align__(16) float s_y[W][kTile][kLanes];      // of sum C h
+// W waves of NS states per lane; SG: groups of W NS states that the waves go
+// through one after another.  Each wave prepares and finishes the tokens wave, wave + W,
+// .. of a tile, a channel per lane.  A tile takes two phases with a barrier each: its
+// states forwards and the gradients of its later eight tokens, then those of the
+// earlier eight; the next tile's steps are prepared, and the outputs of the eight
+// tokens before are finished, in between.
+template <typename T, int W, int NS, int SG, bool kGated>
+__global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequest P) {
+  constexpr int kN = W * NS * SG, kV = 8 * NS, kOwn = kTile / W, kHalf = kOwn / 2;
+  __shared__ float2 s_step[2][kTile][kLanes];                  // dt, dt u
+  __shared__ float s_ds[2][kTile][kLanes];
+  __shared__ float s_write[2][W][8][kLanes];                   // the waves' shares of sum G B
+  __shared__ float s_decay[2][W][8][kLanes];                   // of sum A q
+  __shared__ float s_y[2][W][8][kLanes];                       // of sum C h
   const Place p = place_of(P);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -155,23 +220,15 @@ __global__ __launch_bounds__(W * 64) void backward_kernel(const SelectiveRequest
   const int64_t first = int64_t(p.chunk) * P.chunk_len;
   const int64_t stop = first + P.chunk_len < P.T ? first + P.chunk_len : P.T;
   const int64_t end = length < stop ? length : stop;
-  const T* u = static_cast<const T*>(P.u);
-  const T* delta = static_cast<const T*>(P.delta);
-  const T* z = static_cast<const T*>(P.z);
-  const T* dy = static_cast<const T*>(P.dy);
-  const T* Bm = static_cast<const T*>(P.Bm);
-  const T* Cm = static_cast<const T*>(P.Cm);
-  T* du = static_cast<T*>(P.du);
-  T* ddelta = static_cast<T*>(P.ddelta);
-  T* dz = static_cast<T*>(P.dz);
-  const int64_t d = p.c0 + lane;
   const bool mine = lane < p.width;
-  float a[SG][kNS], G[SG][kNS], start[SG][kNS], dA[SG][kNS];
+  const int c = mine ? lane : 0, bc_at = lane % 16;
+  const int64_t d = p.c0 + c;
+  float a[SG][NS], G[SG][NS], start[SG][NS], dA[SG][NS];
 #pragma unroll
   for (int g = 0; g < SG; ++g)
 #pragma unroll
-    for (int i = 0; i < kNS; ++i) {
-      const int n = (g * W + wave) * kNS + i;
+    for (int i = 0; i < NS; ++i) {
+      const int n = (g * W + wave) * NS + i;
       const bool is = mine && n < P.N;
       const int64_t m = ((int64_t(p.chunk) * P.B + p.b) * P.N + n) * P.D + d, own = (p.b * P.D + d) * P.N + n;
       a[g][i] = is ? P.A[d * P.N + n] : 0.0f;
@@ -184,190 +241,262 @@ __global__ __launch_bounds__(W * 64) void backward_kernel(const SelectiveRequest
         if (P.dh_last) G[g][i] = P.dh_last[own];
       }
     }
-  int at[kPer], c4[kPer];
-  f32x4 bias[kPer], skip[kPer], dskip[kPer], dbias[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int slot = tid + j * W * 64;
-    at[j] = slot / (kLanes / 4);
-    c4[j] = slot % (kLanes / 4) * 4;
-    if (slot < kSlots && c4[j] >= p.width) {  // lanes without a channel add zeros to the sums over channels
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s_step[at[j]][c4[j] + e] = f32x4{};
-    }
-    if (slot >= kSlots || c4[j] >= p.width) at[j] = kTile;
-    bias[j] = skip[j] = dskip[j] = dbias[j] = f32x4{};
-    if (at[j] < kTile) {
-      if (P.bias) bias[j] = load4(P.bias + p.c0 + c4[j], p.width - c4[j]);
-      if (P.skip) skip[j] = load4(P.skip + p.c0 + c4[j], p.width - c4[j]);
-    }
-  }
-  const int64_t parts_row = (int64_t(p.group) * P.tiles_per_group + p.tile) * P.B + p.b;
-  const int64_t tiles = end > first ? (end - first + kTile - 1) / kTile : 0;
-  f32x4 ru[kPer], rd[kPer], rg[kPer], rz[kPer];
+  const float bias = P.bias ? P.bias[d] : 0.0f, skip = P.skip ? P.skip[d] : 0.0f;
+  float dskip = 0.0f, dbias = 0.0f;
+  // A tile's inputs as they stand in memory, and the states in front of it.
+  struct Inputs {
+    T u[kOwn], delta[kOwn], dy[kOwn], z[kOwn];
+    T Bm[SG][NS], Cm[SG][NS];
+    float mark[SG][NS], so_far;
+  } in;
   auto fetch = [&](int64_t t0) {
+    t0 = t0 > first ? t0 : first;
+    const int64_t row0 = p.b * P.T + t0;
+    const int last = int(P.T - 1 - t0), tb = bc_at < last ? bc_at : last;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      ru[j] = rd[j] = rg[j] = rz[j] = f32x4{};
-      if (at[j] < kTile && t0 + at[j] < end) {
-        const int64_t row = p.b * P.T + t0 + at[j], c = p.c0 + c4[j];
-        const int n = p.width - c4[j];
-        ru[j] = load4(u + row * P.ld_u + c, n);
-        rd[j] = load4(delta + row * P.ld_delta + c, n);
-        rg[j] = load4(dy + row * P.ld_dy + c, n);
-        if (z) rz[j] = load4(z + row * P.ld_z + c, n);
+    for (int j = 0; j < kOwn; ++j) {
+      const int t = wave + j * W < last ? wave + j * W : last;  // (uniform)
+      in.u[j] = (static_cast<const T*>(P.u) + (row0 + t) * P.ld_u + p.c0)[c];
+      in.delta[j] = (static_cast<const T*>(P.delta) + (row0 + t) * P.ld_delta + p.c0)[c];
+      in.dy[j] = (static_cast<const T*>(P.dy) + (row0 + t) * P.ld_dy + p.c0)[c];
+      if (kGated) in.z[j] = (static_cast<const T*>(P.z) + (row0 + t) * P.ld_z + p.c0)[c];
+    }
+    const int64_t m = (t0 / kTile * P.B + p.b) * (P.N + 1);
+    in.so_far = (P.marks + (m + P.N) * P.D + p.c0)[c];
+#pragma unroll
+    for (int g = 0; g < SG; ++g) {
+      const int n0 = (g * W + wave) * NS;
+      const T *Bm = static_cast<const T*>(P.Bm) + row0 * P.ld_b + int64_t(p.group) * P.N,
+              *Cm = static_cast<const T*>(P.Cm) + row0 * P.ld_c + int64_t(p.group) * P.N;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int n = n0 + i < P.N ? n0 + i : P.N - 1;  // (uniform)
+        in.Bm[g][i] = *at_byte(Bm + n, bytes_of<T>(tb, P.ld_b, 0));
+        in.Cm[g][i] = *at_byte(Cm + n, bytes_of<T>(tb, P.ld_c, 0));
+      }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) in.mark[g][i] = (P.marks + (m + (n0 + i < P.N ? n0 + i : P.N)) * P.D + p.c0)[c];
+    }
+  };
+  struct Tokens {
+    float u[kOwn], x[kOwn], dy[kOwn], z[kOwn], dt[kOwn];
+  };
+  struct States {
+    float b[SG][NS], c[SG][NS], h[SG][NS];
+  };
+  // Converts what was fetched for the tile at t0 and writes its steps.
+  auto prepare = [&](int64_t t0, int buffer, Tokens& k, States& n) {
+    const int count = int(end - t0 < kTile ? end - t0 : kTile);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const int t = wave + j * W;
+      const bool live = mine && t < count;  // what does not exist adds zeros, and the state passes
+      k.u[j] = live ? to_f32(in.u[j]) : 0.0f;
+      k.x[j] = to_f32(in.delta[j]) + bias;
+      k.dy[j] = live ? to_f32(in.dy[j]) : 0.0f;
+      const float soft = softplus_f(k.x[j]);
+      k.dt[j] = t >= count ? 0.0f : P.softplus ? soft : k.x[j];
+      float ds = k.dy[j];
+      if (kGated) {
+        k.z[j] = live ? to_f32(in.z[j]) : 0.0f;
+        ds *= k.z[j] * logistic_f(k.z[j]);
+      }
+      s_step[buffer][t][lane] = float2{k.dt[j], k.dt[j] * k.u[j]};
+      s_ds[buffer][t][lane] = ds;
+    }
+#pragma unroll
+    for (int g = 0; g < SG; ++g) {
+      const int n0 = (g * W + wave) * NS;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const bool is = bc_at < count && n0 + i < P.N;
+        n.b[g][i] = is ? to_f32(in.Bm[g][i]) : 0.0f;
+        n.c[g][i] = is ? to_f32(in.Cm[g][i]) : 0.0f;
+        n.h[g][i] = mine && n0 + i < P.N ? in.mark[g][i] : 0.0f;
+        // a zero state stays zero however its factor overflows
+        const float grown = fmaf(__builtin_amdgcn_exp2f(in.so_far * (a[g][i] * kLog2e)), start[g][i], n.h[g][i]);
+        n.h[g][i] = start[g][i] != 0.0f ? grown : n.h[g][i];
       }
     }
   };
-  if (tiles > 0) fetch(first + (tiles - 1) * kTile);
-  for (int64_t k = tiles - 1; k >= 0; --k) {
-    const int64_t t0 = first + k * kTile;
-    const int count = int(end - t0 < kTile ? end - t0 : kTile);
-    f32x4 cu[kPer], cx[kPer], cg[kPer], cz[kPer], cdt[kPer];
+  // The waves' shares for a thread's tokens in a half of a tile, read ahead of their use.
+  struct Shares {
+    float write[kHalf][W], decay[kHalf][W], y[kHalf][kGated ? W : 1];
+  };
+  auto collect = [&](auto half, Shares& s) {
+    constexpr int kSide = decltype(half)::value;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      cu[j] = ru[j];
-      cg[j] = rg[j];
-      cz[j] = rz[j];
-      cx[j] = rd[j] + bias[j];
-      if (at[j] >= kTile) continue;
-      f32x4 dt = cx[j], ds = cg[j];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (P.softplus) dt[e] = softplus_f(dt[e]);
-        if (z) ds[e] *= cz[j][e] * logistic_f(cz[j][e]);
-      }
-      if (at[j] >= count) dt = f32x4{};  // and u = dy = 0: the state and its gradient pass
-      cdt[j] = dt;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s_step[at[j]][c4[j] + e] = f32x4{dt[e], dt[e] * cu[j][e], ds[e], 0.0f};
-    }
-    for (int i = tid; i < kTile * kN; i += W * 64) {
-      const int t = i / kN, n = i % kN;
-      const bool is = t < count && n < P.N;
-      const int64_t row = p.b * P.T + t0 + t, off = int64_t(p.group) * P.N + n;
-      s_b[t][n] = is ? to_f32(Bm[row * P.ld_b + off]) : 0.0f;
-      s_c[t][n] = is ? to_f32(Cm[row * P.ld_c + off]) : 0.0f;
-    }
-    if (k > 0) fetch(t0 - kTile);
-    __syncthreads();
-    const int64_t m = (t0 / kTile * P.B + p.b) * (P.N + 1);
-    const float so_far = mine ? P.marks[(m + P.N) * P.D + d] : 0.0f;
-#pragma unroll
-    for (int g = 0; g < SG; ++g) {
-      const int n0 = (g * W + wave) * kNS;
-      float h[kNS], hp[kTile][kNS], decay[kTile][kNS], v[64];
-#pragma unroll
-      for (int i = 0; i < kNS; ++i) {
-        h[i] = mine && n0 + i < P.N ? P.marks[(m + n0 + i) * P.D + d] : 0.0f;
-        if (start[g][i] != 0.0f)  // a zero state stays zero however its factor overflows
-          h[i] = fmaf(__builtin_amdgcn_exp2f(so_far * (a[g][i] * kLog2e)), start[g][i], h[i]);
-      }
-#pragma unroll
-      for (int t = 0; t < kTile; ++t) {
-        const f32x4 s = s_step[t][lane];
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kNS; ++i) {
-          hp[t][i] = h[i];
-          decay[t][i] = __builtin_amdgcn_exp2f(s[0] * (a[g][i] * kLog2e));
-          h[i] = fmaf(decay[t][i], h[i], s[1] * s_b[t][n0 + i]);
-          sum = fmaf(h[i], s_c[t][n0 + i], sum);
-          v[t * kNS + i] = s[2] * h[i];
-        }
-        if (z) s_y[wave][t][lane] = g == 0 ? sum : s_y[wave][t][lane] + sum;
-      }
-      const int64_t to = ((parts_row * P.T + t0 + lane / kNS) * 2) * kN + n0 + lane % kNS;
-      const float dC = sum64(v, lane);
-      if (lane / kNS < count) P.parts[to + kN] = dC;
-#pragma unroll
-      for (int t = kTile - 1; t >= 0; --t) {
-        const f32x4 s = s_step[t][lane];
-        float through = 0.0f, rate = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kNS; ++i) {
-          G[g][i] = fmaf(s[2], s_c[t][n0 + i], G[g][i]);
-          through = fmaf(G[g][i], s_b[t][n0 + i], through);
-          v[t * kNS + i] = G[g][i] * s[1];
-          G[g][i] *= decay[t][i];
-          const float q = G[g][i] * hp[t][i];
-          rate = fmaf(q, a[g][i], rate);
-          dA[g][i] = fmaf(q, s[0], dA[g][i]);
-        }
-        s_write[wave][t][lane] = g == 0 ? through : s_write[wave][t][lane] + through;
-        s_decay[wave][t][lane] = g == 0 ? rate : s_decay[wave][t][lane] + rate;
-      }
-      const float dB = sum64(v, lane);
-      if (lane / kNS < count) P.parts[to] = dB;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (at[j] >= count) continue;
-      f32x4 through{}, rate{}, sum = skip[j] * cu[j], gx, gz;
+    for (int j = 0; j < kHalf; ++j)
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        through += *reinterpret_cast<const f32x4*>(&s_write[w][at[j]][c4[j]]);
-        rate += *reinterpret_cast<const f32x4*>(&s_decay[w][at[j]][c4[j]]);
-        if (z) sum += *reinterpret_cast<const f32x4*>(&s_y[w][at[j]][c4[j]]);
+        const int r = wave + j * W;
+        s.write[j][w] = s_write[kSide][w][r][lane];
+        s.decay[j][w] = s_decay[kSide][w][r][lane];
+        if (kGated) s.y[j][w] = s_y[kSide][w][r][lane];
       }
-      f32x4 ds = cg[j];
-      gx = cu[j] * through + rate;
+    __builtin_amdgcn_sched_barrier(0);  // where they stand: a wait for each would follow else
+  };
+  // The gradients of a thread's tokens in the half of the tile at t0.
+  auto finish = [&](int64_t t0, auto half, const Tokens& k, const Shares& shares) {
+    constexpr int kSide = decltype(half)::value;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (P.softplus) gx[e] *= logistic_f(cx[j][e]);
-        if (z) {
-          const float s = logistic_f(cz[j][e]);
-          gz[e] = cg[j][e] * sum[e] * (s * fmaf(cz[j][e], 1.0f - s, 1.0f));
-          ds[e] *= cz[j][e] * s;
+    for (int jj = 0; jj < kHalf; ++jj) {
+      const int j = kSide * kHalf + jj, t = wave + j * W;
+      float through = 0.0f, rate = 0.0f, sum = skip * k.u[j];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        through += shares.write[jj][w];
+        rate += shares.decay[jj][w];
+        if (kGated) sum += shares.y[jj][w];
+      }
+      float ds = k.dy[j], gz = 0.0f, gx = fmaf(k.u[j], through, rate);
+      if (kGated) {
+        const float s = logistic_f(k.z[j]);
+        gz = k.dy[j] * sum * (s * fmaf(k.z[j], 1.0f - s, 1.0f));
+        ds *= k.z[j] * s;
+      }
+      const float slope = logistic_f(k.x[j]);
+      gx *= P.softplus ? slope : 1.0f;
+      if (t0 + t < end && mine) {
+        dskip = fmaf(ds, k.u[j], dskip);
+        dbias += gx;
+        const int64_t row = (p.b * P.T + t0 + t) * P.D + p.c0;
+        (static_cast<T*>(P.du) + row)[c] = from_f32<T>(fmaf(k.dt[j], through, skip * ds));
+        (static_cast<T*>(P.ddelta) + row)[c] = from_f32<T>(gx);
+        if (kGated) (static_cast<T*>(P.dz) + row)[c] = from_f32<T>(gz);
+      }
+    }
+  };
+  const int64_t parts_row = (int64_t(p.group) * P.tiles_per_group + p.tile) * P.B + p.b;
+  const int64_t last_tile = first + (end - 1 - first) / kTile * kTile;
+  constexpr std::integral_constant<int, 0> kEarly{};
+  constexpr std::integral_constant<int, 1> kLate{};
+  Tokens now, before{};  // of the present tile and the one that came before it, which is later in time
+  States n;
+  if (first < end) {
+    fetch(last_tile);
+    prepare(last_tile, 0, now, n);
+    fetch(last_tile - kTile);
+    __syncthreads();
+  }
+  int buffer = 0;
+  for (int64_t t0 = last_tile; first < end && t0 >= first; t0 -= kTile, buffer ^= 1) {
+    const int count = int(end - t0 < kTile ? end - t0 : kTile);
+    float2 step[kTile];
+    float ds_of[kTile];
+#pragma unroll
+    for (int t = 0; t < kTile; ++t) {
+      step[t] = s_step[buffer][t][lane];
+      ds_of[t] = s_ds[buffer][t][lane];
+    }
+    float h[SG][kTile + 1][NS], decay[SG][kTile][NS];
+#pragma unroll
+    for (int g = 0; g < SG; ++g) {
+      float a2[NS];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        h[g][0][i] = n.h[g][i];
+        a2[i] = a[g][i] * kLog2e;
+      }
+      unrolled<kTile>([&](auto token) {
+        constexpr int t = decltype(token)::value;
+        const float2 s = step[t];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          decay[g][t][i] = __builtin_amdgcn_exp2f(s.x * a2[i]);
+          h[g][t + 1][i] = fmaf(decay[g][t][i], h[g][t][i], of_row<t>(n.b[g][i]) * s.y);
+        }
+      });
+    }
+    // Back over eight tokens; their products for dB and dC take the registers that
+    // their states and decays leave.
+    auto back = [&](auto half) {
+      constexpr int kSide = decltype(half)::value;
+#pragma unroll
+      for (int g = 0; g < SG; ++g) {
+        float vb[kV], vc[kV];
+        unrolled<8>([&](auto token) {
+          constexpr int k = 7 - decltype(token)::value, t = 8 * kSide + k;
+          const float2 s = step[t];
+          const float ds = ds_of[t];
+          row_add<t>(n.c[g], ds, G[g]);
+          const float through = row_dot<t>(n.b[g], G[g]);
+          float rate = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            vc[k * NS + i] = ds * h[g][t + 1][i];
+            vb[k * NS + i] = G[g][i] * s.y;
+            G[g][i] *= decay[g][t][i];
+            const float q = G[g][i] * h[g][t][i];
+            rate = fmaf(q, a[g][i], rate);
+            dA[g][i] = fmaf(q, s.x, dA[g][i]);
+          }
+          s_write[kSide][wave][k][lane] = g == 0 ? through : s_write[kSide][wave][k][lane] + through;
+          s_decay[kSide][wave][k][lane] = g == 0 ? rate : s_decay[kSide][wave][k][lane] + rate;
+          if (kGated) {
+            const float sum = row_dot<t>(n.c[g], h[g][t + 1]);
+            s_y[kSide][wave][k][lane] = g == 0 ? sum : s_y[kSide][wave][k][lane] + sum;
+          }
+        });
+        // lane l has the sums of value l kV / 64: of token l kV / 64 / NS, state l kV / 64 % NS
+        const float dC = sum_lanes(vc, lane), dB = sum_lanes(vb, lane);
+        const int k = lane * kV / 64, t = 8 * kSide + k / NS;
+        if (lane % (64 / kV) == 0 && t < count) {
+          float* to = P.parts + ((parts_row * P.T + t0 + t) * 2) * kN + (g * W + wave) * NS + k % NS;
+          to[0] = dB;
+          to[kN] = dC;
         }
       }
-      dskip[j] += ds * cu[j];
-      dbias[j] += gx;
-      const int64_t o = (p.b * P.T + t0 + at[j]) * P.D + p.c0 + c4[j];
-      const int n = p.width - c4[j];
-      store4(du + o, cdt[j] * through + skip[j] * ds, n);
-      store4(ddelta + o, gx, n);
-      if (z) store4(dz + o, gz, n);
+    };
+    Shares shares;
+    collect(kEarly, shares);
+    back(kLate);
+    if (t0 != last_tile) finish(t0 + kTile, kEarly, before, shares);
+    __syncthreads();
+    collect(kLate, shares);
+    back(kEarly);
+    finish(t0, kLate, now, shares);
+    before = now;
+    if (t0 > first) {
+      prepare(t0 - kTile, buffer ^ 1, now, n);
+      fetch(t0 - 2 * kTile);
     }
+    __syncthreads();
+  }
+  if (first < end) {
+    Shares shares;
+    collect(kEarly, shares);
+    finish(first, kEarly, before, shares);
   }
   // Rows behind the sequence's end are zero.
-  for (int64_t t0 = first > end ? first : end; t0 < stop; t0 += kTile) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (at[j] >= kTile || t0 + at[j] >= stop) continue;
-      const int64_t o = (p.b * P.T + t0 + at[j]) * P.D + p.c0 + c4[j];
-      const int n = p.width - c4[j];
-      store4(du + o, f32x4{}, n);
-      store4(ddelta + o, f32x4{}, n);
-      if (z) store4(dz + o, f32x4{}, n);
-    }
+  for (int64_t t = (first > end ? first : end) + wave; t < stop; t += W) {
+    const int64_t row = (p.b * P.T + t) * P.D + p.c0;
+    if (!mine) continue;
+    (static_cast<T*>(P.du) + row)[c] = T(0);
+    (static_cast<T*>(P.ddelta) + row)[c] = T(0);
+    if (kGated) (static_cast<T*>(P.dz) + row)[c] = T(0);
   }
   const int64_t own = p.b * P.chunks + p.chunk;
 #pragma unroll
   for (int g = 0; g < SG; ++g)
 #pragma unroll
-    for (int i = 0; i < kNS; ++i) {
-      const int n = (g * W + wave) * kNS + i;
-      if (!mine || n >= P.N) continue;
-      P.aparts[(own * (P.N + 2) + n) * P.D + d] = dA[g][i];
-      if (P.dh0 != nullptr && p.chunk == 0) P.dh0[(p.b * P.D + d) * P.N + n] = G[g][i];
+    for (int i = 0; i < NS; ++i) {
+      const int k = (g * W + wave) * NS + i;
+      if (!mine || k >= P.N) continue;
+      P.aparts[(own * (P.N + 2) + k) * P.D + d] = dA[g][i];
+      if (P.dh0 != nullptr && p.chunk == 0) P.dh0[(p.b * P.D + d) * P.N + k] = G[g][i];
     }
-  // The slots' sums over tokens, then over the 16 tokens of a tile.
+  // The waves' sums over their tokens.
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (at[j] < kTile) {
-      *reinterpret_cast<f32x4*>(&s_write[0][at[j]][c4[j]]) = dskip[j];
-      *reinterpret_cast<f32x4*>(&s_decay[0][at[j]][c4[j]]) = dbias[j];
-    }
+  s_write[0][wave][0][lane] = dskip;
+  s_write[0][wave][1][lane] = dbias;
   __syncthreads();
   if (wave == 0 && mine) {
     float sk = 0.0f, bi = 0.0f;
 #pragma unroll
-    for (int t = 0; t < kTile; ++t) {
-      sk += s_write[0][t][lane];
-      bi += s_decay[0][t][lane];
+    for (int w = 0; w < W; ++w) {
+      sk += s_write[0][w][0][lane];
+      bi += s_write[0][w][1][lane];
     }
     P.aparts[(own * (P.N + 2) + P.N) * P.D + d] = sk;
     P.aparts[(own * (P.N + 2) + P.N + 1) * P.D + d] = bi;
@@ -407,41 +536,50 @@ __global__ __launch_bounds__(1024) void reduce_channels_kernel(const SelectiveRe
   });
 }
 
-template <typename T, int W, int SG>
-void launch_main(const SelectiveRequest& P, uint32_t blocks) {
-  hipLaunchKernelGGL((backward_kernel<T, W, SG>), dim3(blocks), dim3(W * 64), 0, P.stream, P);
-}
 template <typename T>
 void launch_all(const SelectiveRequest& P) {
   const uint32_t blocks = uint32_t(P.B * P.G * P.tiles_per_group * P.chunks);
+  auto either = [&](auto* gated, auto* plain, int w) {
+    if (P.z)
+      hipLaunchKernelGGL(gated, dim3(blocks), dim3(w * 64), 0, P.stream, P);
+    else
+      hipLaunchKernelGGL(plain, dim3(blocks), dim3(w * 64), 0, P.stream, P);
+  };
   if (P.N <= 4)
-    launch_main<T, 1, 1>(P, blocks);
+    either(backward_kernel<T, 4, 1, 1, true>, backward_kernel<T, 4, 1, 1, false>, 4);
   else if (P.N <= 8)
-    launch_main<T, 2, 1>(P, blocks);
+    either(backward_kernel<T, 4, 2, 1, true>, backward_kernel<T, 4, 2, 1, false>, 4);
   else if (P.N <= 16)
-    launch_main<T, 4, 1>(P, blocks);
+    either(backward_kernel<T, 8, 2, 1, true>, backward_kernel<T, 8, 2, 1, false>, 8);
   else if (P.N <= 32)
-    launch_main<T, 8, 1>(P, blocks);
+    either(backward_kernel<T, 8, 2, 2, true>, backward_kernel<T, 8, 2, 2, false>, 8);
   else
-    launch_main<T, 8, 2>(P, blocks);
+    either(backward_kernel<T, 8, 2, 4, true>, backward_kernel<T, 8, 2, 4, false>, 8);
   const int padded = int(selective_padded(P.N));
   const int64_t n = P.B * P.T * P.G * 2 * padded;
   if (n > 0) hipLaunchKernelGGL(reduce_tokens_kernel<T>, dim3(uint32_t((n + 255) / 256)), dim3(256), 0, P.stream, P, padded);
 }
-template <typename T>
+template <typename T, int W, int NS>
 void launch_ends(const SelectiveRequest& P) {
   const uint32_t blocks = uint32_t(P.B * P.G * P.tiles_per_group * P.chunks);
-  auto run = [&](auto* kernel, int W) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(W * 64), 0, P.stream, P); };
-  if (P.N <= 4)
-    run(grad_ends_kernel<T, 1>, 1);
-  else if (P.N <= 8)
-    run(grad_ends_kernel<T, 2>, 2);
-  else if (P.N <= 16)
-    run(grad_ends_kernel<T, 4>, 4);
-  else if (P.N <= 32)
-    run(grad_ends_kernel<T, 8>, 8);
+  auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(W * 64), 0, P.stream, P); };
+  if (P.D / P.G % (kTile / W) == 0 && P.N % NS == 0)
+    run(grad_ends_kernel<T, W, NS, true>);
   else
-    run(grad_ends_kernel<T, 16>, 16);
+    run(grad_ends_kernel<T, W, NS, false>);
+}
+template <typename T>
+void launch_ends(const SelectiveRequest& P) {
+  if (P.N <= 4)
+    launch_ends<T, 4, 1>(P);
+  else if (P.N <= 8)
+    launch_ends<T, 4, 2>(P);
+  else if (P.N <= 16)
+    launch_ends<T, 4, 4>(P);
+  else if (P.N <= 32)
+    launch_ends<T, 8, 4>(P);
+  else
+    launch_ends<T, 16, 4>(P);
 }
 
 sr_status launched(const char* what) {
