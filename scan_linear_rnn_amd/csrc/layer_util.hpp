@@ -17,7 +17,7 @@ __device__ __forceinline__ T from_f32(float x);
 template <>
 __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
-__device__ __forceinline__ uint16_t from_f32<uint16_t>(float x) { return uint16_t(bf16_bits(x)); }
+__device__ __forceinline__ uint16_t from_f32<uint16_t>(float x) { return uint16_t(bf16_pair(x, 0.0f)); }
 
 // The element at a byte offset from an address that all lanes share: loads take the
 // two as they are.
@@ -126,6 +126,36 @@ template <int Q>
 __device__ __forceinline__ void values(const Raw<uint16_t, Q>& r, float (&v)[Q]) {
 #pragma unroll
   for (int i = 0; i < Q; ++i) v[i] = __uint_as_float(i % 2 ? r.w[i / 2] & 0xFFFF0000u : r.w[i / 2] << 16);
+}
+
+// Stores of n elements at a byte offset from an address that all lanes share,
+// dropped where the offset is kNowhere: without a branch, so that the loads in
+// flight can be told from the stores behind them and waited for alone.  The
+// elements are aligned as a whole.
+constexpr uint32_t kNowhere = 0xFFFFFFFFu;
+template <typename T, int N>
+__device__ __forceinline__ void store_at(T* base, uint32_t offset, const float (&v)[N]) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, 0x7FFFFFFF, 0x00020000);
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (N == 1) {
+      __builtin_amdgcn_raw_buffer_store_b16(from_f32<uint16_t>(v[0]), rsrc, int(offset), 0, 0);
+    } else if constexpr (N == 2) {
+      __builtin_amdgcn_raw_buffer_store_b32(bf16_pair(v[0], v[1]), rsrc, int(offset), 0, 0);
+    } else {
+      typedef unsigned int Two __attribute__((ext_vector_type(2)));
+      __builtin_amdgcn_raw_buffer_store_b64(Two{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}, rsrc, int(offset), 0, 0);
+    }
+  } else {
+    typedef unsigned int Two __attribute__((ext_vector_type(2)));
+    typedef unsigned int Four __attribute__((ext_vector_type(4)));
+    const auto bits = [&](int i) { return __float_as_uint(v[i]); };
+    if constexpr (N == 1)
+      __builtin_amdgcn_raw_buffer_store_b32(bits(0), rsrc, int(offset), 0, 0);
+    else if constexpr (N == 2)
+      __builtin_amdgcn_raw_buffer_store_b64(Two{bits(0), bits(1)}, rsrc, int(offset), 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b128(Four{bits(0), bits(1), bits(2), bits(3)}, rsrc, int(offset), 0, 0);
+  }
 }
 
 // A weight of either type.

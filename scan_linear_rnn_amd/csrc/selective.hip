@@ -160,12 +160,12 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
 #pragma unroll
       for (int e = 0; e < Q; ++e) sum[e] *= z[e] * logistic_f(z[e]);
     }
-    if (t0 >= first && t0 + at < end && lc < p.width) {
-      T* y = at_byte(static_cast<T*>(P.y) + (p.b * P.T + t0) * P.D + p.c0, bytes(at, P.D, c));
-      if constexpr (kWhole)
-        store_n(y, sum);
-      else
-        store_some(y, nc, sum);
+    const bool live = t0 >= first && t0 + at < end && lc < p.width;
+    T* y = static_cast<T*>(P.y) + (p.b * P.T + t0) * P.D + p.c0;
+    if constexpr (kWhole) {
+      store_at(y, live ? bytes(at, P.D, c) : kNowhere, sum);
+    } else {
+      if (live) store_some(at_byte(y, bytes(at, P.D, c)), nc, sum);
     }
   };
   float total = 0.0f;  // of the steps (the first wave's)
@@ -348,7 +348,8 @@ __global__ __launch_bounds__(256) void step_kernel(const SelectiveRequest P) {
 template <typename T, int W, int NS>
 void launch_scan(const SelectiveRequest& P, bool states, uint32_t blocks) {
   auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(W * 64), 0, P.stream, P); };
-  if (P.D / P.G % (kTile / W) == 0 && P.N % NS == 0)
+  constexpr int Q = kTile / W;
+  if (P.D / P.G % Q == 0 && P.N % NS == 0 && reinterpret_cast<uintptr_t>(P.y) % (Q * sizeof(T)) == 0)
     states ? run(scan_kernel<T, W, NS, true, true>) : run(scan_kernel<T, W, NS, false, true>);
   else
     states ? run(scan_kernel<T, W, NS, true, false>) : run(scan_kernel<T, W, NS, false, false>);

@@ -357,14 +357,15 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
       }
       const float slope = logistic_f(k.x[j]);
       gx *= P.softplus ? slope : 1.0f;
-      if (t0 + t < end && mine) {
-        dskip = fmaf(ds, k.u[j], dskip);
-        dbias += gx;
-        const int64_t row = (p.b * P.T + t0 + t) * P.D + p.c0;
-        (static_cast<T*>(P.du) + row)[c] = from_f32<T>(fmaf(k.dt[j], through, skip * ds));
-        (static_cast<T*>(P.ddelta) + row)[c] = from_f32<T>(gx);
-        if (kGated) (static_cast<T*>(P.dz) + row)[c] = from_f32<T>(gz);
-      }
+      const bool live = t0 + t < end && mine;
+      const int64_t row = (p.b * P.T + t0 + t) * P.D + p.c0;
+      const uint32_t at = live ? uint32_t(lane) * uint32_t(sizeof(T)) : kNowhere;
+      const float gu[1] = {fmaf(k.dt[j], through, skip * ds)}, gd[1] = {gx}, gate[1] = {gz};
+      store_at(static_cast<T*>(P.du) + row, at, gu);
+      store_at(static_cast<T*>(P.ddelta) + row, at, gd);
+      if (kGated) store_at(static_cast<T*>(P.dz) + row, at, gate);
+      dskip = live ? fmaf(ds, k.u[j], dskip) : dskip;
+      dbias = live ? dbias + gx : dbias;
     }
   };
   const int64_t parts_row = (int64_t(p.group) * P.tiles_per_group + p.tile) * P.B + p.b;
@@ -441,26 +442,24 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
         // lane l has the sums of value l kV / 64: of token l kV / 64 / NS, state l kV / 64 % NS
         const float dC = sum_lanes(vc, lane), dB = sum_lanes(vb, lane);
         const int k = lane * kV / 64, t = 8 * kSide + k / NS;
-        if (lane % (64 / kV) == 0 && t < count) {
-          float* to = P.parts + ((parts_row * P.T + t0 + t) * 2) * kN + (g * W + wave) * NS + k % NS;
-          to[0] = dB;
-          to[kN] = dC;
-        }
+        const uint32_t to = lane % (64 / kV) == 0 && t < count ? uint32_t(t * 2 * kN + k % NS) * 4 : kNowhere;
+        float* part = P.parts + ((parts_row * P.T + t0) * 2) * kN + (g * W + wave) * NS;
+        const float gb[1] = {dB}, gc[1] = {dC};
+        store_at(part, to, gb);
+        store_at(part + kN, to, gc);
       }
     };
     Shares shares;
     collect(kEarly, shares);
     back(kLate);
-    if (t0 != last_tile) finish(t0 + kTile, kEarly, before, shares);
+    finish(t0 + kTile, kEarly, before, shares);  // (nothing behind the last tile)
     __syncthreads();
     collect(kLate, shares);
     back(kEarly);
     finish(t0, kLate, now, shares);
     before = now;
-    if (t0 > first) {
-      prepare(t0 - kTile, buffer ^ 1, now, n);
-      fetch(t0 - 2 * kTile);
-    }
+    prepare(t0 - kTile, buffer ^ 1, now, n);  // (in front of the first tile: of no use)
+    fetch(t0 - 2 * kTile);
     __syncthreads();
   }
   if (first < end) {
