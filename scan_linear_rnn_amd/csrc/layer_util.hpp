@@ -163,14 +163,13 @@ __device__ __forceinline__ float weight_at(const void* w, sr_dtype dtype, int64_
   return dtype == SR_BF16 ? to_f32(static_cast<const uint16_t*>(w)[i]) : static_cast<const float*>(w)[i];
 }
 
-// log(1 + e^x) to a few ulps for any x: max(x, 0) + log1p(e^-|x|), the
-// logarithm by W. Kahan's correction log1p(e) = log(u) e / (u - 1) with u the
-// rounded 1 + e, which undoes u's rounding error.
+// log(1 + e^x) to a few ulps for any x: max(x, 0) + log1p(e), e = e^-|x|.  With u the
+// rounded 1 + e, log1p(e) = log(u) + (e - (u - 1)) / u; u's rounding error e - (u - 1) is
+// exact, and what its division by u changes is far below the sum's last place.
 __device__ __forceinline__ float softplus_f(float x) {
   const float e = __builtin_amdgcn_exp2f(-fabsf(x) * kLog2e);
-  const float u = 1.0f + e, d = u - 1.0f;
-  const float l = d > 0.0f ? __builtin_amdgcn_logf(u) * (kLn2 * e) * __builtin_amdgcn_rcpf(d) : e;
-  return fmaxf(x, 0.0f) + l;  // (a NaN is in l)
+  const float u = 1.0f + e;
+  return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.0f));  // (a NaN is in e)
 }
 
 // 1 / (1 + e^-x), to a few ulps.
@@ -185,12 +184,20 @@ __device__ __forceinline__ float of_row(float x) {
   return __uint_as_float(
       uint32_t(__builtin_amdgcn_mov_dpp(int(__float_as_uint(x)), 0x150 + n, 0xF, 0xF, true)));
 }
+// of_row<n>(m) x.  (Opaque behind it, so that products of several numbers are not made
+// vectors of: those would take the operand from a register of its own.)
+template <int n>
+__device__ __forceinline__ float row_times(float m, float x) {
+  float y = of_row<n>(m) * x;
+  asm("" : "+v"(y));
+  return y;
+}
 // sum_i m[i][n] x[i] with m[i][n] in lane n of each row of 16.  (The compiler does not
 // put such an operand into fused multiply-adds by itself.  The two wait states are
 // those between a vector instruction's result and its use across lanes.)
 template <int n>
 __device__ __forceinline__ float row_dot(const float (&m)[1], const float (&x)[1]) {
-  return of_row<n>(m[0]) * x[0];
+  return row_times<n>(m[0], x[0]);
 }
 template <int n>
 __device__ __forceinline__ float row_dot(const float (&m)[2], const float (&x)[2]) {
@@ -218,7 +225,7 @@ __device__ __forceinline__ float row_dot(const float (&m)[4], const float (&x)[4
 // y[i] += m[i][n] x with m[i][n] in lane n of each row of 16.
 template <int n>
 __device__ __forceinline__ void row_add(const float (&m)[1], float x, float (&y)[1]) {
-  y[0] += of_row<n>(m[0]) * x;
+  y[0] += row_times<n>(m[0], x);
 }
 template <int n>
 __device__ __forceinline__ void row_add(const float (&m)[2], float x, float (&y)[2]) {

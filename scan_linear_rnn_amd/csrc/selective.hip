@@ -26,16 +26,20 @@
 namespace sr {
 namespace {
 
-// kStates: the state that the chunk's tokens make of zero (P.ends) and the sum
-// of their steps (P.steps), and with P.marks what the chunk has made of zero in
-// front of each tile, with the sum of the steps so far.  Else: y from the chunk's own
-// start state, and the last state.  W waves of NS states per lane.
+enum Pass {
+  kOutputs,  // y from the chunk's own start state, and the last state
+  kEnds,     // the state that the chunk's tokens make of zero, and the sum of their steps
+  kMarks,    // and what the chunk has made of zero in front of each tile, with the steps so far
+};
+
+// W waves of NS states per lane.
 //
 // While the waves go through tile k, each thread also prepares its part of tile
 // k + 1's steps, sums its part of tile k - 1's outputs and has tile k + 2's inputs on
 // their way: everything between two barriers is independent, one barrier per tile.
-template <typename T, int W, int NS, bool kStates, bool kWhole>
-__global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) {
+template <typename T, int W, int NS, int kPass, bool kWhole>
+__global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel(const SelectiveRequest P) {
+  constexpr bool kStates = kPass != kOutputs;
   constexpr int Q = kTile / W;  // neighbouring channels of a token that a thread prepares
   __shared__ __align__(16) float2 s_step[2][kTile][kLanes];  // dt, dt u
   __shared__ __align__(16) float s_y[2][kStates ? 1 : W][kTile][kLanes];
@@ -83,25 +87,33 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
   const auto bytes = [](int t, int64_t ld, int i) { return uint32_t(t * int(ld) + i) * uint32_t(sizeof(T)); };
   const uint32_t o_u = bytes(at, P.ld_u, c), o_d = bytes(at, P.ld_delta, c), o_z = bytes(at, P.ld_z, c),
                  o_b = bytes(bc_at, P.ld_b, 0), o_c = bytes(bc_at, P.ld_c, 0);
-  // The inputs of the tile at t0, as they stand in memory; behind the sequence's
-  // last token that one again.
-  auto fetch = [&](int64_t t0, Inputs& in) {
-    t0 = t0 < P.T ? t0 : P.T - 1;
-    const int64_t row0 = p.b * P.T + t0;
+  const int64_t row0 = p.b * P.T + first;
+  const T *pu = static_cast<const T*>(P.u) + row0 * P.ld_u + p.c0, *pd = static_cast<const T*>(P.delta) + row0 * P.ld_delta + p.c0,
+          *pz = static_cast<const T*>(P.z) + row0 * P.ld_z + p.c0, *pb = static_cast<const T*>(P.Bm) + row0 * P.ld_b + group0,
+          *pc = static_cast<const T*>(P.Cm) + row0 * P.ld_c + group0;  // at `ahead`, the tile that is fetched next
+  int64_t ahead = first;
+  // The next tile's inputs, as they stand in memory; behind the last tile that one
+  // again, behind the last token that one again.
+  auto fetch = [&](Inputs& in) {
     uint32_t b_u = o_u, b_d = o_d, b_z = o_z, b_b = o_b, b_c = o_c;
-    if (t0 + kTile > P.T) {
-      const int last = int(P.T - 1 - t0), t = at < last ? at : last, tb = bc_at < last ? bc_at : last;
+    if (ahead + kTile > P.T) {
+      const int last = int(P.T - 1 - ahead), t = at < last ? at : last, tb = bc_at < last ? bc_at : last;
       b_u = bytes(t, P.ld_u, c);
       b_d = bytes(t, P.ld_delta, c);
       b_z = bytes(t, P.ld_z, c);
       b_b = bytes(tb, P.ld_b, 0);
       b_c = bytes(tb, P.ld_c, 0);
     }
-    load_raw<kWhole>(at_byte(static_cast<const T*>(P.u) + row0 * P.ld_u + p.c0, b_u), nc, in.u);
-    load_raw<kWhole>(at_byte(static_cast<const T*>(P.delta) + row0 * P.ld_delta + p.c0, b_d), nc, in.delta);
-    if (!kStates && P.z) load_raw<kWhole>(at_byte(static_cast<const T*>(P.z) + row0 * P.ld_z + p.c0, b_z), nc, in.z);
-    load_raw<kWhole>(at_byte(static_cast<const T*>(P.Bm) + row0 * P.ld_b + group0, b_b), nn, in.Bm);
-    if constexpr (!kStates) load_raw<kWhole>(at_byte(static_cast<const T*>(P.Cm) + row0 * P.ld_c + group0, b_c), nn, in.Cm);
+    load_raw<kWhole>(at_byte(pu, b_u), nc, in.u);
+    load_raw<kWhole>(at_byte(pd, b_d), nc, in.delta);
+    if (!kStates && P.z) load_raw<kWhole>(at_byte(pz, b_z), nc, in.z);
+    load_raw<kWhole>(at_byte(pb, b_b), nn, in.Bm);
+    if constexpr (!kStates) load_raw<kWhole>(at_byte(pc, b_c), nn, in.Cm);
+    if (ahead + kTile < end) {
+      ahead += kTile;
+      pu += kTile * P.ld_u, pd += kTile * P.ld_delta, pb += kTile * P.ld_b;
+      if constexpr (!kStates) pz += kTile * P.ld_z, pc += kTile * P.ld_c;
+    }
   };
   // Converts what was fetched for the tile at t0 and writes its steps.
   auto prepare = [&](int64_t t0, int buffer, const Inputs& in, float (&bm)[NS], float (&cm)[NS]) {
@@ -184,22 +196,24 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
     float bm[NS], cm[NS];
     prepare(t0 + kTile, s ^ 1, in[s], bm, cm);
     const Raw<T, Q> un = in[s].u, zn = in[s].z;
-    fetch(t0 + 3 * kTile, in[s]);
-    if constexpr (kStates) {
-      if (P.marks != nullptr) {  // [tile][b][n][D], the steps as one more state
-        const int64_t m = (t0 / kTile * P.B + p.b) * (P.N + 1);
+    fetch(in[s]);
+    if constexpr (kPass == kMarks) {  // [tile][b][n][D], the steps as one more state
+      float* mark = P.marks + (t0 / kTile * P.B + p.b) * (P.N + 1) * P.D + p.c0;
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-          if (mine && n0 + i < P.N) P.marks[(m + n0 + i) * P.D + d] = h[i];
-        if (mine && wave == 0) P.marks[(m + P.N) * P.D + d] = total;
+      for (int i = 0; i < NS; ++i) {
+        const float v[1] = {h[i]};
+        store_at(mark + (n0 + i) * P.D, mine && n0 + i < P.N ? uint32_t(lane) * 4 : kNowhere, v);
       }
+      const float v[1] = {total};
+      store_at(mark + P.N * P.D, mine && wave == 0 ? uint32_t(lane) * 4 : kNowhere, v);
     }
     unrolled<kTile>([&](auto token) {
       constexpr int t = decltype(token)::value;
       if constexpr (kStates) total += step[t].x;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        h[i] = fmaf(__builtin_amdgcn_exp2f(step[t].x * a2[i]), h[i], of_row<t>(b0[i]) * step[t].y);
+        h[i] = fmaf(__builtin_amdgcn_exp2f(step[t].x * a2[i]), h[i],
+                    kStates ? row_times<t>(b0[i], step[t].y) : of_row<t>(b0[i]) * step[t].y);
       if constexpr (!kStates) s_y[s][wave][t][lane] = row_dot<t>(c0, h);
     });
     if constexpr (!kStates) {
@@ -215,11 +229,11 @@ __global__ __launch_bounds__(W * 64) void scan_kernel(const SelectiveRequest P) 
     __syncthreads();
   };
   if (first < end) {
-    fetch(first, in[1]);
-    fetch(first + kTile, in[0]);
+    fetch(in[1]);
+    fetch(in[0]);
     prepare(first, 0, in[1], b0, c0);
     u0 = in[1].u, z0 = in[1].z;
-    fetch(first + 2 * kTile, in[1]);
+    fetch(in[1]);
     __syncthreads();
     int64_t t0 = first;
     for (; t0 + kTile < end; t0 += 2 * kTile) {
@@ -346,26 +360,31 @@ __global__ __launch_bounds__(256) void step_kernel(const SelectiveRequest P) {
 }
 
 template <typename T, int W, int NS>
-void launch_scan(const SelectiveRequest& P, bool states, uint32_t blocks) {
-  auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(W * 64), 0, P.stream, P); };
+void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
   constexpr int Q = kTile / W;
-  if (P.D / P.G % Q == 0 && P.N % NS == 0 && reinterpret_cast<uintptr_t>(P.y) % (Q * sizeof(T)) == 0)
-    states ? run(scan_kernel<T, W, NS, true, true>) : run(scan_kernel<T, W, NS, false, true>);
+  const bool whole =
+      P.D / P.G % Q == 0 && P.N % NS == 0 && reinterpret_cast<uintptr_t>(P.y) % (Q * sizeof(T)) == 0;
+  auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(W * 64), 0, P.stream, P); };
+  auto either = [&](auto* all, auto* any) { whole ? run(all) : run(any); };
+  if (pass == kOutputs)
+    either(scan_kernel<T, W, NS, kOutputs, true>, scan_kernel<T, W, NS, kOutputs, false>);
+  else if (pass == kEnds)
+    either(scan_kernel<T, W, NS, kEnds, true>, scan_kernel<T, W, NS, kEnds, false>);
   else
-    states ? run(scan_kernel<T, W, NS, true, false>) : run(scan_kernel<T, W, NS, false, false>);
+    either(scan_kernel<T, W, NS, kMarks, true>, scan_kernel<T, W, NS, kMarks, false>);
 }
 template <typename T>
-void launch_scan(const SelectiveRequest& P, bool states, uint32_t blocks) {
+void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
   if (P.N <= 4)
-    launch_scan<T, 4, 1>(P, states, blocks);
+    launch_scan<T, 4, 1>(P, pass, blocks);
   else if (P.N <= 8)
-    launch_scan<T, 4, 2>(P, states, blocks);
+    launch_scan<T, 4, 2>(P, pass, blocks);
   else if (P.N <= 16)
-    launch_scan<T, 4, 4>(P, states, blocks);
+    launch_scan<T, 4, 4>(P, pass, blocks);
   else if (P.N <= 32)
-    launch_scan<T, 8, 4>(P, states, blocks);
+    launch_scan<T, 8, 4>(P, pass, blocks);
   else
-    launch_scan<T, 16, 4>(P, states, blocks);
+    launch_scan<T, 16, 4>(P, pass, blocks);
 }
 
 template <typename T, int V>
@@ -427,9 +446,9 @@ SelectivePlan selective_backward_plan(int64_t B, int64_t T, int64_t D, int64_t G
 sr_status launch_selective_states(const SelectiveRequest& P) {
   const uint32_t blocks = uint32_t(P.B * P.G * P.tiles_per_group * P.chunks);
   if (P.dtype == SR_BF16)
-    launch_scan<uint16_t>(P, true, blocks);
+    launch_scan<uint16_t>(P, P.marks ? kMarks : kEnds, blocks);
   else
-    launch_scan<float>(P, true, blocks);
+    launch_scan<float>(P, P.marks ? kMarks : kEnds, blocks);
   return launched("selective scan states");
 }
 
@@ -452,9 +471,9 @@ sr_status launch_selective_scan(const SelectiveRequest& rq) {
   }
   const uint32_t blocks = uint32_t(P.B * P.G * P.tiles_per_group * P.chunks);
   if (P.dtype == SR_BF16)
-    launch_scan<uint16_t>(P, false, blocks);
+    launch_scan<uint16_t>(P, kOutputs, blocks);
   else
-    launch_scan<float>(P, false, blocks);
+    launch_scan<float>(P, kOutputs, blocks);
   return launched("selective scan");
 }
 

@@ -405,7 +405,7 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           decay[g][t][i] = __builtin_amdgcn_exp2f(s.x * a2[i]);
-          h[g][t + 1][i] = fmaf(decay[g][t][i], h[g][t][i], of_row<t>(n.b[g][i]) * s.y);
+          h[g][t + 1][i] = fmaf(decay[g][t][i], h[g][t][i], row_times<t>(n.b[g][i], s.y));
         }
       });
     }
