@@ -354,7 +354,7 @@ sr_status causal_conv_forward(int64_t B, int64_t T, int64_t D, int64_t K, const 
   P.stream = as_stream(stream);
   sr_status st = check_conv(P, T, K);
   if (st != SR_OK) return st;
-  const ConvPlan plan = conv_plan(B, T, D, x_dtype);
+  const ConvPlan plan = conv_plan(B, T, D, x_dtype, false);
   P.run_len = plan.run_len;
   P.runs = plan.runs;
   st = check_grid(conv_blocks(P), 256);
@@ -372,7 +372,7 @@ sr_status causal_conv_forward(int64_t B, int64_t T, int64_t D, int64_t K, const 
 
 size_t causal_conv_backward_workspace_size(int64_t B, int64_t T, int64_t D, int64_t K, sr_dtype x_dtype) {
   if (K < 1 || K > kConvTaps || !is_dtype(x_dtype) || !sizes_ok({B, T < 0 ? -1 : T + kConvTaps, D, kConvTaps + 1})) return 0;
-  return align_up(size_t(B * conv_plan(B, T, D, x_dtype).runs) * size_t(K + 1) * size_t(D) * 4, kAlign);
+  return align_up(size_t(B * conv_plan(B, T, D, x_dtype, true).runs) * size_t(K + 1) * size_t(D) * 4, kAlign);
 }
 
 sr_status causal_conv_backward(int64_t B, int64_t T, int64_t D, int64_t K, const void* x, int64_t ld_x, sr_dtype x_dtype,
@@ -390,7 +390,7 @@ sr_status causal_conv_backward(int64_t B, int64_t T, int64_t D, int64_t K, const
   P.stream = as_stream(stream);
   sr_status st = check_conv(P, T, K);
   if (st != SR_OK) return st;
-  const ConvPlan plan = conv_plan(B, T, D, x_dtype);
+  const ConvPlan plan = conv_plan(B, T, D, x_dtype, true);
   P.run_len = plan.run_len;
   P.runs = plan.runs;
   st = check_grid(conv_blocks(P), 256);

@@ -39,13 +39,15 @@ __device__ __forceinline__ bool run_of(const ConvRequest& P, int64_t i, Run* r) 
   return true;
 }
 
-// A vector of one channel or of several.
+// V elements, an odd number of them one by one.
 template <int V, typename T>
 __device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
-  if constexpr (V == 1)
-    v[0] = to_f32(*p);
-  else
+  if constexpr (V % 2) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = to_f32(p[e]);
+  } else {
     load_n(p, v);
+  }
 }
 template <int V, typename T>
 __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
@@ -69,14 +71,25 @@ __device__ __forceinline__ void input_at(const ConvRequest& P, int64_t b, int64_
   }
 }
 
-template <int K, int V>
-__device__ __forceinline__ void load_taps(const ConvRequest& P, int64_t c, float (&w)[K][V], float (&bias)[V]) {
+// The filters of V neighbouring channels stand one after another.
+template <int K, int V, typename W>
+__device__ __forceinline__ void load_taps(const W* w0, const W* b0, int64_t c, float (&w)[K][V], float (&bias)[V]) {
+  float all[V * K];
+  load_v(w0 + c * K, all);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][e] = weight_at(P.w, P.w_dtype, (c + e) * K + j);
-    bias[e] = P.bias ? weight_at(P.bias, P.w_dtype, c + e) : 0.0f;
+    for (int j = 0; j < K; ++j) w[j][e] = all[e * K + j];
+    bias[e] = 0.0f;
   }
+  if (b0) load_v(b0 + c, bias);
+}
+template <int K, int V>
+__device__ __forceinline__ void load_taps(const ConvRequest& P, int64_t c, float (&w)[K][V], float (&bias)[V]) {
+  if (P.w_dtype == SR_BF16)
+    load_taps<K, V>(static_cast<const uint16_t*>(P.w), static_cast<const uint16_t*>(P.bias), c, w, bias);
+  else
+    load_taps<K, V>(static_cast<const float*>(P.w), static_cast<const float*>(P.bias), c, w, bias);
 }
 
 template <typename T, int K, int V>
@@ -110,40 +123,48 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvRequest P) {
 #pragma unroll
     for (int j = 1; j < K; ++j) input_at<T, K>(P, r.b, r.t0 - K + j, r.c, win[j]);
   }
-  float next[kAhead][V];
-  auto fetch = [&](int64_t t) {
+  auto token = [&](int64_t t, const Raw<T, V>& in) {
+    float x1[V], out[V];
+    values(in, x1);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (t + a < end) load_v(x + (t + a) * P.ld_x, next[a]);
-  };
-  fetch(r.t0);
-  for (int64_t t = r.t0; t < end; t += kAhead) {
-    float in[kAhead][V];
+    for (int e = 0; e < V; ++e) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
+      for (int j = 0; j + 1 < K; ++j) win[j][e] = win[j + 1][e];
+      win[K - 1][e] = x1[e];
+      float c = bias[e];
 #pragma unroll
-      for (int e = 0; e < V; ++e) in[a][e] = next[a][e];
-    fetch(t + kAhead);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (t + a >= end) break;
-      float out[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-#pragma unroll
-        for (int j = 0; j + 1 < K; ++j) win[j][e] = win[j + 1][e];
-        win[K - 1][e] = in[a][e];
-        float c = bias[e];
-#pragma unroll
-        for (int j = 0; j < K; ++j) c = fmaf(w[j][e], win[j][e], c);
-        out[e] = P.silu ? c * logistic_f(c) : c;
-      }
-      store_v(y + (t + a) * P.D, out);
+      for (int j = 0; j < K; ++j) c = fmaf(w[j][e], win[j][e], c);
+      out[e] = P.silu ? c * logistic_f(c) : c;
     }
+    store_v(y + t * P.D, out);
+  };
+  // Whole groups of tokens without a condition (a store that may not happen would
+  // have the loads behind it wait for all stores), then what is left.
+  int64_t t = r.t0;
+  if (t + kAhead <= end) {
+    Raw<T, V> next[kAhead];
+    auto fetch = [&](int64_t t1) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) load_raw<true>(x + (t1 + a < end ? t1 + a : end - 1) * P.ld_x, V, next[a]);
+    };
+    fetch(t);
+    for (; t + kAhead <= end; t += kAhead) {
+      Raw<T, V> in[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) in[a] = next[a];
+      fetch(t + kAhead);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) token(t + a, in[a]);
+    }
+  }
+  for (; t < end; ++t) {
+    Raw<T, V> in;
+    load_raw<true>(x + t * P.ld_x, V, in);
+    token(t, in);
   }
   // Rows behind the sequence's end are zero.
   const float none[V] = {};
-  for (int64_t t = end > r.t0 ? end : r.t0; t < r.t1; ++t) store_v(y + t * P.D, none);
+  for (t = end > r.t0 ? end : r.t0; t < r.t1; ++t) store_v(y + t * P.D, none);
 }
 
 // Backward.  With dc_t = dy_t silu'(c_t):
@@ -173,71 +194,88 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(const ConvRequest P)
 #pragma unroll
     for (int j = 1; j < K; ++j) input_at<T, K>(P, r.b, r.t0 - K + j, r.c, win[j]);
   }
-  float nx[kAhead][V], ng[kAhead][V];
-  auto fetch = [&](int64_t t) {
+  // One token: kInside, all of its parts exist and its neighbours' do.
+  auto token = [&](auto inside, int64_t t, const Raw<T, V>& in_x, const Raw<T, V>& in_g) {
+    constexpr bool kInside = decltype(inside)::value;
+    const bool live = kInside || t < end, own = kInside || t < r.t1;
+    float x1[V], g1[V], out[V];
+    values(in_x, x1);
+    values(in_g, g1);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (t + a < end) {
-        load_v(x + (t + a) * P.ld_x, nx[a]);
-        load_v(dy + (t + a) * P.ld_dy, ng[a]);
-      }
-  };
-  fetch(r.t0);
-  for (int64_t t = r.t0; t < stop; t += kAhead) {
-    float ix[kAhead][V], ig[kAhead][V];
+    for (int e = 0; e < V; ++e) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
+      for (int j = 0; j + 1 < K; ++j) win[j][e] = win[j + 1][e];
+      win[K - 1][e] = live ? x1[e] : 0.0f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        ix[a][e] = nx[a][e];
-        ig[a][e] = ng[a][e];
-      }
-    fetch(t + kAhead);
+      for (int j = K - 1; j > 0; --j) dc[j][e] = dc[j - 1][e];
+      float g = g1[e];
+      float c = bias[e];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (t + a >= stop) break;
-      const bool live = t + a < end;
-      const bool own = t + a < r.t1;
-      float out[V];
+      for (int j = 0; j < K; ++j) c = fmaf(w[j][e], win[j][e], c);
+      const float s = logistic_f(c), slope = s * fmaf(c, 1.0f - s, 1.0f);
+      g *= P.silu ? slope : 1.0f;
+      dc[0][e] = live ? g : 0.0f;
+      const float mine = own ? dc[0][e] : 0.0f;
+      dbias[e] += mine;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
+      for (int j = 0; j < K; ++j) dw[j][e] = fmaf(mine, win[j][e], dw[j][e]);
+      out[e] = 0.0f;
 #pragma unroll
-        for (int j = 0; j + 1 < K; ++j) win[j][e] = win[j + 1][e];
-        win[K - 1][e] = live ? ix[a][e] : 0.0f;
-#pragma unroll
-        for (int j = K - 1; j > 0; --j) dc[j][e] = dc[j - 1][e];
-        float c = bias[e];
-#pragma unroll
-        for (int j = 0; j < K; ++j) c = fmaf(w[j][e], win[j][e], c);
-        float g = ig[a][e];
-        if (P.silu) {
-          const float s = logistic_f(c);
-          g *= s * fmaf(c, 1.0f - s, 1.0f);
-        }
-        dc[0][e] = live ? g : 0.0f;
-        if (own && live) {
-          dbias[e] += g;
-#pragma unroll
-          for (int j = 0; j < K; ++j) dw[j][e] = fmaf(g, win[j][e], dw[j][e]);
-        }
-        out[e] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) out[e] = fmaf(w[j][e], dc[j][e], out[e]);
-      }
-      const int64_t s = t + a - (K - 1);  // the token whose gradient is complete
-      if (s < r.t0 && (s >= 0 || r.t0 > 0)) continue;
-      const int64_t m = s - (r.length - (K - 1));  // its place in the state behind the sequence
-      if (P.dlast && m >= 0 && m < K - 1) {
-        float g[V];
-        load_v(static_cast<const T*>(P.dlast) + (r.b * (K - 1) + m) * P.D + r.c, g);
-#pragma unroll
-        for (int e = 0; e < V; ++e) out[e] += g[e];
-      }
-      if (s >= 0)
-        store_v(dx + s * P.D, out);
-      else if (P.dstate)
-        store_v(static_cast<T*>(P.dstate) + (r.b * (K - 1) + K - 1 + s) * P.D + r.c, out);
+      for (int j = 0; j < K; ++j) out[e] = fmaf(w[j][e], dc[j][e], out[e]);
     }
+    const int64_t s = t - (K - 1);  // the token whose gradient is complete
+    if constexpr (kInside) {
+      store_v(dx + s * P.D, out);
+      return;
+    }
+    if (s < r.t0 && (s >= 0 || r.t0 > 0)) return;
+    const int64_t m = s - (r.length - (K - 1));  // its place in the state behind the sequence
+    if (P.dlast && m >= 0 && m < K - 1) {
+      float g[V];
+      load_v(static_cast<const T*>(P.dlast) + (r.b * (K - 1) + m) * P.D + r.c, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) out[e] += g[e];
+    }
+    if (s >= 0)
+      store_v(dx + s * P.D, out);
+    else if (P.dstate)
+      store_v(static_cast<T*>(P.dstate) + (r.b * (K - 1) + K - 1 + s) * P.D + r.c, out);
+  };
+  auto load = [&](int64_t t, Raw<T, V>& in_x, Raw<T, V>& in_g) {
+    if (end <= r.t0) return;  // (nothing of the run exists)
+    t = t < end ? t : end - 1;
+    load_raw<true>(x + t * P.ld_x, V, in_x);
+    load_raw<true>(dy + t * P.ld_dy, V, in_g);
+  };
+  constexpr std::false_type kAny{};
+  constexpr std::true_type kInside{};
+  int64_t t = r.t0;
+  Raw<T, V> one_x{}, one_g{};
+  for (; t < stop && t < r.t0 + K - 1; ++t) {
+    load(t, one_x, one_g);
+    token(kAny, t, one_x, one_g);
+  }
+  const int64_t inner = end < r.t1 ? end : r.t1;
+  if (t + kAhead <= inner) {
+    Raw<T, V> nx[kAhead], ng[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) load(t + a, nx[a], ng[a]);
+    for (; t + kAhead <= inner; t += kAhead) {
+      Raw<T, V> ix[kAhead], ig[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        ix[a] = nx[a];
+        ig[a] = ng[a];
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) load(t + kAhead + a, nx[a], ng[a]);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) token(kInside, t + a, ix[a], ig[a]);
+    }
+  }
+  for (; t < stop; ++t) {
+    load(t, one_x, one_g);
+    token(kAny, t, one_x, one_g);
   }
   float* to = P.parts + r.index * (K + 1) * P.D + r.c;
 #pragma unroll
@@ -311,7 +349,9 @@ void by_type(sr_dtype dtype, bool whole, F f) {
   }
 }
 
-int64_t vector_of(sr_dtype dtype) { return dtype == SR_BF16 ? 8 : 4; }
+// A thread's channels: 16 bytes, in the backward pass (whose filter, windows and sums
+// are all in registers) four.
+int64_t vector_of(sr_dtype dtype, bool backward) { return dtype == SR_BF16 && !backward ? 8 : 4; }
 
 sr_status launched(const char* what) {
   const hipError_t err = hipGetLastError();
@@ -322,8 +362,8 @@ sr_status launched(const char* what) {
 
 // Runs of tokens: as long as the GPU still has about two waves per SIMD of
 // them, 4 to 64 (the K - 1 inputs in front of a run are read again).
-ConvPlan conv_plan(int64_t B, int64_t T, int64_t D, sr_dtype dtype) {
-  const int64_t v = vector_of(dtype), nvec = D >= v ? (D + v - 1) / v : D;
+ConvPlan conv_plan(int64_t B, int64_t T, int64_t D, sr_dtype dtype, bool backward) {
+  const int64_t v = vector_of(dtype, backward), nvec = D >= v ? (D + v - 1) / v : D;
   ConvPlan plan{4, 0};
   while (plan.run_len < 64 && B * nvec * ((T + 2 * plan.run_len - 1) / (2 * plan.run_len)) >= 131072) plan.run_len *= 2;
   plan.runs = T > 0 ? (T + plan.run_len - 1) / plan.run_len : 1;  // (without tokens the states still pass)
@@ -331,7 +371,7 @@ ConvPlan conv_plan(int64_t B, int64_t T, int64_t D, sr_dtype dtype) {
 }
 
 sr_status launch_conv(const ConvRequest& P) {
-  const int64_t v = vector_of(P.dtype), nvec = P.D >= v ? (P.D + v - 1) / v : P.D;
+  const int64_t v = vector_of(P.dtype, false), nvec = P.D >= v ? (P.D + v - 1) / v : P.D;
   const int64_t n = nvec * (P.B * P.runs + (P.last ? P.B * (P.K - 1) : 0));
   if (n == 0) return SR_OK;
   by_type(P.dtype, P.D >= v, [&](auto t, auto width) {
@@ -344,12 +384,12 @@ sr_status launch_conv(const ConvRequest& P) {
 }
 
 sr_status launch_conv_backward(const ConvRequest& P) {
-  const int64_t v = vector_of(P.dtype), nvec = P.D >= v ? (P.D + v - 1) / v : P.D;
+  const int64_t v = vector_of(P.dtype, true), nvec = P.D >= v ? (P.D + v - 1) / v : P.D;
   const int64_t n = nvec * P.B * P.runs;
   by_type(P.dtype, P.D >= v, [&](auto t, auto width) {
     by_taps(P.K, [&](auto taps) {
       if (n > 0)
-        hipLaunchKernelGGL((conv_backward_kernel<decltype(t), decltype(taps)::value, decltype(width)::value>),
+        hipLaunchKernelGGL((conv_backward_kernel<decltype(t), decltype(taps)::value, decltype(width)::value == 8 ? 4 : decltype(width)::value>),
                            dim3(uint32_t((n + 255) / 256)), dim3(256), 0, P.stream, P);
     });
   });
@@ -360,7 +400,7 @@ sr_status launch_conv_backward(const ConvRequest& P) {
 }
 
 sr_status launch_conv_step(const ConvRequest& P) {
-  const int64_t v = vector_of(P.dtype);
+  const int64_t v = vector_of(P.dtype, false);
   const bool whole = P.D % v == 0;
   const int64_t n = P.B * (whole ? P.D / v : P.D);
   by_type(P.dtype, whole, [&](auto t, auto width) {

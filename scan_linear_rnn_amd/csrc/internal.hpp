@@ -282,7 +282,7 @@ constexpr int kConvTaps = 8;  // most taps per channel
 struct ConvPlan {
   int64_t run_len, runs;  // tokens of a thread, and runs per sequence
 };
-ConvPlan conv_plan(int64_t B, int64_t T, int64_t D, sr_dtype dtype);
+ConvPlan conv_plan(int64_t B, int64_t T, int64_t D, sr_dtype dtype, bool backward);
 
 struct ConvRequest {
   sr_dtype dtype, w_dtype;

@@ -302,60 +302,71 @@ __global__ __launch_bounds__(256) void carry_kernel(const SelectiveRequest P, co
   if (last) last[own] = h;
 }
 
-// One token: L lanes per channel, V states each; y is summed over the lanes.
-// Bound by the states' bytes (read and written once) for many streams, by the
-// launch for a few.
-template <typename T, int V, int L>
+// One token: L lanes per channel, V states each, of R streams one after another; y is
+// summed over the lanes.  Bound by the states' bytes (read and written once) for
+// many streams, whose threads then keep A for four of them, by the launch for a few.
+template <typename T, int V, int L, int R>
 __global__ __launch_bounds__(256) void step_kernel(const SelectiveRequest P) {
-  const int64_t i = int64_t(blockIdx.x) * (256 / L) + threadIdx.x / L;  // row and channel
+  const int64_t i = int64_t(blockIdx.x) * (256 / L) + threadIdx.x / L;  // streams' group and channel
   const int n0 = threadIdx.x % L * V;
-  const bool live = i < P.B * P.D;
-  const int64_t k = live ? i : P.B * P.D - 1;
-  const int64_t b = k / P.D, d = k - b * P.D;
-  const T* Bm = static_cast<const T*>(P.Bm) + b * P.ld_b + d / (P.D / P.G) * P.N;
-  const T* Cm = static_cast<const T*>(P.Cm) + b * P.ld_c + d / (P.D / P.G) * P.N;
-  float h[V], a[V], bm[V], cm[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = a[v] = bm[v] = cm[v] = 0.0f;
-  if (n0 < P.N) {
-    if constexpr (V == 4) {  // N is a multiple of four
-      const f32x4 av = load4(P.A + d * P.N + n0, 4), bv = load4(Bm + n0, 4), cv = load4(Cm + n0, 4);
-      f32x4 hv{};
-      if (P.h0) hv = load4(P.h0 + k * P.N + n0, 4);
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = hv[v], a[v] = av[v], bm[v] = bv[v], cm[v] = cv[v];
-    } else {
-      if (P.h0) h[0] = P.h0[k * P.N + n0];
-      a[0] = P.A[d * P.N + n0];
-      bm[0] = to_f32(Bm[n0]);
-      cm[0] = to_f32(Cm[n0]);
-    }
-  }
-  const float u = to_f32(static_cast<const T*>(P.u)[b * P.ld_u + d]);
-  float x = to_f32(static_cast<const T*>(P.delta)[b * P.ld_delta + d]);
-  const float zv = P.z ? to_f32(static_cast<const T*>(P.z)[b * P.ld_z + d]) : 0.0f;
-  const float skip = P.skip ? P.skip[d] : 0.0f;
-  if (P.bias) x += P.bias[d];
-  const float dt = P.softplus ? softplus_f(x) : x;
-  const float du = dt * u;
-  float sum = 0.0f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = fmaf(__builtin_amdgcn_exp2f(dt * (a[v] * kLog2e)), h[v], du * bm[v]);
-    sum = fmaf(h[v], cm[v], sum);
-  }
-  if (live && n0 < P.N) {
+  const int64_t groups = (P.B + R - 1) / R;
+  const bool live = i < groups * P.D;
+  const int64_t k = live ? i : groups * P.D - 1;
+  const int64_t b0 = k / P.D * R, d = k % P.D, g0 = d / (P.D / P.G) * P.N;
+  const bool has = n0 < P.N;
+  const int n = has ? n0 : 0;
+  // states n .. n + V - 1 (with V = 4, N is a multiple of four)
+  auto load_states = [&](const auto* p, float (&v)[V]) {
     if constexpr (V == 4)
-      store4(P.h_last + i * P.N + n0, f32x4{h[0], h[1], h[2], h[3]}, 4);
+      load_n(p, v);
     else
-      P.h_last[i * P.N + n0] = h[0];
-  }
+      v[0] = to_f32(*p);
+  };
+  float a[V], h[R][V], bm[R][V], cm[R][V], u[R], x[R], z[R];
+  load_states(P.A + d * P.N + n, a);
 #pragma unroll
-  for (int m = 1; m < L; m *= 2) sum += __shfl_xor(sum, m);
-  if (live && n0 == 0) {
-    sum = fmaf(skip, u, sum);
-    if (P.z) sum *= zv * logistic_f(zv);
-    static_cast<T*>(P.y)[i] = from_f32<T>(sum);
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = b0 + r < P.B ? b0 + r : P.B - 1;
+    if (P.h0) {
+      load_states(P.h0 + (b * P.D + d) * P.N + n, h[r]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[r][v] = 0.0f;
+    }
+    load_states(static_cast<const T*>(P.Bm) + b * P.ld_b + g0 + n, bm[r]);
+    load_states(static_cast<const T*>(P.Cm) + b * P.ld_c + g0 + n, cm[r]);
+    u[r] = to_f32(static_cast<const T*>(P.u)[b * P.ld_u + d]);
+    x[r] = to_f32(static_cast<const T*>(P.delta)[b * P.ld_delta + d]);
+    z[r] = P.z ? to_f32(static_cast<const T*>(P.z)[b * P.ld_z + d]) : 0.0f;
+  }
+  const float skip = P.skip ? P.skip[d] : 0.0f, bias = P.bias ? P.bias[d] : 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float soft = softplus_f(x[r] + bias);
+    const float dt = P.softplus ? soft : x[r] + bias;
+    const float du = dt * u[r];
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[r][v] = fmaf(__builtin_amdgcn_exp2f(dt * (a[v] * kLog2e)), h[r][v], du * bm[r][v]);
+      sum = fmaf(h[r][v], has ? cm[r][v] : 0.0f, sum);
+    }
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) sum += __shfl_xor(sum, m);
+    const int64_t b = b0 + r;
+    if (!live || b >= P.B) continue;
+    if (has) {
+      float* to = P.h_last + (b * P.D + d) * P.N + n;
+      if constexpr (V == 4)
+        store_n(to, h[r]);
+      else
+        *to = h[r][0];
+    }
+    if (n0 == 0) {
+      sum = fmaf(skip, u[r], sum);
+      if (P.z) sum *= z[r] * logistic_f(z[r]);
+      static_cast<T*>(P.y)[b * P.D + d] = from_f32<T>(sum);
+    }
   }
 }
 
@@ -387,28 +398,36 @@ void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
     launch_scan<T, 16, 4>(P, pass, blocks);
 }
 
+template <typename T, int V, int L>
+void launch_step(const SelectiveRequest& P) {
+  auto run = [&](auto* kernel, int R) {
+    const int64_t blocks = ((P.B + R - 1) / R * P.D + 256 / L - 1) / (256 / L);
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(256), 0, P.stream, P);
+  };
+  // Four streams per thread where that leaves every CU eight workgroups.
+  if (P.B / 4 * P.D * L >= 256 * 8 * 256)
+    run(step_kernel<T, V, L, 4>, 4);
+  else
+    run(step_kernel<T, V, L, 1>, 1);
+}
 template <typename T, int V>
 void launch_step(const SelectiveRequest& P) {
   const int64_t lanes = (P.N + V - 1) / V;
-  auto run = [&](auto* kernel, int L) {
-    const int64_t blocks = (P.B * P.D + 256 / L - 1) / (256 / L);
-    hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(256), 0, P.stream, P);
-  };
   if (lanes <= 1)
-    run(step_kernel<T, V, 1>, 1);
+    launch_step<T, V, 1>(P);
   else if (lanes <= 2)
-    run(step_kernel<T, V, 2>, 2);
+    launch_step<T, V, 2>(P);
   else if (lanes <= 4)
-    run(step_kernel<T, V, 4>, 4);
+    launch_step<T, V, 4>(P);
   else if (lanes <= 8)
-    run(step_kernel<T, V, 8>, 8);
+    launch_step<T, V, 8>(P);
   else if (lanes <= 16)
-    run(step_kernel<T, V, 16>, 16);
+    launch_step<T, V, 16>(P);
   else if constexpr (V == 1) {
     if (lanes <= 32)
-      run(step_kernel<T, V, 32>, 32);
+      launch_step<T, V, 32>(P);
     else
-      run(step_kernel<T, V, 64>, 64);
+      launch_step<T, V, 64>(P);
   }
 }
 
