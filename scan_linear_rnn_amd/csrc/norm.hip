@@ -22,6 +22,31 @@ constexpr int kV = 8;  // elements per lane and chunk
 
 struct None {};  // no residual
 
+// A lane's chunks of a row of D elements, `step` apart from c0 on; zeros behind the row.  kWhole: D is
+// a multiple of a chunk, and all loads are on the way before the first is waited for.
+template <bool kWhole, int NV, typename T>
+__device__ __forceinline__ void load_row(const T* row, int c0, int step, int D, float (&v)[NV][kV]) {
+  if constexpr (kWhole) {
+    Raw<T, kV> raw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = c0 + j * step;
+      load_raw<true>(row + (c < D ? c : 0), kV, raw[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      values(raw[j], v[j]);
+      if (c0 + j * step >= D) {
+#pragma unroll
+        for (int e = 0; e < kV; ++e) v[j][e] = 0.0f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_some(row + c0 + j * step, D - c0 - j * step, v[j]);
+  }
+}
+
 // Sum, or largest value, over a row of LPR lanes and WPR waves, in all of them;
 // the waves' values meet in LDS (two barriers).
 template <int LPR, int WPR, typename V, typename Join>
@@ -46,7 +71,7 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
 // LPR lanes and WPR waves per row (LPR < 64 only with one wave), NV chunks per
 // lane.  X: the type of x and y, R: of the residual and the sum (None: there
 // is none); CODES: 8-bit codes instead of y.
-template <typename X, typename R, int LPR, int WPR, int NV, bool CODES>
+template <typename X, typename R, int LPR, int WPR, int NV, bool CODES, bool kWhole>
 __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void norm_kernel(const NormRequest P) {
   constexpr int kThreads = WPR > 4 ? WPR * 64 : 256;
   constexpr int kRows = kThreads / (LPR * WPR);
@@ -71,15 +96,15 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void norm_kernel(const No
     const int64_t row = live ? want : last;
     float t[NV][kV];
     float sum = 0.0f;
+    load_row<kWhole>(static_cast<const X*>(P.x) + row * P.ld_x, c0, LPR * WPR * kV, D, t);
+    if constexpr (kResidual) {
+      float r[NV][kV];
+      load_row<kWhole>(static_cast<const R*>(P.r) + row * P.ld_r, c0, LPR * WPR * kV, D, r);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = c0 + j * LPR * WPR * kV;
-      load_some(static_cast<const X*>(P.x) + row * P.ld_x + c, D - c, t[j]);
-      if constexpr (kResidual) {
-        float r[kV];
-        load_some(static_cast<const R*>(P.r) + row * P.ld_r + c, D - c, r);
+      for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * LPR * WPR * kV;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) t[j][e] = to_f32(from_f32<R>(t[j][e] + r[e]));
+        for (int e = 0; e < kV; ++e) t[j][e] = to_f32(from_f32<R>(t[j][e] + r[j][e]));
         if (live) store_some(static_cast<R*>(P.total) + row * P.D + c, D - c, t[j]);
       }
     }
@@ -128,7 +153,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void norm_kernel(const No
   }
 }
 
-template <typename X, typename R, int LPR, int WPR, int NV>
+template <typename X, typename R, int LPR, int WPR, int NV, bool kWhole>
 __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void norm_backward_kernel(const NormRequest P) {
   constexpr int kThreads = WPR > 4 ? WPR * 64 : 256;
   constexpr int kRows = kThreads / (LPR * WPR);
@@ -153,14 +178,15 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void norm_backward_kernel
     const int64_t row = live ? want : P.M - 1;
     float t[NV][kV], g[NV][kV], dt[NV][kV];
     float square = 0.0f, cross = 0.0f;  // of t, and of g t
+    load_row<kWhole>(static_cast<const R*>(P.t) + row * P.ld_t, c0, LPR * WPR * kV, D, t);
+    load_row<kWhole>(static_cast<const X*>(P.dy) + row * P.ld_dy, c0, LPR * WPR * kV, D, g);
+    if (P.dt) {
+      load_row<kWhole>(static_cast<const R*>(P.dt) + row * P.ld_dt, c0, LPR * WPR * kV, D, dt);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = c0 + j * LPR * WPR * kV;
-      load_some(static_cast<const R*>(P.t) + row * P.ld_t + c, D - c, t[j]);
-      load_some(static_cast<const X*>(P.dy) + row * P.ld_dy + c, D - c, g[j]);
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < kV; ++e) dt[j][e] = 0.0f;
-      if (P.dt) load_some(static_cast<const R*>(P.dt) + row * P.ld_dt + c, D - c, dt[j]);
+        for (int e = 0; e < kV; ++e) dt[j][e] = 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -246,12 +272,15 @@ void launch_forward(const NormRequest& P) {
   by_width(P.q ? P.ld_q : P.D, [&](auto shape) {
     using S = decltype(shape);
     const int64_t blocks = capped((P.M + S::kRows - 1) / S::kRows, 2048);
+    auto run = [&](auto* whole, auto* any) {
+      hipLaunchKernelGGL(P.D % kV == 0 ? whole : any, dim3(uint32_t(blocks)), dim3(S::kThreads), 0, P.stream, P);
+    };
     if (P.q)
-      hipLaunchKernelGGL((norm_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, true>), dim3(uint32_t(blocks)),
-                         dim3(S::kThreads), 0, P.stream, P);
+      run(norm_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, true, true>,
+          norm_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, true, false>);
     else
-      hipLaunchKernelGGL((norm_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, false>), dim3(uint32_t(blocks)),
-                         dim3(S::kThreads), 0, P.stream, P);
+      run(norm_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, false, true>,
+          norm_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, false, false>);
   });
 }
 
@@ -259,8 +288,13 @@ template <typename X, typename R>
 void launch_back(const NormRequest& P) {
   by_width(P.D, [&](auto shape) {
     using S = decltype(shape);
-    hipLaunchKernelGGL((norm_backward_kernel<X, R, S::kLanes, S::kWaves, S::kChunks>),
-                       dim3(uint32_t(norm_backward_blocks(P.M, P.D))), dim3(S::kThreads), 0, P.stream, P);
+    auto run = [&](auto* kernel) {
+      hipLaunchKernelGGL(kernel, dim3(uint32_t(norm_backward_blocks(P.M, P.D))), dim3(S::kThreads), 0, P.stream, P);
+    };
+    if (P.D % kV == 0)
+      run(norm_backward_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, true>);
+    else
+      run(norm_backward_kernel<X, R, S::kLanes, S::kWaves, S::kChunks, false>);
   });
 }
 
