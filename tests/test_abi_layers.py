@@ -50,7 +50,7 @@ SHARED = [(dict(B=-1), BAD), (dict(D=-2), BAD), (dict(N=0), BAD), (dict(N=65, ld
 @pytest.mark.parametrize("kw,code", SHARED + [
     (dict(T=-1), BAD), (dict(lengths=at(10, 2)), BAD), (dict(h0=at(10), last=at(10)), BAD), (dict(last=at(8)), BAD),
     (dict(y=at(3, 16)), BAD), (dict(B=1, T=4096, ws=None), BAD), (dict(B=1, T=4096, ws=at(9, 8)), BAD),
-    (dict(B=1, T=4096, n=64), SMALL), (dict(B=1 << 30, T=1), UNSUP)])
+    (dict(B=1, T=4096, n=64), SMALL), (dict(B=1 << 30, T=1), UNSUP), (dict(ld_u=1 << 26), UNSUP), (dict(ld_c=1 << 26), UNSUP)])
 def test_scan_refusals(kw, code):
     assert scan(**kw) == code
     assert lib.scanrnn_last_error()
@@ -88,7 +88,7 @@ def scan_backward(**kw):
     (dict(T=-1), BAD), (dict(dy=None), BAD), (dict(du=None), BAD), (dict(dd=None), BAD), (dict(dB=None), BAD), (dict(dC=None), BAD),
     (dict(dA=None), BAD), (dict(dz=None), BAD), (dict(z=None), BAD), (dict(ld_dy=7), BAD), (dict(ld_dy=1 << 62), BAD),
     (dict(dy=at(8, 2)), BAD), (dict(dA=at(15, 2)), BAD), (dict(du=at(0)), BAD), (dict(du=at(11)), BAD), (dict(dskip=at(17)), BAD),
-    (dict(dh=at(20), dh0=at(20)), BAD), (dict(dB=at(8)), BAD), (dict(ws=None), BAD), (dict(n=64), SMALL)])
+    (dict(dh=at(20), dh0=at(20)), BAD), (dict(dB=at(8)), BAD), (dict(ws=None), BAD), (dict(n=64), SMALL), (dict(ld_dy=1 << 26), UNSUP)])
 def test_scan_backward_refusals(kw, code):
     assert scan_backward(**kw) == code
     assert lib.scanrnn_last_error()
