@@ -2,6 +2,8 @@
 // selective_bwd.hip), the short convolution (conv.hip) and the norm (norm.hip).
 #pragma once
 
+#include <cfloat>
+
 #include "device_util.hpp"
 #include "internal.hpp"
 
@@ -29,7 +31,6 @@ __device__ __forceinline__ T* at_byte(T* base, uint32_t offset) {
 
 // N neighbouring elements at any element: global loads and stores take any
 // address that is a multiple of the element's size.
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <int N, typename T>
 __device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
   if constexpr (sizeof(T) == 4) {
@@ -84,17 +85,6 @@ __device__ __forceinline__ void store_some(T* p, int n, const float (&v)[N]) {
       if (i < n) p[i] = from_f32<T>(v[i]);
   }
 }
-template <typename T>
-__device__ __forceinline__ f32x4 load4(const T* p, int n) {
-  float v[4];
-  load_some(p, n, v);
-  return f32x4{v[0], v[1], v[2], v[3]};
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, f32x4 v, int n) {
-  const float w[4] = {v[0], v[1], v[2], v[3]};
-  store_some(p, n, w);
-}
 
 // Q neighbouring elements as they stand in memory, for loads that are on the way
 // while something else is computed: their conversion waits for them.
@@ -132,7 +122,7 @@ __device__ __forceinline__ void values(const Raw<uint16_t, Q>& r, float (&v)[Q])
 // dropped where the offset is kNowhere: without a branch, so that the loads in
 // flight can be told from the stores behind them and waited for alone.  The
 // elements are aligned as a whole.
-constexpr uint32_t kNowhere = 0xFFFFFFFFu;
+constexpr uint32_t kNowhere = 0x80000000u;  // past the 2^31 - 1 bytes that a store reaches, with what it writes
 template <typename T, int N>
 __device__ __forceinline__ void store_at(T* base, uint32_t offset, const float (&v)[N]) {
   const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, 0x7FFFFFFF, 0x00020000);
@@ -162,6 +152,11 @@ __device__ __forceinline__ void store_at(T* base, uint32_t offset, const float (
 __device__ __forceinline__ float weight_at(const void* w, sr_dtype dtype, int64_t i) {
   return dtype == SR_BF16 ? to_f32(static_cast<const uint16_t*>(w)[i]) : static_cast<const float*>(w)[i];
 }
+
+// A rate of the selective scan, and the factor of a step in its power of two: never minus
+// infinity, so that the steps of zero behind a sequence's end leave the state for any rate.
+__device__ __forceinline__ float bounded(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }
+__device__ __forceinline__ float rate2(float a) { return bounded(a * kLog2e); }
 
 // log(1 + e^x) to a few ulps for any x: max(x, 0) + log1p(e), e = e^-|x|.  With u the
 // rounded 1 + e, log1p(e) = log(u) + (e - (u - 1)) / u; u's rounding error e - (u - 1) is
@@ -285,7 +280,6 @@ __device__ __forceinline__ void column_sums(const float* parts, int64_t rows, in
 
 constexpr int kTile = kSelectiveTile;  // tokens per tile
 constexpr int kLanes = 64;             // channels per workgroup
-constexpr int kNS = 4;                 // states per lane
 
 // Which 64 channels of which sequence and chunk a workgroup has.
 struct Place {

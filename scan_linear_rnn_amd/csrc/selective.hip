@@ -58,7 +58,7 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     const bool is = mine && n0 + i < P.N;
-    a2[i] = is ? P.A[d * P.N + n0 + i] * kLog2e : 0.0f;
+    a2[i] = is ? rate2(P.A[d * P.N + n0 + i]) : 0.0f;
     h[i] = 0.0f;
     if constexpr (!kStates) {
       if (P.ends != nullptr) {  // [chunk][b][n][D]
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(256) void carry_kernel(const SelectiveRequest P, co
   const int64_t bnd = P.B * P.N * P.D;
   if (i >= bnd) return;
   const int64_t d = i % P.D, bn = i / P.D, n = bn % P.N, b = bn / P.N;
-  const float a2 = P.A[d * P.N + n] * kLog2e;
+  const float a2 = rate2(P.A[d * P.N + n]);
   const int64_t own = (b * P.D + d) * P.N + n;
   float h = init ? init[own] : 0.0f;
   constexpr int kAhead = 4;
@@ -348,8 +348,8 @@ __global__ __launch_bounds__(256) void step_kernel(const SelectiveRequest P) {
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      h[r][v] = fmaf(__builtin_amdgcn_exp2f(dt * (a[v] * kLog2e)), h[r][v], du * bm[r][v]);
-      sum = fmaf(h[r][v], has ? cm[r][v] : 0.0f, sum);
+      h[r][v] = fmaf(__builtin_amdgcn_exp2f(dt * rate2(a[v])), h[r][v], du * bm[r][v]);
+      sum = has ? fmaf(h[r][v], cm[r][v], sum) : 0.0f;
     }
 #pragma unroll
     for (int m = 1; m < L; m *= 2) sum += __shfl_xor(sum, m);

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(W * 64) void grad_ends_kernel(const SelectiveReques
   float a2[NS], g[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    a2[i] = mine && n0 + i < P.N ? P.A[d * P.N + n0 + i] * kLog2e : 0.0f;
+    a2[i] = mine && n0 + i < P.N ? rate2(P.A[d * P.N + n0 + i]) : 0.0f;
     g[i] = 0.0f;
   }
   const int at = tid / (kLanes / Q), lc = tid % (kLanes / Q) * Q;
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
       const int n = (g * W + wave) * NS + i;
       const bool is = mine && n < P.N;
       const int64_t m = ((int64_t(p.chunk) * P.B + p.b) * P.N + n) * P.D + d, own = (p.b * P.D + d) * P.N + n;
-      a[g][i] = is ? P.A[d * P.N + n] : 0.0f;
+      a[g][i] = is ? bounded(P.A[d * P.N + n]) : 0.0f;
       start[g][i] = G[g][i] = dA[g][i] = 0.0f;
       if (is && P.chunks > 1) {
         start[g][i] = P.ends[m];
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
       k.x[j] = to_f32(in.delta[j]) + bias;
       k.dy[j] = live ? to_f32(in.dy[j]) : 0.0f;
       const float soft = softplus_f(k.x[j]);
-      k.dt[j] = t >= count ? 0.0f : P.softplus ? soft : k.x[j];
+      k.dt[j] = !mine || t >= count ? 0.0f : P.softplus ? soft : k.x[j];
       float ds = k.dy[j];
       if (kGated) {
         k.z[j] = live ? to_f32(in.z[j]) : 0.0f;
@@ -314,7 +314,7 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
         n.c[g][i] = is ? to_f32(in.Cm[g][i]) : 0.0f;
         n.h[g][i] = mine && n0 + i < P.N ? in.mark[g][i] : 0.0f;
         // a zero state stays zero however its factor overflows
-        const float grown = fmaf(__builtin_amdgcn_exp2f(in.so_far * (a[g][i] * kLog2e)), start[g][i], n.h[g][i]);
+        const float grown = fmaf(__builtin_amdgcn_exp2f(in.so_far * rate2(a[g][i])), start[g][i], n.h[g][i]);
         n.h[g][i] = start[g][i] != 0.0f ? grown : n.h[g][i];
       }
     }
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         h[g][0][i] = n.h[g][i];
-        a2[i] = a[g][i] * kLog2e;
+        a2[i] = rate2(a[g][i]);
       }
       unrolled<kTile>([&](auto token) {
         constexpr int t = decltype(token)::value;

@@ -10,6 +10,8 @@ most 32 elements and 10 halvings, half of whose error reaches the result: 64 u, 
 that for its gradient, whose sum over rows adds at most `rows` more.  bf16
 results are rounded once more: 2^-8 of the value; a code is off by half of its scale."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -214,6 +216,48 @@ def test_norm_shapes_and_strided_rows():
         assert torch.equal(a, b.view(12, 50)) and torch.equal(a, c)
     q, s, t = sr.rms_norm_quantize(x.view(3, 4, 50), w, r.view(3, 4, 50))
     assert q.shape == (3, 4, 128) and s.shape == (3, 4) and t.shape == (3, 4, 50)
+
+
+def test_the_sum_may_take_the_residuals_place():
+    say("norm, total in place")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    lib = sr.raw_library()
+    for D in (9, 200, 2048, 5000, 10000):
+        x, r, w, _ = norm_case(37, D, "bf16", "fp32")
+        want, total = sr.rms_norm_forward(x, w, r)
+        y = torch.empty_like(x)
+        st = lib.rms_norm_forward(37, D, p(x), D, 1, p(r), D, 0, p(w), 1, 1e-6, p(r), p(y),
+                                  ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert st == 0, lib.scanrnn_last_error()
+        assert torch.equal(r, total) and torch.equal(y, want), D
+
+
+def test_rows_past_four_gigabytes():
+    """Inputs and results of more than 2^32 elements: their last rows are those of a small call."""
+    say("norm and convolution, large tensors")
+    rows = (1 << 32) // 2048 + 1000
+    x = torch.randn(rows, 2048, dtype=torch.bfloat16, device="cuda")
+    w = torch.rand(2048, device="cuda").bfloat16()
+    part = slice(rows - 70, rows)
+    y, total = sr.rms_norm_forward(x, w, x)
+    for big, small in zip((y, total), sr.rms_norm_forward(x[part], w, x[part])):
+        assert torch.equal(big[part], small)
+    dx = sr.rms_norm_backward(y, w, total)[0]
+    assert torch.equal(dx[part], sr.rms_norm_backward(y[part], w, total[part])[0])
+    del dx, total
+    q, s, _ = sr.rms_norm_quantize(x, w, x)
+    for big, small in zip((q, s), sr.rms_norm_quantize(x[part], w, x[part])):
+        assert torch.equal(big[part], small)
+    del q, s
+    f = torch.randn(2048, 4, device="cuda").bfloat16()
+    x3, y3 = x.view(1, rows, 2048), y.view(1, rows, 2048)
+    out = sr.causal_conv_forward(x3, f, silu=True)
+    assert torch.equal(out[:, part], sr.causal_conv_forward(x3[:, part], f, silu=True, state=x3[:, rows - 73:rows - 70]))
+    dx = sr.causal_conv_backward(x3, f, y3, silu=True)[0]
+    some = sr.causal_conv_backward(x3[:, part], f, y3[:, part], silu=True, state=x3[:, rows - 73:rows - 70])[0]
+    assert torch.equal(dx[:, part], some)
+    del x, y, x3, y3, out, dx, some
+    torch.cuda.empty_cache()
 
 
 def test_many_rows_of_each_width_repeat():

@@ -12,6 +12,8 @@ summed steps (at most 16, of partial sums that grow: half of them on average).  
 |x| <= 8 that is below 48 X u; X is at most 87 before the term leaves the fp32 range, and in
 these cases at most XMAX.  bf16 results are rounded once more: 2^-8 of the value."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -242,6 +244,107 @@ def test_strong_decay_and_large_steps():
     near(y, want[0], size[0] * 2, 70, "y")
     near(last, want[1], size[1] * 2, 70, "h")
     assert all(torch.isfinite(t).all() for t in sr.selective_scan_backward(*args(c), c["dy"], **given(c)))
+
+
+@pytest.mark.parametrize("N", [9, 12, 16])
+def test_a_step_from_an_infinite_state(N):
+    """Lanes without a state add nothing, whatever the others hold."""
+    say("selective step, infinite state", N)
+    c = case(2, 1, 5, N, dtype="fp32", gated=False)
+    tok = [t[:, 0] if t.dim() > 2 else t for t in args(c)]
+    c["h0"][1, 3, 0] = float("inf")
+    c["C"].abs_()
+    y, h = sr.selective_step(*tok, skip=c["skip"], delta_bias=c["bias"], delta_softplus=True, h_prev=c["h0"])
+    want, size = reference(c), reference(c, magnitudes=True)
+    assert y[1, 3] == float("inf") and h[1, 3, 0] == float("inf")
+    ok = np.isfinite(want[0][:, 0])
+    assert ok.sum() == 9
+    assert (np.abs(host(y) - want[0][:, 0])[ok] <= (2 + 64 + 48 * XMAX) * U * size[0][:, 0][ok]).all()
+
+
+def test_a_rate_of_minus_infinity():
+    """Such a state forgets at once; the steps of zero behind a sequence's end leave it all the same."""
+    say("selective scan, A = -inf")
+    for T in (40, 200):
+        c = case(3, T, 70, 16, dtype="fp32", lengths=[T, 21, 0])
+        c["A"][3, 2] = c["A"][65, 15] = -1e30  # exp(-1e30 dt) is zero in 64 bits too
+        want, size = reference(c, c["dy"], c["dh"]), reference(c, c["dy"], c["dh"], True)
+        c["A"][3, 2] = c["A"][65, 15] = float("-inf")
+        y, last = sr.selective_scan_forward(*args(c), **given(c), return_last=True)
+        near(y, want[0], size[0], T, "y")
+        near(last, want[1], size[1], T, "h_last")
+        got = dict(zip(GRADS, sr.selective_scan_backward(*args(c), c["dy"], dh_last=c["dh"], **given(c))))
+        for name in GRADS:
+            near(got[name], want[2][name], size[2][name], T + (3 * T if name in ("dA", "dskip", "dbias") else 0), name)
+        tok = [t[:, 0] if t.dim() > 2 else t for t in args(c)]
+        y1, h1 = sr.selective_step(*tok, skip=c["skip"], z=c["z"][:, 0], delta_bias=c["bias"], delta_softplus=True, h_prev=c["h0"])
+        near(y1[:2], want[0][:2, 0], size[0][:2, 0], 1, "token")
+        assert torch.isfinite(h1).all()
+
+
+@pytest.mark.parametrize("shape", [(1, 300, 130, 64, 2), (2, 180, 10, 6, 2), (1, 200, 37, 33, 1), (1, 150, 66, 20, 2),
+                                   (230, 140, 5, 16, 1)])
+def test_long_sequences_of_odd_widths(shape):
+    """Cut into chunks, or too many for it, where rows are not taken whole."""
+    say("selective scan", shape)
+    c = case(*shape, dtype="bf16")
+    check_forward(c)
+    check_backward(c)
+
+
+def test_outputs_at_an_odd_element():
+    """y where no wide store may go, through the C entry point."""
+    say("selective scan, y at an odd element")
+    B, T, D, N = 2, 30, 64, 16
+    c = case(B, T, D, N, dtype="bf16")
+    want = sr.selective_scan_forward(*args(c), **given(c))
+    buf = torch.full((B * T * D + 2,), 7.0, dtype=torch.bfloat16, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    lib = sr.raw_library()
+    st = lib.selective_scan_forward(B, T, D, N, 1, p(c["u"]), D, p(c["delta"]), D, p(c["z"]), D, p(c["B"]), N, p(c["C"]), N, 1,
+                                    p(c["A"]), p(c["skip"]), p(c["bias"]), 1, p(c["h0"]), None, p(buf[1:]), None, None, 0,
+                                    ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0, lib.scanrnn_last_error()
+    assert torch.equal(buf[1:-1].view(B, T, D), want)
+    assert buf[0] == 7 and buf[-1] == 7
+
+
+def test_rows_past_four_gigabytes():
+    """Rows as far apart as they may be (2^25 elements): offsets pass 2^32 elements, and the results 2^32 bytes."""
+    say("selective scan, rows 2^25 elements apart")
+    T, D, N = 140, 9, 5
+    c = case(1, T, D, N, dtype="bf16")
+    far = torch.empty(1, T, 1 << 25, dtype=torch.bfloat16, device="cuda")
+    assert far.numel() > 1 << 32
+    v, at = dict(c), (1 << 25) - 64
+    for name in ("u", "delta", "z", "B", "C", "dy"):
+        flat = c[name].reshape(1, T, -1)
+        part = far[..., at:at + flat.shape[2]]
+        part.copy_(flat)
+        v[name] = part.unsqueeze(2) if name in ("B", "C") else part
+        at += flat.shape[2]
+    want = sr.selective_scan_forward(*args(c), **given(c), return_last=True)
+    got = sr.selective_scan_forward(*args(v), **given(v), return_last=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    grads = sr.selective_scan_backward(*args(c), c["dy"], dh_last=c["dh"], **given(c))
+    again = sr.selective_scan_backward(*args(v), v["dy"], dh_last=c["dh"], **given(v))
+    for name, a, b in zip(GRADS, again, grads):
+        assert torch.equal(a.flatten(), b.flatten()), name
+    del far, v
+    say("selective scan, large results")
+    B, T, D, N = 45, 100, 1 << 20, 1
+    u = torch.randn(B, T, D, dtype=torch.bfloat16, device="cuda")
+    A, bc = -torch.rand(D, N, device="cuda"), torch.randn(B, T, 1, N, dtype=torch.bfloat16, device="cuda")
+    y = sr.selective_scan_forward(u, u, A, bc, bc, delta_softplus=True)
+    assert y.numel() > 1 << 32
+    part = slice(B - 2, B)
+    assert torch.equal(y[part], sr.selective_scan_forward(u[part], u[part], A, bc[part], bc[part], delta_softplus=True))
+    dA_all = sr.selective_scan_backward(u, u, A, bc, bc, u, delta_softplus=True)
+    for whole, own in zip(dA_all[:2] + dA_all[3:5], range(4)):
+        some = sr.selective_scan_backward(u[part], u[part], A, bc[part], bc[part], u[part], delta_softplus=True)
+        assert torch.equal(whole[part], (some[:2] + some[3:5])[own]), own
+    del u, y, dA_all, whole, some
+    torch.cuda.empty_cache()
 
 
 def test_growing_states_from_zero():
