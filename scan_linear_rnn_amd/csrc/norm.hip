@@ -8,9 +8,9 @@
 //     n = t / rms,  g = dy w,  dx = (g - n mean(g n)) / rms + dt,  dw = sum over rows of dy n
 //
 // Bound by the rows' bytes: a row is read once and stays in registers, 8 elements
-// per lane at a time; a row has 16 lanes, 32, a wave or several, by its length.  The
-// rows of a workgroup are strided by the grid, so that the weight is loaded once for
-// all of them.
+// per lane at a time; a row has 16 lanes, 32, a wave or several, by its length.  Sum and
+// 8-bit codes of 131072 x 2048 in bf16 take 337 us (5.6 TB/s); the backward pass of 16384 x
+// 2048 with fp32 sums 83 us and 5 for the weight's gradient (5.7 TB/s).
 
 #include "layer_util.hpp"
 #include "quant.hpp"
@@ -247,18 +247,37 @@ struct Shape {
   static constexpr int kThreads = WPR > 4 ? WPR * 64 : 256;
   static constexpr int kRows = kThreads / (LPR * WPR);
 };
-// Calls f with the lanes, waves and chunks per lane for rows of D elements
-// (for codes: the padded row).
-template <typename F>
+// Calls f with the lanes, waves and chunks per lane for rows of D elements (for codes:
+// the padded row): as few lanes as hold a row in one or two chunks each, so that no lane
+// idles and the reductions are short, and four waves from 1024 elements on.  Measured in us,
+// bf16, one wave / four: codes of 131072 x 2048 346 / 337, of 256 x 2048 6.5 / 4.1; fp32 sums:
+// codes of 131072 x 2048 559 / 516, their backward 575 / 548, of 256 rows 12.1 / 7.1; 131072 x 1024
+// codes 173 / 271.  Four waves of four chunks / of two, 65536 x 4096: codes 458 / 336, backward with
+// fp32 sums 614 / 521.  Up to 8192 the forward kernels are faster with eight waves of two chunks than
+// with four of four (32768 rows of codes 348 / 336, 1024 rows 16.2 / 14.3), the backward kernel is
+// not (563 / 526).
+template <bool kBackward, typename F>
 void by_width(int64_t D, F f) {
   if (D <= 16 * kV) return f(Shape<16, 1, 1>{});
   if (D <= 32 * kV) return f(Shape<32, 1, 1>{});
   if (D <= 64 * kV) return f(Shape<64, 1, 1>{});
   if (D <= 2 * 64 * kV) return f(Shape<64, 1, 2>{});
-  if (D <= 4 * 64 * kV) return f(Shape<64, 1, 4>{});
-  if (D <= 4 * 256 * kV) return f(Shape<64, 4, 4>{});
+  if (D <= 256 * kV) return f(Shape<64, 4, 1>{});
+  if (D <= 2 * 256 * kV) return f(Shape<64, 4, 2>{});
+  if (D <= 4 * 256 * kV) return f(Shape<64, kBackward ? 4 : 8, kBackward ? 4 : 2>{});
   return f(Shape<64, 8, 4>{});
 }
+
+// Workgroups.  Forward: one for its few rows, and no loop in it, is faster than as many as the CUs
+// hold, each with its share of the rows (the loop's stores are in the way of the next row's loads):
+// 1024 / 8192 / one each, us: 131072 x 2048 codes 373 / 406 / 337, 1048576 x 128 198 / 188 / 168, but
+// 16384 x 16384 384 / 431 / 431, whose workgroups fill half of a CU.  The backward kernel writes its
+// sums for the weight once per workgroup: with 256 / 512 / 1024 of them 131072 x 2048 takes 951 / 548 /
+// 564, 8192 x 4096 90 / 72 / 79, 1024 x 16384 50 / 57 / 70, 65536 x 512 70 / 44 / 36.
+template <typename S>
+constexpr int64_t kForwardBlocks = S::kWaves * S::kChunks == 32 ? 1024 : 1 << 20;
+template <typename S>
+constexpr int64_t kBackwardBlocks = S::kWaves == 1 ? 1024 : S::kWaves == 4 ? 512 : 256;
 
 sr_status launched(const char* what) {
   const hipError_t err = hipGetLastError();
@@ -269,9 +288,9 @@ int64_t capped(int64_t blocks, int64_t most) { return blocks < most ? blocks : m
 
 template <typename X, typename R>
 void launch_forward(const NormRequest& P) {
-  by_width(P.q ? P.ld_q : P.D, [&](auto shape) {
+  by_width<false>(P.q ? P.ld_q : P.D, [&](auto shape) {
     using S = decltype(shape);
-    const int64_t blocks = capped((P.M + S::kRows - 1) / S::kRows, 2048);
+    const int64_t blocks = capped((P.M + S::kRows - 1) / S::kRows, kForwardBlocks<S>);
     auto run = [&](auto* whole, auto* any) {
       hipLaunchKernelGGL(P.D % kV == 0 ? whole : any, dim3(uint32_t(blocks)), dim3(S::kThreads), 0, P.stream, P);
     };
@@ -286,7 +305,7 @@ void launch_forward(const NormRequest& P) {
 
 template <typename X, typename R>
 void launch_back(const NormRequest& P) {
-  by_width(P.D, [&](auto shape) {
+  by_width<true>(P.D, [&](auto shape) {
     using S = decltype(shape);
     auto run = [&](auto* kernel) {
       hipLaunchKernelGGL(kernel, dim3(uint32_t(norm_backward_blocks(P.M, P.D))), dim3(S::kThreads), 0, P.stream, P);
@@ -302,7 +321,10 @@ void launch_back(const NormRequest& P) {
 
 int64_t norm_backward_blocks(int64_t M, int64_t D) {
   int64_t blocks = 0;
-  by_width(D, [&](auto shape) { blocks = capped((M + decltype(shape)::kRows - 1) / decltype(shape)::kRows, 1024); });
+  by_width<true>(D, [&](auto shape) {
+    using S = decltype(shape);
+    blocks = capped((M + S::kRows - 1) / S::kRows, kBackwardBlocks<S>);
+  });
   return blocks;
 }
 

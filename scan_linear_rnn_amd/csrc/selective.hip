@@ -404,8 +404,9 @@ void launch_step(const SelectiveRequest& P) {
     const int64_t blocks = ((P.B + R - 1) / R * P.D + 256 / L - 1) / (256 / L);
     hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(256), 0, P.stream, P);
   };
-  // Four streams per thread where that leaves every CU eight workgroups.
-  if (P.B / 4 * P.D * L >= 256 * 8 * 256)
+  // Four streams per thread where that leaves two waves per SIMD.  Measured in us, D = 2048,
+  // 16 states, one stream / four: 32 streams 4.1 / 4.7, 64 6.0 / 5.9, 128 9.6 / 8.4, 1024 51.6 / 46.2.
+  if (P.B / 4 * P.D * L >= 2 * 4 * 256 * 64)
     run(step_kernel<T, V, L, 4>, 4);
   else
     run(step_kernel<T, V, L, 1>, 1);

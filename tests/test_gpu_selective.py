@@ -232,6 +232,12 @@ def test_single_tokens(B, D, N, G, dtype):
         assert torch.equal(y1, y0)
 
 
+@pytest.mark.parametrize("B,D,N,G", [(67, 2048, 16, 1), (70, 512, 33, 2), (257, 1024, 8, 4), (131, 4096, 1, 1)])
+def test_single_tokens_of_many_streams(B, D, N, G):
+    """Several streams per thread, a number of them that leaves some threads without."""
+    test_single_tokens(B, D, N, G, "bf16")
+
+
 def test_strong_decay_and_large_steps():
     """Steps that wipe the state, and decays that underflow."""
     say("selective scan, strong decay")
