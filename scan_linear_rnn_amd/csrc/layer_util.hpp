@@ -204,17 +204,51 @@ __device__ __forceinline__ float row_dot(const float (&m)[2], const float (&x)[2
       : "v"(m[0]), "v"(m[1]), "v"(x[0]), "v"(x[1]), "i"(n));
   return sum;
 }
+// Two of them, n and n + 1: neither has to wait for its own last product.
 template <int n>
-__device__ __forceinline__ float row_dot(const float (&m)[4], const float (&x)[4]) {
-  float sum;
+__device__ __forceinline__ void row_dots(const float (&m)[1], const float (&x)[1], const float (&y)[1], float& sx, float& sy) {
+  sx = row_times<n>(m[0], x[0]);
+  sy = row_times<n + 1>(m[0], y[0]);
+}
+template <int n>
+__device__ __forceinline__ void row_dots(const float (&m)[2], const float (&x)[2], const float (&y)[2], float& sx, float& sy) {
   asm("s_nop 1\n\t"
-      "v_mul_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
-      "v_fmac_f32_dpp %0, %2, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
-      "v_fmac_f32_dpp %0, %3, %7 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
-      "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
-      : "=&v"(sum)
-      : "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "i"(n));
-  return sum;
+      "v_mul_f32_dpp %0, %2, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %1, %2, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %3, %5 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %3, %7 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+      : "=&v"(sx), "=&v"(sy)
+      : "v"(m[0]), "v"(m[1]), "v"(x[0]), "v"(x[1]), "v"(y[0]), "v"(y[1]), "i"(n), "i"(n + 1));
+}
+template <int n>
+__device__ __forceinline__ void row_dots(const float (&m)[4], const float (&x)[4], const float (&y)[4], float& sx, float& sy) {
+  asm("s_nop 1\n\t"
+      "v_mul_f32_dpp %0, %2, %6 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %1, %2, %10 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %3, %7 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %3, %11 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %4, %12 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %0, %5, %9 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %5, %13 row_newbcast:%15 row_mask:0xf bank_mask:0xf"
+      : "=&v"(sx), "=&v"(sy)
+      : "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(y[0]), "v"(y[1]),
+        "v"(y[2]), "v"(y[3]), "i"(n), "i"(n + 1));
+}
+
+template <int n>
+__device__ __forceinline__ void row_dots(const float (&m)[8], const float (&x)[8], const float (&y)[8], float& sx, float& sy) {
+  const auto half = [](const float (&v)[8], int at, float (&to)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = v[at + i];
+  };
+  float a[4], b[4], c[4], bx, by;
+  half(m, 0, a), half(x, 0, b), half(y, 0, c);
+  row_dots<n>(a, b, c, sx, sy);
+  half(m, 4, a), half(x, 4, b), half(y, 4, c);
+  row_dots<n>(a, b, c, bx, by);
+  sx += bx;
+  sy += by;
 }
 
 // y[i] += m[i][n] x with m[i][n] in lane n of each row of 16.
@@ -239,6 +273,21 @@ __device__ __forceinline__ void row_add(const float (&m)[4], float x, float (&y)
       "v_fmac_f32_dpp %3, %7, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
       : "+&v"(y[0]), "+&v"(y[1]), "+&v"(y[2]), "+&v"(y[3])
       : "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "v"(x), "i"(n));
+}
+
+template <int n>
+__device__ __forceinline__ void row_add(const float (&m)[8], float x, float (&y)[8]) {
+  asm("s_nop 1\n\t"
+      "v_fmac_f32_dpp %0, %8, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %9, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %2, %10, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %3, %11, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %4, %12, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %5, %13, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %6, %14, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %7, %15, %16 row_newbcast:%17 row_mask:0xf bank_mask:0xf"
+      : "+&v"(y[0]), "+&v"(y[1]), "+&v"(y[2]), "+&v"(y[3]), "+&v"(y[4]), "+&v"(y[5]), "+&v"(y[6]), "+&v"(y[7])
+      : "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "v"(m[4]), "v"(m[5]), "v"(m[6]), "v"(m[7]), "v"(x), "i"(n));
 }
 
 // Calls f with 0 .. n - 1 as constants.

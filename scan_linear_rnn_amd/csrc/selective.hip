@@ -7,19 +7,27 @@
 // with A per channel and state, and B, C per token (shared by the channels of
 // a group).  States, sums and gates are fp32; y is rounded once.
 //
-// A workgroup owns 64 channels (a lane each) of one sequence and walks over
-// its tokens in tiles of 16; its waves hold four states per lane each.  The
+// A workgroup owns 64 channels (a lane each) of one sequence and walks over its
+// tokens in tiles of 16; its waves hold one to eight states per lane each (four
+// waves of four for 16 states).  B and C go from memory to lanes, token t in lane t of
+// each row of 16, and from there into products as operands across lanes.  The
 // waves share what is per token and channel: each prepares a part of the
-// tile's steps (softplus and the like) in LDS, and sums its part of the
-// waves' shares of y.  So every input is read once, wide, and the
-// recurrence, 16 x (2 products, exp, 2 fused multiply-adds), is what the
-// vector units spend their time on.
+// tile's steps (softplus and the like) in LDS, and sums its part of the waves'
+// shares of y.  So every input is read once, wide, and the recurrence, 16 x (2
+// products, exp, 2 fused multiply-adds), is what the vector units spend their time on.
 //
 // Where there are too few sequences and channels to fill the GPU, the tokens are
-// cut into chunks: a first pass (kStates) computes what each chunk adds to a
+// cut into chunks: a first pass (kEnds) computes what each chunk adds to a
 // zero state and the sum of its steps, whose exponential is the chunk's decay; one
 // thread per state then carries the states over the chunks (carry_kernel); and the
 // full pass starts each chunk from its own state.
+//
+// 8 x 4096 x 2048, 16 states, gated, bf16: 360 us (1.5 TB/s, 3.0e12 states a second).  Bound by what
+// a SIMD issues: about 430 instructions per wave and tile, 64 of them exponentials at two
+// slots, where the recurrence with the sum over states alone takes 400 slots of 4 cycles (a
+// probe of it 190 us).  Eight waves of two states take as long: what they hide, their LDS
+// reads cost.  1 x 65536 x 1024 in 96 chunks: 460 us (first
+// pass 207, carry 17, outputs 296 where each is traced).
 
 #include "layer_util.hpp"
 
@@ -37,8 +45,8 @@ enum Pass {
 // While the waves go through tile k, each thread also prepares its part of tile
 // k + 1's steps, sums its part of tile k - 1's outputs and has tile k + 2's inputs on
 // their way: everything between two barriers is independent, one barrier per tile.
-template <typename T, int W, int NS, int kPass, bool kWhole>
-__global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel(const SelectiveRequest P) {
+template <typename T, int W, int NS, int kPass, bool kWhole, bool kGated>
+__global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void scan_kernel(const SelectiveRequest P) {
   constexpr bool kStates = kPass != kOutputs;
   constexpr int Q = kTile / W;  // neighbouring channels of a token that a thread prepares
   __shared__ __align__(16) float2 s_step[2][kTile][kLanes];  // dt, dt u
@@ -94,9 +102,10 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
   int64_t ahead = first;
   // The next tile's inputs, as they stand in memory; behind the last tile that one
   // again, behind the last token that one again.
-  auto fetch = [&](Inputs& in) {
+  auto fetch = [&](auto inner, Inputs& in) {
+    constexpr bool kInner = decltype(inner)::value;
     uint32_t b_u = o_u, b_d = o_d, b_z = o_z, b_b = o_b, b_c = o_c;
-    if (ahead + kTile > P.T) {
+    if (!kInner && ahead + kTile > P.T) {
       const int last = int(P.T - 1 - ahead), t = at < last ? at : last, tb = bc_at < last ? bc_at : last;
       b_u = bytes(t, P.ld_u, c);
       b_d = bytes(t, P.ld_delta, c);
@@ -106,42 +115,39 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
     }
     load_raw<kWhole>(at_byte(pu, b_u), nc, in.u);
     load_raw<kWhole>(at_byte(pd, b_d), nc, in.delta);
-    if (!kStates && P.z) load_raw<kWhole>(at_byte(pz, b_z), nc, in.z);
+    if constexpr (kGated) load_raw<kWhole>(at_byte(pz, b_z), nc, in.z);
     load_raw<kWhole>(at_byte(pb, b_b), nn, in.Bm);
     if constexpr (!kStates) load_raw<kWhole>(at_byte(pc, b_c), nn, in.Cm);
-    if (ahead + kTile < end) {
+    if (kInner || ahead + kTile < end) {
       ahead += kTile;
       pu += kTile * P.ld_u, pd += kTile * P.ld_delta, pb += kTile * P.ld_b;
-      if constexpr (!kStates) pz += kTile * P.ld_z, pc += kTile * P.ld_c;
+      if constexpr (!kStates) pc += kTile * P.ld_c;
+      if constexpr (kGated) pz += kTile * P.ld_z;
     }
   };
   // Converts what was fetched for the tile at t0 and writes its steps.
-  auto prepare = [&](int64_t t0, int buffer, const Inputs& in, float (&bm)[NS], float (&cm)[NS]) {
+  auto prepare = [&](auto inner, int64_t t0, int buffer, const Inputs& in, float (&bm)[NS], float (&cm)[NS]) {
     float u[Q], dt[Q], du[Q];
     values(in.u, u);
     values(in.delta, dt);
 #pragma unroll
     for (int e = 0; e < Q; ++e) dt[e] += bias[e];
-    if (P.softplus) {
 #pragma unroll
-      for (int e = 0; e < Q; ++e) dt[e] = softplus_f(dt[e]);
+    for (int e = 0; e < Q; ++e) {
+      const float soft = softplus_f(dt[e]);
+      dt[e] = P.softplus ? soft : dt[e];
     }
 #pragma unroll
     for (int e = 0; e < Q; ++e) du[e] = dt[e] * u[e];
     values(in.Bm, bm);
     if constexpr (!kStates) values(in.Cm, cm);
-    if (t0 + kTile > end) {  // behind the end the state stays, whatever stands there
+    if (!decltype(inner)::value && t0 + kTile > end) {  // behind the end the state stays, whatever stands there
 #pragma unroll
       for (int e = 0; e < Q; ++e)
         if (t0 + at >= end) dt[e] = du[e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
         if (t0 + bc_at >= end) bm[i] = cm[i] = 0.0f;
-    }
-    if (!kWhole || n0 >= P.N) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (n0 + i >= P.N) bm[i] = cm[i] = 0.0f;
     }
     float pair[2 * Q];
 #pragma unroll
@@ -150,6 +156,20 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
       pair[2 * e + 1] = du[e];
     }
     __builtin_memcpy(__builtin_assume_aligned(&s_step[buffer][at][lc], Q > 1 ? 16 : 8), pair, 8 * Q);
+  };
+  // Takes over what was prepared, once the tile before is done with its own.
+  float b0[NS], c0[NS];
+  auto take = [&](const float (&bm)[NS], const float (&cm)[NS]) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      b0[i] = bm[i];
+      c0[i] = cm[i];
+    }
+    if (!kWhole || n0 >= P.N) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (n0 + i >= P.N) b0[i] = c0[i] = 0.0f;
+    }
   };
   // The waves' shares of y for a thread's token.
   auto collect = [&](int buffer, float (&part)[W][Q]) {
@@ -167,7 +187,7 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
     for (int w = 0; w < W; ++w)
 #pragma unroll
       for (int e = 0; e < Q; ++e) sum[e] += part[w][e];
-    if (P.z) {
+    if constexpr (kGated) {
       values(rz, z);
 #pragma unroll
       for (int e = 0; e < Q; ++e) sum[e] *= z[e] * logistic_f(z[e]);
@@ -183,9 +203,9 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
   float total = 0.0f;  // of the steps (the first wave's)
   Inputs in[2];        // of the next tile and the one after it
   Raw<T, Q> u0{}, z0{}, u1{}, z1{};  // of the present tile and the one before it
-  float b0[NS], c0[NS];
-  // One tile, at t0: the waves go through it, in[s] is the next one's input.
-  auto tile = [&](auto parity, int64_t t0) {
+  // One tile, at t0: the waves go through it, in[s] is the next one's input.  kInner: the four
+  // behind it are whole, and nothing is asked on the way.
+  auto tile = [&](auto inner, auto parity, int64_t t0) {
     constexpr int s = decltype(parity)::value;
     float2 step[kTile];
 #pragma unroll
@@ -194,9 +214,9 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
     if constexpr (!kStates) collect(s ^ 1, part);
     __builtin_amdgcn_sched_barrier(0);  // all reads first: a wait for each would follow else
     float bm[NS], cm[NS];
-    prepare(t0 + kTile, s ^ 1, in[s], bm, cm);
+    prepare(inner, t0 + kTile, s ^ 1, in[s], bm, cm);
     const Raw<T, Q> un = in[s].u, zn = in[s].z;
-    fetch(in[s]);
+    fetch(inner, in[s]);
     if constexpr (kPass == kMarks) {  // [tile][b][n][D], the steps as one more state
       float* mark = P.marks + (t0 / kTile * P.B + p.b) * (P.N + 1) * P.D + p.c0;
 #pragma unroll
@@ -207,41 +227,63 @@ __global__ __launch_bounds__(W * 64, W > 8 ? 4 : kPass ? 3 : 2) void scan_kernel
       const float v[1] = {total};
       store_at(mark + P.N * P.D, mine && wave == 0 ? uint32_t(lane) * 4 : kNowhere, v);
     }
-    unrolled<kTile>([&](auto token) {
-      constexpr int t = decltype(token)::value;
+    auto token = [&](auto which) {
+      constexpr int t = decltype(which)::value;
       if constexpr (kStates) total += step[t].x;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
         h[i] = fmaf(__builtin_amdgcn_exp2f(step[t].x * a2[i]), h[i],
                     kStates ? row_times<t>(b0[i], step[t].y) : of_row<t>(b0[i]) * step[t].y);
-      if constexpr (!kStates) s_y[s][wave][t][lane] = row_dot<t>(c0, h);
+    };
+    unrolled<kTile / 2>([&](auto pair) {
+      constexpr int t = 2 * decltype(pair)::value;
+      float before[NS];
+      token(std::integral_constant<int, t>{});
+#pragma unroll
+      for (int i = 0; i < NS; ++i) before[i] = h[i];
+      token(std::integral_constant<int, t + 1>{});
+      if constexpr (!kStates) {
+        float y0, y1;
+        row_dots<t>(c0, before, h, y0, y1);
+        s_y[s][wave][t][lane] = y0;
+        s_y[s][wave][t + 1][lane] = y1;
+      }
+      // Two tokens after two: the products of all, made ahead, would not fit the registers.
+#pragma unroll
+      for (int i = 0; i < NS; ++i) asm volatile("" : "+v"(h[i]));
     });
     if constexpr (!kStates) {
       finish(t0 - kTile, part, u1, z1);
       u1 = u0, z1 = z0;
       u0 = un, z0 = zn;
     }
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      b0[i] = bm[i];
-      c0[i] = cm[i];
-    }
+    take(bm, cm);
     __syncthreads();
   };
   if (first < end) {
-    fetch(in[1]);
-    fetch(in[0]);
-    prepare(first, 0, in[1], b0, c0);
+    constexpr std::false_type kAny{};
+    constexpr std::true_type kInner{};
+    constexpr std::integral_constant<int, 0> kEven{};
+    constexpr std::integral_constant<int, 1> kOdd{};
+    float bm[NS], cm[NS];
+    fetch(kAny, in[1]);
+    fetch(kAny, in[0]);
+    prepare(kAny, first, 0, in[1], bm, cm);
+    take(bm, cm);
     u0 = in[1].u, z0 = in[1].z;
-    fetch(in[1]);
+    fetch(kAny, in[1]);
     __syncthreads();
     int64_t t0 = first;
+    for (; t0 + 5 * kTile < end; t0 += 2 * kTile) {  // (a token is left to fetch)
+      tile(kInner, kEven, t0);
+      tile(kInner, kOdd, t0 + kTile);
+    }
     for (; t0 + kTile < end; t0 += 2 * kTile) {
-      tile(std::integral_constant<int, 0>{}, t0);
-      tile(std::integral_constant<int, 1>{}, t0 + kTile);
+      tile(kAny, kEven, t0);
+      tile(kAny, kOdd, t0 + kTile);
     }
     const bool odd = t0 < end;
-    if (odd) tile(std::integral_constant<int, 0>{}, t0);
+    if (odd) tile(kAny, kEven, t0);
     if constexpr (!kStates) {
       float part[W][Q];
       collect(odd ? 0 : 1, part);
@@ -370,19 +412,27 @@ __global__ __launch_bounds__(256) void step_kernel(const SelectiveRequest P) {
   }
 }
 
-template <typename T, int W, int NS>
-void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
+template <typename T, int W, int NS, int kPass, bool kGated = false>
+void launch_pass(const SelectiveRequest& P, uint32_t blocks) {
   constexpr int Q = kTile / W;
   const bool whole =
       P.D / P.G % Q == 0 && P.N % NS == 0 && reinterpret_cast<uintptr_t>(P.y) % (Q * sizeof(T)) == 0;
   auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(W * 64), 0, P.stream, P); };
-  auto either = [&](auto* all, auto* any) { whole ? run(all) : run(any); };
-  if (pass == kOutputs)
-    either(scan_kernel<T, W, NS, kOutputs, true>, scan_kernel<T, W, NS, kOutputs, false>);
-  else if (pass == kEnds)
-    either(scan_kernel<T, W, NS, kEnds, true>, scan_kernel<T, W, NS, kEnds, false>);
+  if (whole)
+    run(scan_kernel<T, W, NS, kPass, true, kGated>);
   else
-    either(scan_kernel<T, W, NS, kMarks, true>, scan_kernel<T, W, NS, kMarks, false>);
+    run(scan_kernel<T, W, NS, kPass, false, kGated>);
+}
+template <typename T, int W, int NS>
+void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
+  if (pass == kEnds)
+    launch_pass<T, W, NS, kEnds>(P, blocks);
+  else if (pass == kMarks)
+    launch_pass<T, W, NS, kMarks>(P, blocks);
+  else if (P.z)
+    launch_pass<T, W, NS, kOutputs, true>(P, blocks);
+  else
+    launch_pass<T, W, NS, kOutputs, false>(P, blocks);
 }
 template <typename T>
 void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
@@ -395,7 +445,7 @@ void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
   else if (P.N <= 32)
     launch_scan<T, 8, 4>(P, pass, blocks);
   else
-    launch_scan<T, 16, 4>(P, pass, blocks);
+    launch_scan<T, 8, 8>(P, pass, blocks);
 }
 
 template <typename T, int V, int L>

@@ -10,17 +10,24 @@
 //     G_n  <- a_n G_n
 //     ddelta = ddt sigma(delta + bias),  dz = dy s silu'(z)
 //
-// The states are computed again from marks: the forward's first pass
-// (scan_kernel with kStates) writes what each chunk has made of a zero state in front of
+// The states are computed again from marks: the forward's first pass (scan_kernel
+// with kMarks) writes what each chunk has made of a zero state in front of
 // every 16 tokens, and the sum of its steps there, so that the state itself is one
 // exponential and one product away from the chunk's start.  A workgroup then owns
 // 64 channels of one chunk, a lane each, goes back over its tiles of 16
-// tokens, runs each forward into registers and back again.  The sums over
-// channels, dB and dC, are 64 values each per wave and tile (16 tokens, 4 states) to be
-// summed over 64 lanes: a halving exchange (swaps of half waves, then of rows,
-// then DPP) leaves one sum in every lane at about two instructions per value,
-// where separate sums would take six.  They go out per 64 channels and
-// reduce_kernel adds those up, always in the same order.
+// tokens, runs each forward into registers and back again; its eight waves hold two
+// states per lane each (four of one or two up to eight states; above 16 each wave goes through
+// two or four such groups of states, whose forward walk is repeated for each half of
+// a tile).  The sums over channels, dB and dC, are 32 values each per wave and half
+// tile (8 tokens, 2 states, both) to be summed over 64 lanes: a halving exchange (swaps of
+// half waves, then of rows, then DPP) leaves one sum in every lane at about two
+// instructions per value, where separate sums would take six.  They go out per 64
+// channels and reduce_tokens_kernel adds those up, always in the same order.
+//
+// 8 x 2048 x 1024, 16 states, gated, bf16: 452 us, of them marks 63, the gradients in front of
+// the chunks 63, two carries 10, this kernel 310 to 350, sums 17.  Its vector units are busy
+// for 65% of its time: a workgroup takes 123 KB of LDS, so a SIMD has two waves to choose from.
+// 32 states 988 us; 64 states, whose groups do not fit the registers, 3.1 ms.
 
 #include "layer_util.hpp"
 
@@ -390,31 +397,39 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
       step[t] = s_step[buffer][t][lane];
       ds_of[t] = s_ds[buffer][t][lane];
     }
-    float h[SG][kTile + 1][NS], decay[SG][kTile][NS];
-#pragma unroll
-    for (int g = 0; g < SG; ++g) {
+    // The states of group g before and behind the tile's tokens, and their factors.
+    struct Walk {
+      float h[kTile + 1][NS], decay[kTile][NS];
+    } walk;
+    auto forward = [&](int g, auto tokens, Walk& w) {
       float a2[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        h[g][0][i] = n.h[g][i];
+        w.h[0][i] = n.h[g][i];
         a2[i] = rate2(a[g][i]);
+        if constexpr (SG > 1) asm volatile("" : "+v"(a2[i]));  // computed again, not kept
       }
-      unrolled<kTile>([&](auto token) {
+      unrolled<decltype(tokens)::value>([&](auto token) {
         constexpr int t = decltype(token)::value;
         const float2 s = step[t];
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          decay[g][t][i] = __builtin_amdgcn_exp2f(s.x * a2[i]);
-          h[g][t + 1][i] = fmaf(decay[g][t][i], h[g][t][i], row_times<t>(n.b[g][i], s.y));
+          w.decay[t][i] = __builtin_amdgcn_exp2f(s.x * a2[i]);
+          w.h[t + 1][i] = fmaf(w.decay[t][i], w.h[t][i], row_times<t>(n.b[g][i], s.y));
         }
       });
-    }
+    };
+    if constexpr (SG == 1) forward(0, std::integral_constant<int, kTile>{}, walk);
     // Back over eight tokens; their products for dB and dC take the registers that
     // their states and decays leave.
     auto back = [&](auto half) {
       constexpr int kSide = decltype(half)::value;
 #pragma unroll
       for (int g = 0; g < SG; ++g) {
+        if constexpr (SG > 1) {  // the registers hold one group's states at a time
+          __builtin_amdgcn_sched_barrier(0);
+          forward(g, std::integral_constant<int, kSide ? kTile : kTile / 2>{}, walk);
+        }
         float vb[kV], vc[kV];
         unrolled<8>([&](auto token) {
           constexpr int k = 7 - decltype(token)::value, t = 8 * kSide + k;
@@ -425,17 +440,17 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
           float rate = 0.0f;
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            vc[k * NS + i] = ds * h[g][t + 1][i];
+            vc[k * NS + i] = ds * walk.h[t + 1][i];
             vb[k * NS + i] = G[g][i] * s.y;
-            G[g][i] *= decay[g][t][i];
-            const float q = G[g][i] * h[g][t][i];
+            G[g][i] *= walk.decay[t][i];
+            const float q = G[g][i] * walk.h[t][i];
             rate = fmaf(q, a[g][i], rate);
             dA[g][i] = fmaf(q, s.x, dA[g][i]);
           }
           s_write[kSide][wave][k][lane] = g == 0 ? through : s_write[kSide][wave][k][lane] + through;
           s_decay[kSide][wave][k][lane] = g == 0 ? rate : s_decay[kSide][wave][k][lane] + rate;
           if (kGated) {
-            const float sum = row_dot<t>(n.c[g], h[g][t + 1]);
+            const float sum = row_dot<t>(n.c[g], walk.h[t + 1]);
             s_y[kSide][wave][k][lane] = g == 0 ? sum : s_y[kSide][wave][k][lane] + sum;
           }
         });
@@ -578,7 +593,7 @@ void launch_ends(const SelectiveRequest& P) {
   else if (P.N <= 32)
     launch_ends<T, 8, 4>(P);
   else
-    launch_ends<T, 16, 4>(P);
+    launch_ends<T, 8, 8>(P);
 }
 
 sr_status launched(const char* what) {
