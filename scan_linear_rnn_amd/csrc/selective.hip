@@ -26,8 +26,8 @@
 // a SIMD issues: about 430 instructions per wave and tile, 64 of them exponentials at two
 // slots, where the recurrence with the sum over states alone takes 400 slots of 4 cycles (a
 // probe of it 190 us).  Eight waves of two states take as long: what they hide, their LDS
-// reads cost.  1 x 65536 x 1024 in 96 chunks: 460 us (first
-// pass 207, carry 17, outputs 296 where each is traced).
+// reads cost.  1 x 65536 x 1024 in 96 chunks: 460 us
+// (under a tracer first pass 207, carry 17, outputs 296).
 
 #include "layer_util.hpp"
 
@@ -44,7 +44,8 @@ enum Pass {
 //
 // While the waves go through tile k, each thread also prepares its part of tile
 // k + 1's steps, sums its part of tile k - 1's outputs and has tile k + 2's inputs on
-// their way: everything between two barriers is independent, one barrier per tile.
+// their way: everything between two barriers is independent, one barrier per tile.  Tiles with
+// four whole ones behind them go without a branch, as one block that the compiler can order.
 template <typename T, int W, int NS, int kPass, bool kWhole, bool kGated>
 __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void scan_kernel(const SelectiveRequest P) {
   constexpr bool kStates = kPass != kOutputs;
@@ -513,7 +514,7 @@ SelectivePlan chunked(int64_t T, int64_t tiles_per_group, int64_t want) {
 // Chunks over time: none where sequences and channels fill the GPU by themselves (the
 // first pass computes three quarters of what the second does), else about 1536 workgroups
 // in all.  Measured, 4096 tokens in bf16, workgroups without chunks: us without chunks /
-// with them: 8: 384 / 38, 64: 379 / 134, 128: 380 / 250, 192: 385 / 356, 256: 391 / 455.
+// with them: 8: 353 / 37, 64: 354 / 131, 128: 349 / 242, 192: 351 / 344, 256: 356 / 455.
 SelectivePlan selective_plan(int64_t B, int64_t T, int64_t D, int64_t G) {
   const int64_t tiles = (D / G + kLanes - 1) / kLanes, blocks = B * G * tiles;
   return chunked(T, tiles, blocks > 0 && blocks < 224 ? (1536 + blocks - 1) / blocks : 1);
@@ -521,8 +522,8 @@ SelectivePlan selective_plan(int64_t B, int64_t T, int64_t D, int64_t G) {
 
 // The backward pass has one workgroup per CU at a time, and its chunks cost a fifth more
 // (the pass that carries gradients backwards): the number of them that leaves the
-// fewest rounds over the 256 CUs for a chunk's work.  Measured as above: 8: 1415 / 96,
-// 64: 1441 / 444; of 2048 tokens 128: 741 / 446, 192: 749 / 641, 256: 752 / 835.
+// fewest rounds over the 256 CUs for a chunk's work.  Measured as above, of 2048 tokens: 8: 703 /
+// 81, 64: 717 / 238, 128: 724 / 455, 192: 729 / 652, 256: 736 / 828.
 SelectivePlan selective_backward_plan(int64_t B, int64_t T, int64_t D, int64_t G) {
   const int64_t tiles = (D / G + kLanes - 1) / kLanes, blocks = B * G * tiles;
   int64_t best = 1;
