@@ -432,6 +432,29 @@ def test_captured_calls_replay():
         del junk
 
 
+def test_two_streams_at_once():
+    """Calls in flight together do not share what they work in."""
+    say("selective scan, two streams")
+    cases = [case(1, 700, 192, 16, dtype="bf16", seed=k) for k in range(2)]
+
+    def work(c):
+        return sr.selective_scan_backward(*args(c), c["dy"], dh_last=c["dh"], **given(c)) + (
+            sr.selective_scan_forward(*args(c), **given(c)),)
+
+    want = [[t.clone() for t in work(c)] for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    out = [[], []]
+    for _ in range(4):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                out[k].append(work(cases[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for got in out[k]:
+            assert all(torch.equal(a, b) for a, b in zip(got, want[k])), k
+
+
 def test_given_state_counts_a_version():
     c = case(2, 1, 8, 16, dtype="fp32")
     tok = [t[:, 0] if t.dim() > 2 else t for t in args(c)]
