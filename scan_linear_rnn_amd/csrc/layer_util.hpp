@@ -158,6 +158,13 @@ __device__ __forceinline__ float weight_at(const void* w, sr_dtype dtype, int64_
 __device__ __forceinline__ float bounded(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }
 __device__ __forceinline__ float rate2(float a) { return bounded(a * kLog2e); }
 
+// 2^x h + e for the decay of many tokens, whose factor may leave the fp32 range where
+// its product does not (a small state that grows): in two halves.
+__device__ __forceinline__ float decayed(float x, float h, float e) {
+  const float half = __builtin_amdgcn_exp2f(0.5f * x);
+  return fmaf(half, half * h, e);
+}
+
 // log(1 + e^x) to a few ulps for any x: max(x, 0) + log1p(e), e = e^-|x|.  With u the
 // rounded 1 + e, log1p(e) = log(u) + (e - (u - 1)) / u; u's rounding error e - (u - 1) is
 // exact, and what its division by u changes is far below the sum's last place.

@@ -339,7 +339,7 @@ __global__ __launch_bounds__(256) void carry_kernel(const SelectiveRequest P, co
       const int64_t k = reverse ? P.chunks - 1 - (c0 + j) : c0 + j;
       P.ends[k * bnd + i] = h;
       // a zero state stays zero however its factor overflows
-      h = h == 0.0f ? e[j] : fmaf(__builtin_amdgcn_exp2f(a2 * s[j]), h, e[j]);
+      h = h == 0.0f ? e[j] : decayed(a2 * s[j], h, e[j]);
     }
   }
   if (last) last[own] = h;
