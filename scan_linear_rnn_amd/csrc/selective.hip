@@ -201,7 +201,10 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
       if (live) store_some(at_byte(y, bytes(at, P.D, c)), nc, sum);
     }
   };
-  float total = 0.0f;  // of the steps (the first wave's)
+  // The sum of the steps (the first wave's), of whole tiles with what rounding lost of them:
+  // the steps one after another would drift with the number of tokens (8192 equal ones by
+  // 1258 x 2^-24), and the decay of many tokens is an exponential of this sum.
+  float total = 0.0f, lost = 0.0f;
   Inputs in[2];        // of the next tile and the one after it
   Raw<T, Q> u0{}, z0{}, u1{}, z1{};  // of the present tile and the one before it
   // One tile, at t0: the waves go through it, in[s] is the next one's input.  kInner: the four
@@ -228,9 +231,10 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
       const float v[1] = {total};
       store_at(mark + P.N * P.D, mine && wave == 0 ? uint32_t(lane) * 4 : kNowhere, v);
     }
+    float steps = 0.0f;  // of this tile
     auto token = [&](auto which) {
       constexpr int t = decltype(which)::value;
-      if constexpr (kStates) total += step[t].x;
+      if constexpr (kStates) steps += step[t].x;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
         h[i] = fmaf(__builtin_amdgcn_exp2f(step[t].x * a2[i]), h[i],
@@ -253,7 +257,11 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
 #pragma unroll
       for (int i = 0; i < NS; ++i) asm volatile("" : "+v"(h[i]));
     });
-    if constexpr (!kStates) {
+    if constexpr (kStates) {
+      const float more = steps - lost, sum = total + more;
+      lost = fabsf(sum) <= FLT_MAX ? (sum - total) - more : 0.0f;  // (nothing of an infinite sum)
+      total = sum;
+    } else {
       finish(t0 - kTile, part, u1, z1);
       u1 = u0, z1 = z0;
       u0 = un, z0 = zn;
