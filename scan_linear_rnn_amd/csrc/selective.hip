@@ -63,17 +63,25 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
   const int64_t d = p.c0 + lane;
   const int n0 = wave * NS;
   const bool mine = lane < p.width;
+  // Where N is less than the waves hold, the places behind the last state repeat states and take a
+  // part of their C: kWhole, whole waves those of the last wave that has any (an eighth
+  // each), else each the last state (a 64th), and what is repeated keeps the rest.  (With zeros for
+  // B and C an infinite input would make them NaN, and y with them.)
+  const int from = kWhole ? (n0 < P.N ? n0 : P.N - NS) : (n0 < P.N ? n0 : P.N - 1);  // the wave's first state
+  const float part_of = kWhole ? 0.125f : 0.015625f;
+  const float rest_of = 1.0f - part_of * float(kWhole ? W - P.N / NS : W * NS - P.N);
+  const bool shares = P.N < W * NS && n0 + NS >= P.N;
   float a2[NS], h[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    const bool is = mine && n0 + i < P.N;
-    a2[i] = is ? rate2(P.A[d * P.N + n0 + i]) : 0.0f;
+    const int n = kWhole || from + i < P.N ? from + i : P.N - 1;
+    a2[i] = mine ? rate2(P.A[d * P.N + n]) : 0.0f;
     h[i] = 0.0f;
     if constexpr (!kStates) {
       if (P.ends != nullptr) {  // [chunk][b][n][D]
-        if (is) h[i] = P.ends[((int64_t(p.chunk) * P.B + p.b) * P.N + n0 + i) * P.D + d];
-      } else if (P.h0 != nullptr && is) {
-        h[i] = P.h0[(p.b * P.D + d) * P.N + n0 + i];
+        if (mine) h[i] = P.ends[((int64_t(p.chunk) * P.B + p.b) * P.N + n) * P.D + d];
+      } else if (P.h0 != nullptr && mine) {
+        h[i] = P.h0[(p.b * P.D + d) * P.N + n];
       }
     }
   }
@@ -87,8 +95,8 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
   // B and C go from memory to where the recurrence takes them from: lane t of each
   // row of 16 has the wave's states of a tile's token t.
   const int bc_at = lane % 16;
-  const int64_t group0 = int64_t(p.group) * P.N + (n0 < P.N ? n0 : 0);
-  const int nn = n0 < P.N ? P.N - n0 : 1;
+  const int64_t group0 = int64_t(p.group) * P.N + from;
+  const int nn = P.N - from;
   struct Inputs {
     Raw<T, Q> u, delta, z;
     Raw<T, NS> Bm, Cm;
@@ -166,10 +174,14 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
       b0[i] = bm[i];
       c0[i] = cm[i];
     }
-    if (!kWhole || n0 >= P.N) {
+    if (!kStates && shares) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (n0 + i >= P.N) b0[i] = c0[i] = 0.0f;
+      for (int i = 0; i < NS; ++i) {
+        if (n0 + i >= P.N)
+          c0[i] *= part_of;
+        else if (kWhole || n0 + i == P.N - 1)
+          c0[i] *= rest_of;
+      }
     }
   };
   // The waves' shares of y for a thread's token.
