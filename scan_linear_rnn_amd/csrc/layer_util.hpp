@@ -158,10 +158,10 @@ __device__ __forceinline__ float weight_at(const void* w, sr_dtype dtype, int64_
 __device__ __forceinline__ float bounded(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }
 __device__ __forceinline__ float rate2(float a) { return bounded(a * kLog2e); }
 
-// 2^x h + e for the decay of many tokens, whose factor may leave the fp32 range where
-// its product does not (a small state that grows): in two halves.
-__device__ __forceinline__ float decayed(float x, float h, float e) {
-  const float half = __builtin_amdgcn_exp2f(0.5f * x);
+// e^(a s) h + e for the decay of many tokens by their summed steps s: its factor may leave the
+// fp32 range where the product does not (a small state that grows), so it comes in two halves.
+__device__ __forceinline__ float decayed(float a, float s, float h, float e) {
+  const float half = __builtin_amdgcn_exp2f(s * bounded(a * (0.5f * kLog2e)));
   return fmaf(half, half * h, e);
 }
 

@@ -321,7 +321,7 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
         n.c[g][i] = is ? to_f32(in.Cm[g][i]) : 0.0f;
         n.h[g][i] = mine && n0 + i < P.N ? in.mark[g][i] : 0.0f;
         // a zero state stays zero however its factor overflows
-        const float full = decayed(in.so_far * rate2(a[g][i]), start[g][i], n.h[g][i]);
+        const float full = decayed(a[g][i], in.so_far, start[g][i], n.h[g][i]);
         n.h[g][i] = start[g][i] != 0.0f ? full : n.h[g][i];
       }
     }
