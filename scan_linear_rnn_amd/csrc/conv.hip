@@ -217,10 +217,11 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(const ConvRequest P)
       const float s = logistic_f(c), slope = s * fmaf(c, 1.0f - s, 1.0f);
       g *= P.silu ? slope : 1.0f;
       dc[0][e] = live ? g : 0.0f;
-      const float mine = own ? dc[0][e] : 0.0f;
-      dbias[e] += mine;
+      // (not a product with zero for the other tokens: an input in their window may be infinite)
+      const bool counts = live && own;
+      dbias[e] += counts ? dc[0][e] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < K; ++j) dw[j][e] = fmaf(mine, win[j][e], dw[j][e]);
+      for (int j = 0; j < K; ++j) dw[j][e] = counts ? fmaf(dc[0][e], win[j][e], dw[j][e]) : dw[j][e];
       out[e] = 0.0f;
 #pragma unroll
       for (int j = 0; j < K; ++j) out[e] = fmaf(w[j][e], dc[j][e], out[e]);
