@@ -481,8 +481,8 @@ sr_status adamw_step_each(int64_t n_tensors, const sr_adamw_tensor* tensors, voi
  *   h0, h_last    [B,D,N] fp32 state in front of and behind the tokens; NULL: zeros,
  *                 and not wanted.
  *   y             [B,T,D] in x_dtype.
- * States, steps and gates are fp32; y is rounded once.  N at most 64, rows at most
- * 2^25 elements apart (else SR_ERR_UNSUPPORTED).  Few channels and long sequences are cut into chunks of
+ * States, steps and gates are fp32; y is rounded once.  N at most 64, rows of several
+ * tokens at most 2^25 elements apart (else SR_ERR_UNSUPPORTED).  Few channels and long sequences are cut into chunks of
  * tokens whose decay is the exponential of their summed steps; a state that left the
  * fp32 range stays non-finite, but may become NaN where one token after the other would
  * give an infinity.

@@ -102,10 +102,10 @@ sr_status check_selective(const SelectiveRequest& P, int64_t tokens, int64_t N, 
   SR_REQUIRE(P.softplus == 0 || P.softplus == 1, "delta_softplus must be 0 or 1 (got %d)", P.softplus);
   return SR_OK;
 }
-// A tile's rows are addressed in 32 bits.
-sr_status check_rows(std::initializer_list<int64_t> apart) {
+// A tile's rows are addressed in 32 bits from its first one; a sequence of one token has no other.
+sr_status check_rows(int64_t tokens, std::initializer_list<int64_t> apart) {
   for (int64_t ld : apart)
-    if (ld > kSelectiveRow)
+    if (tokens > 1 && ld > kSelectiveRow)
       return fail(SR_ERR_UNSUPPORTED, "rows are at most %lld elements apart (%lld)", (long long)kSelectiveRow, (long long)ld);
   return SR_OK;
 }
@@ -239,7 +239,7 @@ sr_status selective_scan_forward(int64_t B, int64_t T, int64_t D, int64_t N, int
   P.h0 = h0, P.lengths = lengths, P.y = y, P.h_last = h_last;
   P.stream = as_stream(stream);
   sr_status st = check_selective(P, T, N, G);
-  if (st == SR_OK) st = check_rows({D, ld_u, ld_delta, z ? ld_z : 0, ld_b, ld_c});
+  if (st == SR_OK) st = check_rows(T, {D, ld_u, ld_delta, z ? ld_z : 0, ld_b, ld_c});
   if (st != SR_OK) return st;
   const SelectiveLayout L = selective_layout(B, T, D, N, G, false);
   st = check_grid(B * G * L.plan.tiles_per_group * L.plan.chunks, 1024);
@@ -291,7 +291,7 @@ sr_status selective_scan_backward(int64_t B, int64_t T, int64_t D, int64_t N, in
   const int64_t n = B * T * D;
   SR_REQUIRE(ld_dy >= D && sizes_ok({B * T, ld_dy}), "ld_dy (%lld) must be >= D (%lld) and fit int64", (long long)ld_dy,
              (long long)D);
-  st = check_rows({D, ld_u, ld_delta, z ? ld_z : 0, ld_b, ld_c, ld_dy});
+  st = check_rows(T, {D, ld_u, ld_delta, z ? ld_z : 0, ld_b, ld_c, ld_dy});
   if (st != SR_OK) return st;
   SR_REQUIRE(n == 0 || (dy && du && ddelta && dB && dC), "dy, du, ddelta, dB and dC are required");
   SR_REQUIRE(D == 0 || dA, "dA is required");

@@ -223,7 +223,7 @@ sr_status launch_adamw(const AdamWRequest& rq);
 
 constexpr int kSelectiveTile = 16;        // tokens a workgroup handles between barriers
 constexpr int kSelectiveStates = 64;      // most states per channel
-constexpr int64_t kSelectiveRow = int64_t(1) << 25;  // furthest that rows may be apart
+constexpr int64_t kSelectiveRow = int64_t(1) << 25;  // furthest that rows of several tokens may be apart
 constexpr int64_t kSelectiveMinTokens = 128;  // tokens of the shortest sequence that is cut
 
 // How a call is cut: 64 channels of a group per workgroup, the tokens in chunks.

@@ -334,6 +334,13 @@ __device__ __forceinline__ void column_sums(const float* parts, int64_t rows, in
   }
 }
 
+// The offset in bytes of element i of a tile's row t.  (Rows that may be further apart than 32 bits hold
+// are rows of one token, t = 0.)
+template <typename T>
+__device__ __forceinline__ uint32_t row_bytes(int t, int64_t ld, int i) {
+  return (uint32_t(t) * uint32_t(ld) + uint32_t(i)) * uint32_t(sizeof(T));
+}
+
 constexpr int kTile = kSelectiveTile;  // tokens per tile
 constexpr int kLanes = 64;             // channels per workgroup
 

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
     Raw<T, Q> u, delta, z;
     Raw<T, NS> Bm, Cm;
   };
-  const auto bytes = [](int t, int64_t ld, int i) { return uint32_t(t * int(ld) + i) * uint32_t(sizeof(T)); };
+  const auto bytes = [](int t, int64_t ld, int i) { return row_bytes<T>(t, ld, i); };
   const uint32_t o_u = bytes(at, P.ld_u, c), o_d = bytes(at, P.ld_delta, c), o_z = bytes(at, P.ld_z, c),
                  o_b = bytes(bc_at, P.ld_b, 0), o_c = bytes(bc_at, P.ld_c, 0);
   const int64_t row0 = p.b * P.T + first;

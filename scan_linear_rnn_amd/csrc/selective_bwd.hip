@@ -83,12 +83,6 @@ __device__ __forceinline__ float sum_lanes(float (&v)[n], int lane) {
   return v[0];
 }
 
-// The offsets of a thread's elements in a tile's rows, in bytes.
-template <typename T>
-__device__ __forceinline__ uint32_t bytes_of(int t, int64_t ld, int i) {
-  return uint32_t(t * int(ld) + i) * uint32_t(sizeof(T));
-}
-
 // The gradient that each chunk's own outputs send in front of it (P.gends):
 // g <- (g + ds C) a from its last token to its first.  Tiles as in scan_kernel, last one first.
 template <typename T, int W, int NS, bool kWhole>
@@ -125,10 +119,10 @@ __global__ __launch_bounds__(W * 64) void grad_ends_kernel(const SelectiveReques
     t0 = t0 < first ? first : t0;
     const int64_t row0 = p.b * P.T + t0;
     const int last = int(P.T - 1 - t0), t = at < last ? at : last, tb = bc_at < last ? bc_at : last;
-    load_raw<kWhole>(at_byte(static_cast<const T*>(P.delta) + row0 * P.ld_delta + p.c0, bytes_of<T>(t, P.ld_delta, c)), nc, in.delta);
-    load_raw<kWhole>(at_byte(static_cast<const T*>(P.dy) + row0 * P.ld_dy + p.c0, bytes_of<T>(t, P.ld_dy, c)), nc, in.dy);
-    if (P.z) load_raw<kWhole>(at_byte(static_cast<const T*>(P.z) + row0 * P.ld_z + p.c0, bytes_of<T>(t, P.ld_z, c)), nc, in.z);
-    load_raw<kWhole>(at_byte(static_cast<const T*>(P.Cm) + row0 * P.ld_c + group0, bytes_of<T>(tb, P.ld_c, 0)), nn, in.Cm);
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.delta) + row0 * P.ld_delta + p.c0, row_bytes<T>(t, P.ld_delta, c)), nc, in.delta);
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.dy) + row0 * P.ld_dy + p.c0, row_bytes<T>(t, P.ld_dy, c)), nc, in.dy);
+    if (P.z) load_raw<kWhole>(at_byte(static_cast<const T*>(P.z) + row0 * P.ld_z + p.c0, row_bytes<T>(t, P.ld_z, c)), nc, in.z);
+    load_raw<kWhole>(at_byte(static_cast<const T*>(P.Cm) + row0 * P.ld_c + group0, row_bytes<T>(tb, P.ld_c, 0)), nn, in.Cm);
   };
   auto prepare = [&](int64_t t0, int buffer, const Inputs& in, float (&cm)[NS]) {
     float dt[Q], ds[Q], z[Q];
@@ -278,8 +272,8 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int n = n0 + i < P.N ? n0 + i : P.N - 1;  // (uniform)
-        in.Bm[g][i] = *at_byte(Bm + n, bytes_of<T>(tb, P.ld_b, 0));
-        in.Cm[g][i] = *at_byte(Cm + n, bytes_of<T>(tb, P.ld_c, 0));
+        in.Bm[g][i] = *at_byte(Bm + n, row_bytes<T>(tb, P.ld_b, 0));
+        in.Cm[g][i] = *at_byte(Cm + n, row_bytes<T>(tb, P.ld_c, 0));
       }
 #pragma unroll
       for (int i = 0; i < NS; ++i) in.mark[g][i] = (P.marks + (m + (n0 + i < P.N ? n0 + i : P.N)) * P.D + p.c0)[c];
