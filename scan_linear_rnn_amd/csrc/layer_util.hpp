@@ -158,12 +158,13 @@ __device__ __forceinline__ float weight_at(const void* w, sr_dtype dtype, int64_
 __device__ __forceinline__ float bounded(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }
 __device__ __forceinline__ float rate2(float a) { return bounded(a * kLog2e); }
 
-// e^(a s) h + e for the decay of many tokens by their summed steps s: its factor may leave the
-// fp32 range where the product does not (a small state that grows), so it comes in two halves.
-__device__ __forceinline__ float decayed(float a, float s, float h, float e) {
-  const float half = __builtin_amdgcn_exp2f(s * bounded(a * (0.5f * kLog2e)));
+// 4^x h + e, the decay of many tokens: its factor may leave the fp32 range where the
+// product does not (a small state that grows), so it comes in two halves of x each.
+__device__ __forceinline__ float decayed(float x, float h, float e) {
+  const float half = __builtin_amdgcn_exp2f(x);
   return fmaf(half, half * h, e);
 }
+__device__ __forceinline__ float half_rate2(float a) { return bounded(a * (0.5f * kLog2e)); }
 
 // log(1 + e^x) to a few ulps for any x: max(x, 0) + log1p(e), e = e^-|x|.  With u the
 // rounded 1 + e, log1p(e) = log(u) + (e - (u - 1)) / u; u's rounding error e - (u - 1) is

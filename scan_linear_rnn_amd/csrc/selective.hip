@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256) void carry_kernel(const SelectiveRequest P, co
   const int64_t bnd = P.B * P.N * P.D;
   if (i >= bnd) return;
   const int64_t d = i % P.D, bn = i / P.D, n = bn % P.N, b = bn / P.N;
-  const float a = P.A[d * P.N + n];
+  const float a2 = half_rate2(P.A[d * P.N + n]);
   const int64_t own = (b * P.D + d) * P.N + n;
   float h = init ? init[own] : 0.0f;
   constexpr int kAhead = 4;
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(256) void carry_kernel(const SelectiveRequest P, co
       const int64_t k = reverse ? P.chunks - 1 - (c0 + j) : c0 + j;
       P.ends[k * bnd + i] = h;
       // a zero state stays zero however its factor overflows
-      h = h == 0.0f ? e[j] : decayed(a, s[j], h, e[j]);
+      h = h == 0.0f ? e[j] : decayed(a2 * s[j], h, e[j]);
     }
   }
   if (last) last[own] = h;

@@ -315,7 +315,9 @@ __global__ __launch_bounds__(W * 64, 2) void backward_kernel(const SelectiveRequ
         n.c[g][i] = is ? to_f32(in.Cm[g][i]) : 0.0f;
         n.h[g][i] = mine && n0 + i < P.N ? in.mark[g][i] : 0.0f;
         // a zero state stays zero however its factor overflows
-        const float full = decayed(a[g][i], in.so_far, start[g][i], n.h[g][i]);
+        // of several groups the walk's own rates: others in registers beside them spill (64 states 3.26 ms, so 3.11)
+        const float half = SG > 1 ? 0.5f * (in.so_far * rate2(a[g][i])) : in.so_far * half_rate2(a[g][i]);
+        const float full = decayed(half, start[g][i], n.h[g][i]);
         n.h[g][i] = start[g][i] != 0.0f ? full : n.h[g][i];
       }
     }
