@@ -465,7 +465,8 @@ sr_status adamw_step_each(int64_t n_tensors, const sr_adamw_tensor* tensors, voi
  *   outputs     contiguous.  They must not overlap inputs or each other
  *               (SR_ERR_INVALID_ARGUMENT).
  * Repeated calls give identical bits.  No call allocates, waits for the GPU or
- * keeps anything; all can be captured into a graph.
+ * keeps anything; all can be captured into a graph.  Sizes whose launches would
+ * take 2^32 work-items or more are SR_ERR_UNSUPPORTED.
  *
  * selective_scan_forward:
  *

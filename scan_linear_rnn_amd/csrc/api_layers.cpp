@@ -346,7 +346,7 @@ sr_status selective_step(int64_t B, int64_t D, int64_t N, int64_t G, const void*
   SR_REQUIRE(!overlaps_inputs(P, {y, size * B * D}, 1) && !overlaps_inputs(P, {h_next, states}, 1) &&
                  !overlaps_any({y, size * B * D}, {{h_prev, states}, {h_next, states}}),
              "outputs must not overlap inputs or each other");
-  st = check_grid((B * D * 64 + 255) / 256, 256);
+  st = check_grid(selective_step_blocks(B, D, N), 256);
   if (st != SR_OK) return st;
   if (B == 0 || D == 0) return SR_OK;
   return launch_selective_step(P);

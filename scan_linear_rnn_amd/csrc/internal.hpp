@@ -272,6 +272,7 @@ sr_status launch_selective_scan(const SelectiveRequest& rq);
 sr_status launch_selective_states(const SelectiveRequest& rq);
 sr_status launch_selective_carry(const SelectiveRequest& rq, const float* init, float* last, bool reverse);
 sr_status launch_selective_backward(const SelectiveRequest& rq);
+int64_t selective_step_blocks(int64_t B, int64_t D, int64_t N);  // workgroups of 256
 sr_status launch_selective_step(const SelectiveRequest& rq);
 // States of one row of `parts`: N rounded up to what the workgroup's waves hold.
 inline int64_t selective_padded(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }

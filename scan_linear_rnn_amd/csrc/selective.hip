@@ -469,37 +469,41 @@ void launch_scan(const SelectiveRequest& P, int pass, uint32_t blocks) {
     launch_scan<T, 8, 8>(P, pass, blocks);
 }
 
-template <typename T, int V, int L>
-void launch_step(const SelectiveRequest& P) {
-  auto run = [&](auto* kernel, int R) {
-    const int64_t blocks = ((P.B + R - 1) / R * P.D + 256 / L - 1) / (256 / L);
-    hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(256), 0, P.stream, P);
-  };
+// Of a step: states per lane, lanes per channel, streams per thread.
+struct StepShape {
+  int states, lanes, streams;
+};
+StepShape step_shape(int64_t B, int64_t D, int64_t N) {
+  StepShape s{N % 4 == 0 ? 4 : 1, 1, 1};
+  while (s.lanes * s.states < N) s.lanes *= 2;
   // Four streams per thread where that leaves two waves per SIMD.  Measured in us, D = 2048,
   // 16 states, one stream / four: 32 streams 4.1 / 4.7, 64 6.0 / 5.9, 128 9.6 / 8.4, 1024 51.6 / 46.2.
-  if (P.B / 4 * P.D * L >= 2 * 4 * 256 * 64)
-    run(step_kernel<T, V, L, 4>, 4);
+  if (B / 4 * D * s.lanes >= 2 * 4 * 256 * 64) s.streams = 4;
+  return s;
+}
+
+template <typename T, int V, int L>
+void launch_step(const SelectiveRequest& P, int streams) {
+  const dim3 blocks(uint32_t(selective_step_blocks(P.B, P.D, P.N)));
+  if (streams == 4)
+    hipLaunchKernelGGL((step_kernel<T, V, L, 4>), blocks, dim3(256), 0, P.stream, P);
   else
-    run(step_kernel<T, V, L, 1>, 1);
+    hipLaunchKernelGGL((step_kernel<T, V, L, 1>), blocks, dim3(256), 0, P.stream, P);
 }
 template <typename T, int V>
-void launch_step(const SelectiveRequest& P) {
-  const int64_t lanes = (P.N + V - 1) / V;
-  if (lanes <= 1)
-    launch_step<T, V, 1>(P);
-  else if (lanes <= 2)
-    launch_step<T, V, 2>(P);
-  else if (lanes <= 4)
-    launch_step<T, V, 4>(P);
-  else if (lanes <= 8)
-    launch_step<T, V, 8>(P);
-  else if (lanes <= 16)
-    launch_step<T, V, 16>(P);
-  else if constexpr (V == 1) {
-    if (lanes <= 32)
-      launch_step<T, V, 32>(P);
+void launch_step(const SelectiveRequest& P, StepShape shape) {
+  switch (shape.lanes) {
+    case 1: return launch_step<T, V, 1>(P, shape.streams);
+    case 2: return launch_step<T, V, 2>(P, shape.streams);
+    case 4: return launch_step<T, V, 4>(P, shape.streams);
+    case 8: return launch_step<T, V, 8>(P, shape.streams);
+    case 16: return launch_step<T, V, 16>(P, shape.streams);
+  }
+  if constexpr (V == 1) {
+    if (shape.lanes == 32)
+      launch_step<T, V, 32>(P, shape.streams);
     else
-      launch_step<T, V, 64>(P);
+      launch_step<T, V, 64>(P, shape.streams);
   }
 }
 
@@ -592,18 +596,25 @@ sr_status launch_selective_scan(const SelectiveRequest& rq) {
   return launched("selective scan");
 }
 
+int64_t selective_step_blocks(int64_t B, int64_t D, int64_t N) {
+  const StepShape s = step_shape(B, D, N);
+  const int64_t per = 256 / s.lanes;
+  return ((B + s.streams - 1) / s.streams * D + per - 1) / per;
+}
+
 sr_status launch_selective_step(const SelectiveRequest& P) {
   const bool bf16 = P.dtype == SR_BF16;
-  if (P.N % 4 == 0) {
+  const StepShape shape = step_shape(P.B, P.D, P.N);
+  if (shape.states == 4) {
     if (bf16)
-      launch_step<uint16_t, 4>(P);
+      launch_step<uint16_t, 4>(P, shape);
     else
-      launch_step<float, 4>(P);
+      launch_step<float, 4>(P, shape);
   } else {
     if (bf16)
-      launch_step<uint16_t, 1>(P);
+      launch_step<uint16_t, 1>(P, shape);
     else
-      launch_step<float, 1>(P);
+      launch_step<float, 1>(P, shape);
   }
   return launched("selective step");
 }
