@@ -110,6 +110,12 @@ sr_status check_rows(int64_t tokens, std::initializer_list<int64_t> apart) {
   return SR_OK;
 }
 
+// The scan's workgroups, and a thread per state where there are chunks to carry it over.
+sr_status check_selective_grids(const SelectiveRequest& P, int64_t G, const SelectivePlan& plan, int threads) {
+  const sr_status st = check_grid(P.B * G * plan.tiles_per_group * plan.chunks, threads);
+  return st != SR_OK || plan.chunks == 1 ? st : check_grid((P.B * P.N * P.D + 255) / 256, 256);
+}
+
 Area input_area(const SelectiveRequest& P, const void* p, int64_t ld, int64_t tokens, int64_t width) {
   return rows(p, P.B * tokens, ld, width, P.dtype);
 }
@@ -242,8 +248,7 @@ sr_status selective_scan_forward(int64_t B, int64_t T, int64_t D, int64_t N, int
   if (st == SR_OK) st = check_rows(T, {D, ld_u, ld_delta, z ? ld_z : 0, ld_b, ld_c});
   if (st != SR_OK) return st;
   const SelectiveLayout L = selective_layout(B, T, D, N, G, false);
-  st = check_grid(B * G * L.plan.tiles_per_group * L.plan.chunks, 1024);
-  if (st == SR_OK) st = check_grid((B * N * D + 255) / 256, 256);
+  st = check_selective_grids(P, G, L.plan, selective_threads(N, false));
   if (st != SR_OK) return st;
   const int64_t size = int64_t(elem_size(x_dtype)), states = 4 * B * D * N;
   SR_REQUIRE(y || B * T * D == 0, "y is NULL");
@@ -312,8 +317,7 @@ sr_status selective_scan_backward(int64_t B, int64_t T, int64_t D, int64_t N, in
   const SelectiveLayout L = selective_layout(B, T, D, N, G, true);
   st = check_workspace(workspace, workspace_bytes, L.total);
   if (st != SR_OK) return st;
-  st = check_grid(B * G * L.plan.tiles_per_group * L.plan.chunks, 1024);
-  if (st == SR_OK) st = check_grid((B * N * D + 255) / 256, 256);
+  st = check_selective_grids(P, G, L.plan, selective_threads(N, true));
   if (st == SR_OK) st = check_grid((B * T * G * 2 * selective_padded(N) + 255) / 256, 256);
   if (st == SR_OK) st = check_grid(((N + 2) * D + 63) / 64, 1024);
   if (st != SR_OK) return st;

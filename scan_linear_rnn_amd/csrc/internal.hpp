@@ -274,6 +274,8 @@ sr_status launch_selective_carry(const SelectiveRequest& rq, const float* init, 
 sr_status launch_selective_backward(const SelectiveRequest& rq);
 int64_t selective_step_blocks(int64_t B, int64_t D, int64_t N);  // workgroups of 256
 sr_status launch_selective_step(const SelectiveRequest& rq);
+// Threads of its largest workgroup: four waves or eight.
+inline int selective_threads(int64_t N, bool backward) { return N <= (backward ? 8 : 16) ? 256 : 512; }
 // States of one row of `parts`: N rounded up to what the workgroup's waves hold.
 inline int64_t selective_padded(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 
