@@ -160,9 +160,6 @@ sr_status check_conv(const ConvRequest& P, int64_t tokens, int64_t K) {
   return SR_OK;
 }
 int64_t conv_state_bytes(const ConvRequest& P) { return P.B * (P.K - 1) * P.D * int64_t(elem_size(P.dtype)); }
-int64_t conv_blocks(const ConvRequest& P) {
-  return (P.D * (P.B * P.runs + P.B * (P.K - 1)) + 255) / 256;
-}
 
 // ----------------------------------------------------------------------- norm
 
@@ -371,7 +368,7 @@ sr_status causal_conv_forward(int64_t B, int64_t T, int64_t D, int64_t K, const 
   const ConvPlan plan = conv_plan(B, T, D, x_dtype, false);
   P.run_len = plan.run_len;
   P.runs = plan.runs;
-  st = check_grid(conv_blocks(P), 256);
+  st = check_grid((conv_threads(P) + 255) / 256, 256);
   if (st != SR_OK) return st;
   const int64_t size = int64_t(elem_size(x_dtype)), kept = conv_state_bytes(P), out = size * B * T * D;
   SR_REQUIRE(y || B * T * D == 0, "y is NULL");
@@ -407,7 +404,7 @@ sr_status causal_conv_backward(int64_t B, int64_t T, int64_t D, int64_t K, const
   const ConvPlan plan = conv_plan(B, T, D, x_dtype, true);
   P.run_len = plan.run_len;
   P.runs = plan.runs;
-  st = check_grid(conv_blocks(P), 256);
+  st = check_grid((conv_backward_threads(P) + 255) / 256, 256);
   if (st == SR_OK) st = check_grid(((K + 1) * D + 63) / 64, 1024);
   if (st != SR_OK) return st;
   const size_t e = elem_size(x_dtype);
@@ -455,7 +452,7 @@ sr_status causal_conv_step(int64_t B, int64_t D, int64_t K, const void* x, int64
   SR_REQUIRE(!overlaps_any({y, size * B * D}, {in, {state, kept}, {state_next, kept}, wa, ba}) &&
                  !overlaps_any({state_next, kept}, {in, wa, ba}),
              "outputs must not overlap inputs or each other");
-  st = check_grid((B * D + 255) / 256, 256);
+  st = check_grid((conv_step_threads(P) + 255) / 256, 256);
   if (st != SR_OK) return st;
   if (B == 0 || D == 0) return SR_OK;
   return launch_conv_step(P);

@@ -377,9 +377,21 @@ ConvPlan conv_plan(int64_t B, int64_t T, int64_t D, sr_dtype dtype, bool backwar
   return plan;
 }
 
-sr_status launch_conv(const ConvRequest& P) {
+int64_t conv_threads(const ConvRequest& P) {
   const int64_t v = vector_of(P.dtype, false), nvec = P.D >= v ? (P.D + v - 1) / v : P.D;
-  const int64_t n = nvec * (P.B * P.runs + (P.last ? P.B * (P.K - 1) : 0));
+  return nvec * (P.B * P.runs + (P.last ? P.B * (P.K - 1) : 0));
+}
+int64_t conv_backward_threads(const ConvRequest& P) {
+  const int64_t v = vector_of(P.dtype, true), nvec = P.D >= v ? (P.D + v - 1) / v : P.D;
+  return nvec * P.B * P.runs;
+}
+int64_t conv_step_threads(const ConvRequest& P) {
+  const int64_t v = vector_of(P.dtype, false);
+  return P.B * (P.D % v == 0 ? P.D / v : P.D);
+}
+
+sr_status launch_conv(const ConvRequest& P) {
+  const int64_t v = vector_of(P.dtype, false), n = conv_threads(P);
   if (n == 0) return SR_OK;
   by_type(P.dtype, P.D >= v, [&](auto t, auto width) {
     by_taps(P.K, [&](auto taps) {
@@ -391,8 +403,7 @@ sr_status launch_conv(const ConvRequest& P) {
 }
 
 sr_status launch_conv_backward(const ConvRequest& P) {
-  const int64_t v = vector_of(P.dtype, true), nvec = P.D >= v ? (P.D + v - 1) / v : P.D;
-  const int64_t n = nvec * P.B * P.runs;
+  const int64_t v = vector_of(P.dtype, true), n = conv_backward_threads(P);
   by_type(P.dtype, P.D >= v, [&](auto t, auto width) {
     by_taps(P.K, [&](auto taps) {
       if (n > 0)
@@ -407,10 +418,8 @@ sr_status launch_conv_backward(const ConvRequest& P) {
 }
 
 sr_status launch_conv_step(const ConvRequest& P) {
-  const int64_t v = vector_of(P.dtype, false);
-  const bool whole = P.D % v == 0;
-  const int64_t n = P.B * (whole ? P.D / v : P.D);
-  by_type(P.dtype, whole, [&](auto t, auto width) {
+  const int64_t n = conv_step_threads(P);
+  by_type(P.dtype, P.D % vector_of(P.dtype, false) == 0, [&](auto t, auto width) {
     by_taps(P.K, [&](auto taps) {
       hipLaunchKernelGGL((conv_step_kernel<decltype(t), decltype(taps)::value, decltype(width)::value>),
                          dim3(uint32_t((n + 255) / 256)), dim3(256), 0, P.stream, P);

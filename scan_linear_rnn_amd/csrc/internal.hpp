@@ -310,6 +310,10 @@ struct ConvRequest {
   float* parts;       // [B][runs][K + 1][D]
 };
 
+// Threads of their launches, in workgroups of 256.
+int64_t conv_threads(const ConvRequest& rq);
+int64_t conv_backward_threads(const ConvRequest& rq);
+int64_t conv_step_threads(const ConvRequest& rq);
 sr_status launch_conv(const ConvRequest& rq);
 sr_status launch_conv_backward(const ConvRequest& rq);
 sr_status launch_conv_step(const ConvRequest& rq);
