@@ -7,7 +7,10 @@
 namespace sr {
 namespace {
 
-constexpr int64_t kMost = int64_t(1) << 40;  // of any size: products of two padded ones fit int64
+constexpr int64_t kMost = int64_t(1) << 40;  // of any size
+
+// A size with what is added to it, where that cannot overflow (else it stays too large).
+int64_t padded(int64_t size, int64_t more) { return size > kMost ? size : size + more; }
 
 bool sizes_ok(std::initializer_list<int64_t> sizes) {
   int64_t n = 16;  // bytes per element, with room to spare
@@ -147,7 +150,7 @@ sr_status check_conv(const ConvRequest& P, int64_t tokens, int64_t K) {
   SR_REQUIRE(P.B >= 0 && tokens >= 0 && P.D >= 0 && K >= 1, "bad sizes (B=%lld T=%lld D=%lld K=%lld)", (long long)P.B,
              (long long)tokens, (long long)P.D, (long long)K);
   if (K > kConvTaps) return fail(SR_ERR_UNSUPPORTED, "at most %d taps per channel (K=%lld)", kConvTaps, (long long)K);
-  SR_REQUIRE(sizes_ok({P.B, tokens + kConvTaps, P.D}) && sizes_ok({P.B * tokens, P.ld_x}), "tensor sizes overflow int64");
+  SR_REQUIRE(sizes_ok({P.B, padded(tokens, kConvTaps), P.D}) && sizes_ok({P.B * tokens, P.ld_x}), "tensor sizes overflow int64");
   SR_REQUIRE(is_dtype(P.dtype) && is_dtype(P.w_dtype), "dtype unsupported");
   SR_REQUIRE(P.ld_x >= P.D, "ld_x (%lld) must be >= D (%lld)", (long long)P.ld_x, (long long)P.D);
   SR_REQUIRE(P.x || P.B * tokens * P.D == 0, "x is NULL");
@@ -165,7 +168,7 @@ int64_t conv_state_bytes(const ConvRequest& P) { return P.B * (P.K - 1) * P.D * 
 
 sr_status check_norm(int64_t M, int64_t D, sr_dtype dtype, sr_dtype r_dtype, const void* w, sr_dtype w_dtype, float eps) {
   SR_REQUIRE(M >= 0 && D >= 1, "M (%lld) must be non-negative and D (%lld) positive", (long long)M, (long long)D);
-  SR_REQUIRE(sizes_ok({M, D + kI8Align}), "tensor sizes overflow int64");
+  SR_REQUIRE(sizes_ok({M, padded(D, kI8Align)}), "tensor sizes overflow int64");
   if (D > kNormWidth)
     return fail(SR_ERR_UNSUPPORTED, "rows of at most %lld elements (D=%lld)", (long long)kNormWidth, (long long)D);
   SR_REQUIRE(is_dtype(dtype) && is_dtype(r_dtype) && is_dtype(w_dtype), "dtype unsupported");
@@ -382,7 +385,7 @@ sr_status causal_conv_forward(int64_t B, int64_t T, int64_t D, int64_t K, const 
 }
 
 size_t causal_conv_backward_workspace_size(int64_t B, int64_t T, int64_t D, int64_t K, sr_dtype x_dtype) {
-  if (K < 1 || K > kConvTaps || !is_dtype(x_dtype) || !sizes_ok({B, T < 0 ? -1 : T + kConvTaps, D, kConvTaps + 1})) return 0;
+  if (K < 1 || K > kConvTaps || !is_dtype(x_dtype) || !sizes_ok({B, T < 0 ? -1 : padded(T, kConvTaps), D, kConvTaps + 1})) return 0;
   return align_up(size_t(B * conv_plan(B, T, D, x_dtype, true).runs) * size_t(K + 1) * size_t(D) * 4, kAlign);
 }
 
