@@ -321,7 +321,7 @@ sr_status selective_scan_backward(int64_t B, int64_t T, int64_t D, int64_t N, in
   if (st == SR_OK) st = check_grid((B * T * G * 2 * selective_padded(N) + 255) / 256, 256);
   if (st == SR_OK) st = check_grid(((N + 2) * D + 63) / 64, 1024);
   if (st != SR_OK) return st;
-  if (D == 0) return SR_OK;
+  if (D == 0 && (B * T == 0 || (!dB && !dC))) return SR_OK;
   place_workspace(P, L, workspace);
   return launch_selective_backward(P);
 }

@@ -530,7 +530,7 @@ __global__ __launch_bounds__(256) void reduce_tokens_kernel(const SelectiveReque
     for (int k = 0; k < P.tiles_per_group; ++k) sum += src[k * rows * per];
   }
   T* out = static_cast<T*>(w ? P.dC : P.dB);
-  out[(r * P.G + g) * P.N + n] = from_f32<T>(sum);
+  if (out != nullptr) out[(r * P.G + g) * P.N + n] = from_f32<T>(sum);  // (may be null without channels)
 }
 
 // dA, dskip and dbias from the parts of each sequence and chunk.
@@ -544,6 +544,11 @@ __global__ __launch_bounds__(1024) void reduce_channels_kernel(const SelectiveRe
     else if (n == P.N + 1 && P.dbias)
       P.dbias[d] = sum;
   });
+}
+
+sr_status launched(const char* what) {
+  const hipError_t err = hipGetLastError();
+  return err == hipSuccess ? SR_OK : fail(SR_ERR_HIP, "%s: %s", what, hipGetErrorString(err));
 }
 
 template <typename T>
@@ -565,9 +570,19 @@ void launch_all(const SelectiveRequest& P) {
     either(backward_kernel<T, 8, 2, 2, true>, backward_kernel<T, 8, 2, 2, false>, 8);
   else
     either(backward_kernel<T, 8, 2, 4, true>, backward_kernel<T, 8, 2, 4, false>, 8);
+}
+sr_status launch_reduce_tokens(const SelectiveRequest& P) {
   const int padded = int(selective_padded(P.N));
   const int64_t n = P.B * P.T * P.G * 2 * padded;
-  if (n > 0) hipLaunchKernelGGL(reduce_tokens_kernel<T>, dim3(uint32_t((n + 255) / 256)), dim3(256), 0, P.stream, P, padded);
+  if (n == 0) return SR_OK;
+  auto run = [&](auto* kernel) {
+    hipLaunchKernelGGL(kernel, dim3(uint32_t((n + 255) / 256)), dim3(256), 0, P.stream, P, padded);
+  };
+  if (P.dtype == SR_BF16)
+    run(reduce_tokens_kernel<uint16_t>);
+  else
+    run(reduce_tokens_kernel<float>);
+  return launched("selective scan gradient sums over channels");
 }
 template <typename T, int W, int NS>
 void launch_ends(const SelectiveRequest& P) {
@@ -592,14 +607,10 @@ void launch_ends(const SelectiveRequest& P) {
     launch_ends<T, 8, 8>(P);
 }
 
-sr_status launched(const char* what) {
-  const hipError_t err = hipGetLastError();
-  return err == hipSuccess ? SR_OK : fail(SR_ERR_HIP, "%s: %s", what, hipGetErrorString(err));
-}
-
 }  // namespace
 
 sr_status launch_selective_backward(const SelectiveRequest& P) {
+  if (P.D == 0) return launch_reduce_tokens(P);  // zeros: sums of no channels
   sr_status st = P.B > 0 ? launch_selective_states(P) : SR_OK;
   if (st != SR_OK) return st;
   if (P.B > 0 && P.chunks > 1) {
@@ -622,6 +633,7 @@ sr_status launch_selective_backward(const SelectiveRequest& P) {
     else
       launch_all<float>(P);
     st = launched("selective scan backward");
+    if (st == SR_OK) st = launch_reduce_tokens(P);
     if (st != SR_OK) return st;
   }
   const int64_t n = int64_t(P.N + 2) * P.D;
