@@ -464,7 +464,8 @@ sr_status adamw_step_each(int64_t n_tensors, const sr_adamw_tensor* tensors, voi
  *               (b*T + t) * ld: halves of one projection's output are rows of it.
  *   outputs     contiguous.  They must not overlap inputs or each other
  *               (SR_ERR_INVALID_ARGUMENT).
- * Repeated calls give identical bits.  No call allocates, waits for the GPU or
+ * Repeated calls of equal sizes give identical bits (a sequence alone may be cut
+ * otherwise than in a batch, and differ by roundings).  No call allocates, waits for the GPU or
  * keeps anything; all can be captured into a graph.  Sizes whose launches would
  * take 2^32 work-items or more are SR_ERR_UNSUPPORTED.
  *
@@ -482,11 +483,13 @@ sr_status adamw_step_each(int64_t n_tensors, const sr_adamw_tensor* tensors, voi
  *   h0, h_last    [B,D,N] fp32 state in front of and behind the tokens; NULL: zeros,
  *                 and not wanted.
  *   y             [B,T,D] in x_dtype.
- * States, steps and gates are fp32; y is rounded once.  N at most 64, rows of several
- * tokens at most 2^25 elements apart (else SR_ERR_UNSUPPORTED).  Few channels and long sequences are cut into chunks of
- * tokens whose decay is the exponential of their summed steps; a state that left the
- * fp32 range stays non-finite, but may become NaN where one token after the other would
- * give an infinity.
+ * States, steps and gates are fp32; y is rounded once.  N at most 64, rows of
+ * several tokens at most 2^25 elements apart (else SR_ERR_UNSUPPORTED).  Few channels
+ * and long sequences are cut into chunks of tokens whose decay is the exponential of
+ * their summed steps; a state that left the fp32 range stays non-finite, but may
+ * become NaN where one token after the other would give an infinity.  The gradients
+ * that an infinite input or state goes into may be NaN where the formula gives an infinity;
+ * other channels', sequences' and groups' stay as they are.
  *
  * selective_scan_backward: for dL/dy = dy and dL/dh_last = dh_last (or NULL), the
  * gradients of u, delta, z, Bm and Cm in x_dtype (dB and dC summed over the

@@ -4,7 +4,7 @@
 //
 // with the last K - 1 inputs as the state that a following call takes in front of
 // its tokens.  Bound by the bytes of x and y: 8 x 4096 x 2048 in bf16 takes 46 us, 5.8
-// TB/s; its single-token form, 256 x 2048, 4.0 us, launch included.  A thread owns 16 bytes of
+// TB/s; its single-token form, 256 x 2048, 4.1 us (the call 5.1, bound by the host).  A thread owns 16 bytes of
 // channels and a run of tokens, keeps the window of its taps in registers and reads
 // every input once but for the K - 1 in front of its run; the next tokens' loads
 // are on the way while the present ones are computed.  Where D is no multiple
@@ -173,7 +173,8 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvRequest P) {
 // and the gradient of the state behind the sequence added to the inputs it is made of.
 // A run goes over its tokens and the K - 1 behind it (whose dc it computes too), so
 // dx needs no second pass (8 x 2048 x 1024 in bf16 27 us, 3.7 TB/s: one wave per
-// SIMD, its vector unit active for two thirds of the time); a run's sums for dw and dbias go out per run and are added
+// SIMD, its vector unit active for two thirds of the time; shorter runs and two waves take as
+// long, and about 64 bytes per lane are on their way); a run's sums for dw and dbias go out per run and are added
 // up by column_sums.
 template <typename T, int K, int V>
 __global__ __launch_bounds__(256) void conv_backward_kernel(const ConvRequest P) {
@@ -353,7 +354,7 @@ void by_type(sr_dtype dtype, bool whole, F f) {
 }
 
 // A thread's channels: 16 bytes, in the backward pass (whose filter, windows and sums
-// are all in registers) four: 8 x 2048 x 1024 in bf16 30.2 us, with eight of them 34.4.
+// are all in registers) four: the call of 8 x 2048 x 1024 in bf16 31.3 us, with eight of them 33.6.
 int64_t vector_of(sr_dtype dtype, bool backward) { return dtype == SR_BF16 && !backward ? 8 : 4; }
 
 sr_status launched(const char* what) {

@@ -148,11 +148,6 @@ __device__ __forceinline__ void store_at(T* base, uint32_t offset, const float (
   }
 }
 
-// A weight of either type.
-__device__ __forceinline__ float weight_at(const void* w, sr_dtype dtype, int64_t i) {
-  return dtype == SR_BF16 ? to_f32(static_cast<const uint16_t*>(w)[i]) : static_cast<const float*>(w)[i];
-}
-
 // A rate of the selective scan, and the factor of a step in its power of two: never minus
 // infinity, so that the steps of zero behind a sequence's end leave the state for any rate.
 __device__ __forceinline__ float bounded(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }
@@ -166,16 +161,17 @@ __device__ __forceinline__ float decayed(float x, float h, float e) {
 }
 __device__ __forceinline__ float half_rate2(float a) { return bounded(a * (0.5f * kLog2e)); }
 
-// log(1 + e^x) to a few ulps for any x: max(x, 0) + log1p(e), e = e^-|x|.  With u the
-// rounded 1 + e, log1p(e) = log(u) + (e - (u - 1)) / u; u's rounding error e - (u - 1) is
-// exact, and what its division by u changes is far below the sum's last place.
+// log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x|.  With u the rounded 1 + e, log1p(e) = log(u) +
+// (e - (u - 1)) / u; u's rounding error e - (u - 1) is exact, and what its division by u
+// changes is far below the sum's last place.  The exponent |x| log2 e is rounded (the constant
+// too), so the result is off by up to (2 |x| + 8) 2^-24 of it.
 __device__ __forceinline__ float softplus_f(float x) {
   const float e = __builtin_amdgcn_exp2f(-fabsf(x) * kLog2e);
   const float u = 1.0f + e;
   return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.0f));  // (a NaN is in e)
 }
 
-// 1 / (1 + e^-x), to a few ulps.
+// 1 / (1 + e^-x), off by up to (2 |x| + 6) 2^-24 of it by the rounded exponent.
 __device__ __forceinline__ float logistic_f(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * kLog2e));
 }

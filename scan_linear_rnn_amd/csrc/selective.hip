@@ -22,12 +22,13 @@
 // thread per state then carries the states over the chunks (carry_kernel); and the
 // full pass starts each chunk from its own state.
 //
-// 8 x 4096 x 2048, 16 states, gated, bf16: 360 us (1.5 TB/s, 3.0e12 states a second).  Bound by what
-// a SIMD issues: about 430 instructions per wave and tile, 64 of them exponentials at two
-// slots, where the recurrence with the sum over states alone takes 400 slots of 4 cycles (a
-// probe of it 190 us).  Eight waves of two states take as long: what they hide, their LDS
-// reads cost.  1 x 65536 x 1024 in 96 chunks: 460 us
-// (under a tracer first pass 207, carry 17, outputs 296).
+// 8 x 4096 x 2048, 16 states, gated, bf16: 351 to 366 us (1.5 TB/s, 3.0e12 states a second).  A
+// workgroup per CU, one wave per SIMD: about 455 vector instructions per wave and tile, 64 of
+// them exponentials at two slots, which keep its unit active for 67% of the time (a probe of the
+// recurrence with the sum over states alone takes 190 us); the rest is waits that no other wave fills.
+// Eight waves of two states take as long, 353 us, and more where a CU has several workgroups:
+// 16 x 2048 x 2048 292 us with four waves, 358 with eight; 1 x 65536 x 1024 in 96 chunks 465 and 587
+// (four waves under a tracer: first pass 212, carry 17, outputs 298, whose vector units are 92% active).
 
 #include "layer_util.hpp"
 
@@ -43,8 +44,8 @@ enum Pass {
 // W waves of NS states per lane.
 //
 // While the waves go through tile k, each thread also prepares its part of tile
-// k + 1's steps, sums its part of tile k - 1's outputs and has tile k + 2's inputs on
-// their way: everything between two barriers is independent, one barrier per tile.  Tiles with
+// k + 1's steps, sums its part of tile k - 1's outputs and has the inputs of tiles k + 2 and
+// k + 3 on their way: everything between two barriers is independent, one barrier per tile.  Tiles with
 // four whole ones behind them go without a branch, as one block that the compiler can order.
 template <typename T, int W, int NS, int kPass, bool kWhole, bool kGated>
 __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void scan_kernel(const SelectiveRequest P) {
@@ -214,8 +215,8 @@ __global__ __launch_bounds__(W * 64, kPass != kOutputs && NS < 8 ? 3 : 2) void s
     }
   };
   // The sum of the steps (the first wave's), of whole tiles with what rounding lost of them:
-  // the steps one after another would drift with the number of tokens (8192 equal ones by
-  // 1258 x 2^-24), and the decay of many tokens is an exponential of this sum.
+  // the steps one after another would drift with the number of tokens (8192 equal ones by more than
+  // 1000 x 2^-24), and the decay of many tokens is an exponential of this sum.
   float total = 0.0f, lost = 0.0f;
   Inputs in[2];        // of the next tile and the one after it
   Raw<T, Q> u0{}, z0{}, u1{}, z1{};  // of the present tile and the one before it
@@ -539,6 +540,9 @@ SelectivePlan chunked(int64_t T, int64_t tiles_per_group, int64_t want) {
 // first pass computes three quarters of what the second does), else about 1536 workgroups
 // in all.  Measured, 4096 tokens in bf16, workgroups without chunks: us without chunks /
 // with them: 8: 353 / 37, 64: 354 / 131, 128: 349 / 242, 192: 351 / 344, 256: 356 / 455.
+// In all 256 / 512 / 1024 / 1536 / 2048 of them, us: 1 x 65536 x 1024 with 4 states 380 / 272 / 251 / 247 / 252,
+// 16 states 601 / 498 / 467 / 465 / 463, 64 states 1528 / 1498 / 1504 / 1527 / 1543; 4 x 4096 x 2048 with 4 states
+// 179 / 136 / 123 / 124 / 122, 16 states 306 / 256 / 239 / 241 / 236, 64 states 778 / 764 / 775 / 806 / 805.
 SelectivePlan selective_plan(int64_t B, int64_t T, int64_t D, int64_t G) {
   const int64_t tiles = (D / G + kLanes - 1) / kLanes, blocks = B * G * tiles;
   return chunked(T, tiles, blocks > 0 && blocks < 224 ? (1536 + blocks - 1) / blocks : 1);
@@ -546,8 +550,10 @@ SelectivePlan selective_plan(int64_t B, int64_t T, int64_t D, int64_t G) {
 
 // The backward pass has one workgroup per CU at a time, and its chunks cost a fifth more
 // (the pass that carries gradients backwards): the number of them that leaves the
-// fewest rounds over the 256 CUs for a chunk's work.  Measured as above, of 2048 tokens: 8: 703 /
-// 81, 64: 717 / 238, 128: 724 / 455, 192: 729 / 652, 256: 736 / 828.
+// fewest rounds over the 256 CUs for a chunk's work, where a round's start and end cost 0.15 of it and a
+// chunk's carry 0.002.  Measured in us, 2048 tokens, 16 states, workgroups without chunks: without / the rule's / the
+// best of 2 to 32 chunks: 8: 698 / 86 / 83, 64: 710 / 250 / 242, 128: 721 / 459 / 441, 192: 730 / 657 / 642,
+// 256: 736 / 736 / 832, 320: 1372 / 1058 / 1032, 640: 2049 / 2118 / 1993; 8192 tokens, 16 workgroups 2750 / 250 / 246.
 SelectivePlan selective_backward_plan(int64_t B, int64_t T, int64_t D, int64_t G) {
   const int64_t tiles = (D / G + kLanes - 1) / kLanes, blocks = B * G * tiles;
   int64_t best = 1;

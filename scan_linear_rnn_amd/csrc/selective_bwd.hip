@@ -24,10 +24,11 @@
 // instructions per value, where separate sums would take six.  They go out per 64
 // channels and reduce_tokens_kernel adds those up, always in the same order.
 //
-// 8 x 2048 x 1024, 16 states, gated, bf16: 452 us, of them marks 63, the gradients in front of
-// the chunks 63, two carries 10, this kernel 310 to 350, sums 17.  Its vector units are busy
-// for 65% of its time: a workgroup takes 123 KB of LDS, so a SIMD has two waves to choose from.
-// 32 states 988 us; 64 states, whose groups do not fit the registers, 3.1 ms.
+// 8 x 2048 x 1024, 16 states, gated, bf16: 456 us, of them marks 65, the gradients in front of
+// the chunks 63, two carries 10, this kernel 340 to 354 (traced), sums 16.  Its vector units are busy
+// for 65% of its time: 123 KB of LDS per workgroup and 232 registers per lane, each of which by itself leaves a
+// SIMD two waves to choose from.  32 states 1.0 ms (27 registers spilled); 64 states, whose groups do not fit the
+// registers (165 to 196 spilled), 3.1 ms.
 
 #include "layer_util.hpp"
 
